@@ -75,8 +75,9 @@ uint64_t kvs_launch_count(void);
 
 /* Device-side error word shared by all kernels of the library on the current device
  * (0 = none; 1 = a bounded wait of a tensor-core kernel ran out, 3 = shared-memory
- * window misaligned, 4/5 = kvs_decode_step out of pages, 6 = kvs_value_refit met a
- * non-positive pivot).  Reading synchronises
+ * window misaligned, 4/5 = kvs_decode_step or kvs_append_paged out of pages, 6 =
+ * kvs_value_refit met a non-positive pivot, 8 = kvs_append_paged met a token start, length
+ * or page id out of range, 9 = kvs_attn_decode did).  Reading synchronises
  * `stream`; `clear` != 0 resets it to 0. */
 kvs_status kvs_device_error(int32_t* code_out, int32_t clear, void* stream);
 
@@ -431,6 +432,110 @@ kvs_status kvs_compact_paged_multi(const kvs_dims* dims, const kvs_bf16* k, cons
                                    int32_t capacity_pages, int32_t* block_table, int32_t max_pages,
                                    int32_t* seq_lens, int32_t* needed_pages, void* ws,
                                    size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * kvs_rope -- position rotation of queries and keys, at explicit positions (for a pruned
+ * cache a token's position is not its slot).  Pair i < rot_dim / 2 of the token at
+ * position p turns by p * inv_freq[i]:
+ *
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ *
+ * where (a, b) are dimensions (i, i + rot_dim / 2) with interleaved == 0 and
+ * (2 i, 2 i + 1) otherwise; dimensions from rot_dim on are copied.  Whole turns are taken
+ * off without loss at any position, so the angle is good to 2^-22 radians (the fp32
+ * resolution of [-pi, pi]) for |pos * inv_freq| up to 2^27; the products are fp32, and each
+ * result is rounded to bf16 once.  Negated frequencies undo a rotation; since a rotation is orthogonal, the
+ * same call on the gradients of the outputs gives the gradients of the inputs.
+ *
+ *   pos        [N]             int32; any value
+ *   inv_freq   [rot_dim / 2]   double in HOST memory, radians per position, finite; read
+ *                              before the call returns (a captured graph keeps the values)
+ *   q, q_out   [L][H_q][N][d]  bf16; both NULL to leave queries out
+ *   k, k_out   [L][H_kv][N][d] bf16; both NULL to leave keys out
+ * An output is its input (rotation in place) or does not overlap it.  Requires rot_dim a
+ * multiple of 16 with 0 <= rot_dim <= d.
+ * ------------------------------------------------------------------------------- */
+kvs_status kvs_rope(const kvs_dims* dims, int32_t N, const int32_t* pos, int32_t rot_dim,
+                    const double* inv_freq, int32_t interleaved, const kvs_bf16* q,
+                    kvs_bf16* q_out, const kvs_bf16* k, kvs_bf16* k_out, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * kvs_append_paged -- append new tokens to the paged cache of kvs_compact_paged and
+ * kvs_decode_step, with the rotation of kvs_rope on the way: a chunk of a prompt, or one
+ * token per sequence, of a ragged batch of B sequences.  Tokens tok_start[b] ..
+ * tok_start[b + 1] - 1 of the batch's N belong to sequence b; for every row
+ * r = (l * H_kv + hk) * B + b, the j-th of them goes to slot seq_lens[r] + j:
+ *
+ *   page block_table[r][slot / page_size], row slot % page_size
+ *   k rotated at pos[t], v as it is; q_out = q rotated at pos[t] (if q is given)
+ *
+ * A row that fills its last page takes new pages from next_page[0] on, in row order (page
+ * ids are deterministic); the unused rows of its last new page are zero-filled.
+ * All or nothing: if the pool (error word 4) or a row's block table (5) is too small, or a
+ * token start, length or page id is out of range (8), no page, table entry or query is
+ * written, the outputs seq_lens_out and next_page_out equal their inputs, and the device
+ * error word is set (kvs_device_error).  With seq_lens_out and next_page_out apart from
+ * their inputs a caller keeps the state before the call, and takes the append back by
+ * going on from it (a rejected draft).
+ *
+ *   tok_start [B + 1] int32, 0 = tok_start[0] <= ... <= tok_start[B] <= N; tokens from
+ *             tok_start[B] on are padding: nothing is read or written for them.  NULL
+ *             with N == B: one token per sequence
+ *   pos       [N] int32 (NULL with rot_dim == 0);  rot_dim, inv_freq, interleaved as kvs_rope
+ *   q, q_out  [L][H_q][N][d] bf16, or both NULL; q_out == q rotates in place
+ *   k, v      [L][H_kv][N][d] bf16
+ *   k_pages, v_pages [capacity_pages][page_size][d] bf16 state
+ *   next_page, next_page_out [1] int32; may be the same (kvs_compact_paged leaves the
+ *             count of used pages in needed_pages)
+ *   block_table [L][H_kv][B][max_pages] int32 state
+ *   seq_lens, seq_lens_out [L][H_kv][B] int32; may be the same
+ *   ws        scratch of kvs_append_paged_workspace_size() bytes; calls that may overlap
+ *             on the GPU need their own
+ * No two rows may own the same page.
+ * ------------------------------------------------------------------------------- */
+size_t kvs_append_paged_workspace_size(const kvs_dims* dims, int32_t B);
+kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const int32_t* tok_start,
+                            const int32_t* pos, int32_t rot_dim, const double* inv_freq,
+                            int32_t interleaved, const kvs_bf16* q, kvs_bf16* q_out,
+                            const kvs_bf16* k, const kvs_bf16* v, int32_t page_size,
+                            kvs_bf16* k_pages, kvs_bf16* v_pages, int32_t capacity_pages,
+                            const int32_t* next_page, int32_t* next_page_out,
+                            int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                            int32_t* seq_lens_out, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * kvs_attn_decode -- attention of one new token per sequence over its pruned cache
+ * [KVzap limitation 3: head lengths differ; KVzap 3.2, Eq. 2: the output of head hq].
+ * The keys of row r = (l * H_kv + hk) * B + b are its seq_lens[r] paged tokens and, with
+ * w > 0, the tokens in the ring that kvs_decode_step keeps: slots 0 .. min(pos[b], w) - 1,
+ * where pos[b] counts the tokens that have entered the ring (as kvs_decode_step leaves it
+ * with advance_pos != 0).
+ *
+ *   lse[l][hq][b] = ln sum_i exp(q[l][hq][b] . k_i / sqrt(d))
+ *   o[l][hq][b]   = sum_i exp(q[l][hq][b] . k_i / sqrt(d) - lse) v_i
+ *
+ * over the keys of KV head hq / g.  A row without keys gives o = 0 and lse = -inf.  The
+ * softmax weights are rounded to bf16 before they multiply V on the tensor cores; sums
+ * and statistics are fp32 and o is stored as bf16.  Results do not depend on the order in
+ * which blocks run.
+ * A length outside [0, max_pages * page_size] is taken as the nearest bound and keys of a
+ * page id outside [0, capacity_pages) are left out; either sets the device error word (9).
+ *
+ *   q, o   [L][H_q][B][d] bf16;  lse [L][H_q][B] fp32 output, or NULL
+ *   k_pages, v_pages [capacity_pages][page_size][d] bf16
+ *   block_table [L][H_kv][B][max_pages] int32;  seq_lens [L][H_kv][B] int32
+ *   pos    [B] int32;  ring_k, ring_v [L][H_kv][B][w][d] bf16   (NULL with w == 0)
+ *   ws     scratch of kvs_attn_decode_workspace_size() bytes; calls that may overlap on
+ *          the GPU need their own
+ * With B = 1 the pages are those of kvs_compact_paged as they are.
+ * ------------------------------------------------------------------------------- */
+size_t kvs_attn_decode_workspace_size(const kvs_dims* dims, int32_t B);
+kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, int32_t page_size,
+                           const kvs_bf16* k_pages, const kvs_bf16* v_pages,
+                           int32_t capacity_pages, const int32_t* block_table, int32_t max_pages,
+                           const int32_t* seq_lens, int32_t w, const int32_t* pos,
+                           const kvs_bf16* ring_k, const kvs_bf16* ring_v, kvs_bf16* o,
+                           float* lse, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -84,6 +84,13 @@ _SIGS = {
     "kvs_compact_multi_workspace_size": ([_D, _I, _I], _S),
     "kvs_compact_paged_multi": ([_D, _P, _P, _I, _I, _P, _I, _P, _P, _I, _P, _I, _P, _P, _P, _S,
                                  _P], ctypes.c_int),
+    "kvs_rope": ([_D, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P], ctypes.c_int),
+    "kvs_append_paged_workspace_size": ([_D, _I], _S),
+    "kvs_append_paged": ([_D, _I, _I, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, _P, _P, _I, _P, _P,
+                          _P, _I, _P, _P, _P, _S, _P], ctypes.c_int),
+    "kvs_attn_decode_workspace_size": ([_D, _I], _S),
+    "kvs_attn_decode": ([_D, _I, _P, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _S,
+                         _P], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -259,3 +266,82 @@ def kvs_compact_paged(dm, k, v, T, mask, page_size, k_pages, v_pages, capacity_p
                                   _ptr(k_pages), _ptr(v_pages), capacity_pages, _ptr(block_table),
                                   max_pages, _ptr(seq_lens), _ptr(needed_pages), _ptr(ws),
                                   ws_bytes, _stream(stream)))
+
+
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
+def _arg(t, dtype, n, name):
+    """Device pointer of a tensor argument that must hold at least n elements of dtype."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or t.numel() < n:
+        raise ValueError(f"kvs: {name} must hold at least {n} elements of {dtype}, got "
+                         f"{t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
+def _freqs(inv_freq, rot_dim):
+    """Host pointer of the rotation frequencies (a float64 CPU tensor, or any sequence of
+    floats) and the object that keeps them alive during the call."""
+    if inv_freq is None or rot_dim <= 0:
+        return None, None
+    f = inv_freq
+    if not (isinstance(f, torch.Tensor) and f.dtype is torch.float64 and not f.is_cuda
+            and f.is_contiguous()):
+        f = torch.tensor([float(x) for x in inv_freq], dtype=torch.float64)
+    if f.numel() < rot_dim // 2:
+        raise ValueError(f"kvs: inv_freq holds {f.numel()} frequencies, {rot_dim // 2} needed")
+    return f.data_ptr(), f
+
+
+def kvs_rope(dm, N, pos, rot_dim, inv_freq, interleaved, q, q_out, k, k_out, stream=None):
+    """inv_freq: rot_dim / 2 radians per position in host memory (a float64 CPU tensor or a
+    sequence of floats)."""
+    fp, _keep = _freqs(inv_freq, rot_dim)
+    nq, nk = dm.L * dm.H_q * N * dm.d, dm.L * dm.H_kv * N * dm.d
+    _check(_lib.kvs_rope(_d(dm), N, _arg(pos, _I32, N, "pos"), rot_dim, fp, 1 if interleaved else 0,
+                         _arg(q, _BF16, nq, "q"), _arg(q_out, _BF16, nq, "q_out"),
+                         _arg(k, _BF16, nk, "k"), _arg(k_out, _BF16, nk, "k_out"),
+                         _stream(stream)))
+
+
+def kvs_append_paged_workspace_size(dm, B) -> int:
+    return _lib.kvs_append_paged_workspace_size(_d(dm), B)
+
+
+def kvs_append_paged(dm, B, N, tok_start, pos, rot_dim, inv_freq, interleaved, q, q_out, k, v,
+                     page_size, k_pages, v_pages, capacity_pages, next_page, next_page_out,
+                     block_table, max_pages, seq_lens, seq_lens_out, ws, ws_bytes, stream=None):
+    """inv_freq as for kvs_rope; tok_start None: one token per sequence (N == B)."""
+    fp, _keep = _freqs(inv_freq, rot_dim)
+    rows, d = dm.L * dm.H_kv * B, dm.d
+    nq, nk, pool = dm.L * dm.H_q * N * d, dm.L * dm.H_kv * N * d, capacity_pages * page_size * d
+    _check(_lib.kvs_append_paged(
+        _d(dm), B, N, _arg(tok_start, _I32, B + 1, "tok_start"), _arg(pos, _I32, N, "pos"), rot_dim,
+        fp, 1 if interleaved else 0, _arg(q, _BF16, nq, "q"), _arg(q_out, _BF16, nq, "q_out"),
+        _arg(k, _BF16, nk, "k"), _arg(v, _BF16, nk, "v"), page_size,
+        _arg(k_pages, _BF16, pool, "k_pages"), _arg(v_pages, _BF16, pool, "v_pages"),
+        capacity_pages, _arg(next_page, _I32, 1, "next_page"),
+        _arg(next_page_out, _I32, 1, "next_page_out"),
+        _arg(block_table, _I32, rows * max_pages, "block_table"), max_pages,
+        _arg(seq_lens, _I32, rows, "seq_lens"), _arg(seq_lens_out, _I32, rows, "seq_lens_out"),
+        _arg(ws, torch.uint8, ws_bytes, "ws"), ws_bytes, _stream(stream)))
+
+
+def kvs_attn_decode_workspace_size(dm, B) -> int:
+    return _lib.kvs_attn_decode_workspace_size(_d(dm), B)
+
+
+def kvs_attn_decode(dm, B, q, page_size, k_pages, v_pages, capacity_pages, block_table, max_pages,
+                    seq_lens, w, pos, ring_k, ring_v, o, lse, ws, ws_bytes, stream=None):
+    rows, d = dm.L * dm.H_kv * B, dm.d
+    nq, pool = dm.L * dm.H_q * B, capacity_pages * page_size * d
+    _check(_lib.kvs_attn_decode(
+        _d(dm), B, _arg(q, _BF16, nq * d, "q"), page_size, _arg(k_pages, _BF16, pool, "k_pages"),
+        _arg(v_pages, _BF16, pool, "v_pages"), capacity_pages,
+        _arg(block_table, _I32, rows * max_pages, "block_table"), max_pages,
+        _arg(seq_lens, _I32, rows, "seq_lens"), w, _arg(pos, _I32, B if w else 0, "pos"),
+        _arg(ring_k, _BF16, rows * w * d, "ring_k"), _arg(ring_v, _BF16, rows * w * d, "ring_v"),
+        _arg(o, _BF16, nq * d, "o"), _arg(lse, _F32, nq, "lse"),
+        _arg(ws, torch.uint8, ws_bytes, "ws"), ws_bytes, _stream(stream)))

@@ -1,5 +1,6 @@
 // C ABI of the kvs library: argument validation, then launches on the caller's stream.
 // Declarations and argument documentation: include/kvs.h.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -8,11 +9,13 @@
 
 #include "../../include/kvs.h"
 #include "attn.cuh"
+#include "attn_decode.cuh"
 #include "compact.cuh"
 #include "decode.cuh"
 #include "gram.cuh"
 #include "mlp.cuh"
 #include "prune.cuh"
+#include "rope.cuh"
 #include "surrogate.cuh"
 #include "vnorm.cuh"
 
@@ -94,13 +97,16 @@ uint64_t kvs_launch_count(void) { return kvs::g_launches.load(std::memory_order_
 
 kvs_status kvs_device_error(int32_t* code_out, int32_t clear, void* stream) {
   REQUIRE(code_out, KVS_ERR_ARG, "kvs_device_error: code_out is NULL");
-  int codes[6] = {0, 0, 0, 0, 0, 0};
+  int codes[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   cudaError_t e = kvs::attn_device_error(&codes[0], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::mlp_device_error(&codes[1], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::fwd_device_error(&codes[2], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::decode_device_error(&codes[3], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::gram_device_error(&codes[4], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::chol_device_error(&codes[5], clear != 0, as_stream(stream));
+  if (e == cudaSuccess) e = kvs::rope_device_error(&codes[6], clear != 0, as_stream(stream));
+  if (e == cudaSuccess)
+    e = kvs::attn_decode_device_error(&codes[7], clear != 0, as_stream(stream));
   if (e != cudaSuccess) return cuda_status(e, "kvs_device_error");
   *code_out = 0;
   for (int c : codes)
@@ -630,6 +636,186 @@ kvs_status kvs_prune_topk_multi(const kvs_dims* dims, const float* score, int32_
   return cuda_status(kvs::launch_topk(score, dims->L * dims->H_kv, T, n_budgets, kb, w, masks,
                                       keeps, as_stream(stream)),
                      "kvs_prune_topk_multi");
+}
+
+namespace {
+bool overlap(const void* a, const void* b, size_t a_bytes, size_t b_bytes) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+// The rotation of one call: sizes, and each pair's radians per position as turns in a
+// 64-bit binary fraction.  The magnitude is converted and the sign applied to the integer,
+// so that negated frequencies give exactly the opposite angles.
+kvs_status check_rope(const char* fn, const kvs_dims* dm, int32_t N, const int32_t* pos,
+                      int32_t rot_dim, const double* inv_freq, int32_t interleaved,
+                      kvs::RopeArgs* r) {
+  REQUIRE(N >= 0, KVS_ERR_ARG, "%s: N = %d is negative", fn, N);
+  REQUIRE(rot_dim >= 0 && rot_dim <= dm->d && rot_dim % 16 == 0, KVS_ERR_UNSUPPORTED,
+          "%s: rot_dim = %d must be a multiple of 16 in 0 .. d = %d", fn, rot_dim, dm->d);
+  r->L = dm->L; r->Hq = dm->H_q; r->Hkv = dm->H_kv; r->d = dm->d; r->N = N;
+  r->rot_dim = rot_dim; r->interleaved = interleaved != 0; r->pos = pos;
+  if (rot_dim == 0) return KVS_OK;
+  REQUIRE(inv_freq, KVS_ERR_ARG, "%s: inv_freq is NULL", fn);
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    REQUIRE(isfinite(inv_freq[i]), KVS_ERR_ARG, "%s: inv_freq[%d] is not finite", fn, i);
+    const double turns = fabs(inv_freq[i]) * 0.15915494309189533577;  // 1 / (2 pi)
+    const uint64_t f = (uint64_t)((turns - floor(turns)) * 0x1p64);
+    r->freq[i] = inv_freq[i] < 0 ? 0 - f : f;
+  }
+  if (N > 0) {
+    REQUIRE(pos, KVS_ERR_ARG, "%s: pos is NULL", fn);
+    REQUIRE(aligned16(pos), KVS_ERR_ALIGN, "%s: pos is not 16-byte aligned", fn);
+  }
+  return KVS_OK;
+}
+
+// A tensor and its rotated form: both or neither, in place or apart.
+kvs_status check_rotated(const char* fn, const char* name, const kvs_bf16* x, const kvs_bf16* out,
+                         size_t bytes) {
+  REQUIRE((x == nullptr) == (out == nullptr), KVS_ERR_ARG, "%s: one of %s and %s_out is NULL", fn,
+          name, name);
+  REQUIRE(aligned16(x) && aligned16(out), KVS_ERR_ALIGN,
+          "%s: %s or %s_out is not 16-byte aligned", fn, name, name);
+  REQUIRE(!x || x == out || !overlap(x, out, bytes, bytes), KVS_ERR_ARG,
+          "%s: %s_out overlaps %s without being it", fn, name, name);
+  return KVS_OK;
+}
+}  // namespace
+
+kvs_status kvs_rope(const kvs_dims* dims, int32_t N, const int32_t* pos, int32_t rot_dim,
+                    const double* inv_freq, int32_t interleaved, const kvs_bf16* q,
+                    kvs_bf16* q_out, const kvs_bf16* k, kvs_bf16* k_out, void* stream) {
+  kvs_status st = check_dims(dims, __func__);
+  if (st) return st;
+  kvs::RopeArgs r;
+  st = check_rope(__func__, dims, N, pos, rot_dim, inv_freq, interleaved, &r);
+  if (st) return st;
+  if (N == 0) return ok();
+  const size_t row = (size_t)dims->L * N * dims->d * sizeof(kvs_bf16);
+  st = check_rotated(__func__, "q", q, q_out, row * dims->H_q);
+  if (st) return st;
+  st = check_rotated(__func__, "k", k, k_out, row * dims->H_kv);
+  if (st) return st;
+  REQUIRE((int64_t)dims->L * ((int64_t)dims->H_q + dims->H_kv) < INT32_MAX, KVS_ERR_UNSUPPORTED,
+          "kvs_rope: too many heads");
+  r.q = q; r.q_out = q_out; r.k = k; r.k_out = k_out;
+  return cuda_status(kvs::launch_rope(r, as_stream(stream)), "kvs_rope");
+}
+
+size_t kvs_append_paged_workspace_size(const kvs_dims* dims, int32_t B) {
+  if (!dims || dims->L <= 0 || dims->H_kv <= 0 || B <= 0 ||
+      (int64_t)dims->L * dims->H_kv >= INT32_MAX / 32 / B + 1)
+    return 0;
+  return kvs::append_workspace_bytes(dims->L * dims->H_kv * B);
+}
+
+kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const int32_t* tok_start,
+                            const int32_t* pos, int32_t rot_dim, const double* inv_freq,
+                            int32_t interleaved, const kvs_bf16* q, kvs_bf16* q_out,
+                            const kvs_bf16* k, const kvs_bf16* v, int32_t page_size,
+                            kvs_bf16* k_pages, kvs_bf16* v_pages, int32_t capacity_pages,
+                            const int32_t* next_page, int32_t* next_page_out,
+                            int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                            int32_t* seq_lens_out, void* ws, size_t ws_bytes, void* stream) {
+  kvs_status st = check_dims(dims, __func__);
+  if (st) return st;
+  kvs::RopeArgs r;
+  st = check_rope(__func__, dims, N, pos, rot_dim, inv_freq, interleaved, &r);
+  if (st) return st;
+  REQUIRE(B >= 0 && capacity_pages >= 0, KVS_ERR_ARG, "kvs_append_paged: negative size");
+  REQUIRE(page_size >= 1 && page_size <= 4096, KVS_ERR_UNSUPPORTED,
+          "kvs_append_paged: page_size = %d (1..4096)", page_size);
+  REQUIRE(max_pages >= 1, KVS_ERR_SHAPE, "kvs_append_paged: max_pages = %d must be >= 1",
+          max_pages);
+  REQUIRE(tok_start || N == B, KVS_ERR_ARG,
+          "kvs_append_paged: without tok_start N = %d must be B = %d", N, B);
+  REQUIRE((int64_t)dims->L * dims->H_kv < INT32_MAX / 32 / (B > 0 ? B : 1), KVS_ERR_UNSUPPORTED,
+          "kvs_append_paged: too many rows");
+  REQUIRE((int64_t)dims->L * ((int64_t)dims->H_q + 2 * dims->H_kv) < INT32_MAX,
+          KVS_ERR_UNSUPPORTED, "kvs_append_paged: too many heads");
+  if (B == 0) return ok();
+  REQUIRE_OPT_PTR(tok_start);
+  const size_t row = (size_t)dims->L * N * dims->d * sizeof(kvs_bf16);
+  const size_t rows = (size_t)dims->L * dims->H_kv * B;
+  if (N > 0) {
+    st = check_rotated(__func__, "q", q, q_out, row * dims->H_q);
+    if (st) return st;
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(v);
+  }
+  if (capacity_pages > 0) {
+    REQUIRE_PTR(k_pages);
+    REQUIRE_PTR(v_pages);
+  }
+  REQUIRE_PTR(next_page);
+  REQUIRE_PTR(next_page_out);
+  REQUIRE_PTR(block_table);
+  REQUIRE_PTR(seq_lens);
+  REQUIRE_PTR(seq_lens_out);
+  REQUIRE(seq_lens == seq_lens_out || !overlap(seq_lens, seq_lens_out, rows * 4, rows * 4),
+          KVS_ERR_ARG, "kvs_append_paged: seq_lens_out overlaps seq_lens without being it");
+  REQUIRE_PTR(ws);
+  const size_t need = kvs_append_paged_workspace_size(dims, B);
+  REQUIRE(ws_bytes >= need, KVS_ERR_CAPACITY,
+          "kvs_append_paged: workspace of %zu bytes, %zu needed", ws_bytes, need);
+  r.q = N > 0 ? q : nullptr; r.q_out = q_out; r.k = k;
+  kvs::AppendArgs a;
+  a.v = v; a.B = B; a.page_size = page_size; a.max_pages = max_pages; a.capacity = capacity_pages;
+  a.tok_start = tok_start; a.k_pages = k_pages; a.v_pages = v_pages;
+  a.next_page = next_page; a.next_page_out = next_page_out; a.block_table = block_table;
+  a.seq_lens = seq_lens; a.seq_lens_out = seq_lens_out; a.plan = static_cast<int*>(ws);
+  return cuda_status(kvs::launch_append(r, a, as_stream(stream)), "kvs_append_paged");
+}
+
+size_t kvs_attn_decode_workspace_size(const kvs_dims* dims, int32_t B) {
+  if (!dims || dims->L <= 0 || dims->H_kv <= 0 || dims->H_q <= 0 || dims->H_q % dims->H_kv ||
+      B <= 0 || (int64_t)dims->L * dims->H_q >= INT32_MAX / 32 / B + 1)
+    return 0;
+  return kvs::attn_decode_workspace_bytes(dims->L * dims->H_kv * B, dims->H_q / dims->H_kv,
+                                          dims->d);
+}
+
+kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, int32_t page_size,
+                           const kvs_bf16* k_pages, const kvs_bf16* v_pages,
+                           int32_t capacity_pages, const int32_t* block_table, int32_t max_pages,
+                           const int32_t* seq_lens, int32_t w, const int32_t* pos,
+                           const kvs_bf16* ring_k, const kvs_bf16* ring_v, kvs_bf16* o,
+                           float* lse, void* ws, size_t ws_bytes, void* stream) {
+  kvs_status st = check_dims(dims, __func__);
+  if (st) return st;
+  REQUIRE(B >= 0 && w >= 0 && capacity_pages >= 0, KVS_ERR_ARG, "kvs_attn_decode: negative size");
+  REQUIRE(page_size >= 1 && page_size <= 4096, KVS_ERR_UNSUPPORTED,
+          "kvs_attn_decode: page_size = %d (1..4096)", page_size);
+  REQUIRE(max_pages >= 1, KVS_ERR_SHAPE, "kvs_attn_decode: max_pages = %d must be >= 1",
+          max_pages);
+  REQUIRE((int64_t)dims->L * dims->H_q < INT32_MAX / 32 / (B > 0 ? B : 1), KVS_ERR_UNSUPPORTED,
+          "kvs_attn_decode: too many rows");
+  if (B == 0) return ok();
+  REQUIRE_PTR(q);
+  REQUIRE_PTR(block_table);
+  REQUIRE_PTR(seq_lens);
+  if (capacity_pages > 0) {
+    REQUIRE_PTR(k_pages);
+    REQUIRE_PTR(v_pages);
+  }
+  if (w > 0) {
+    REQUIRE_PTR(pos);
+    REQUIRE_PTR(ring_k);
+    REQUIRE_PTR(ring_v);
+  }
+  REQUIRE_PTR(o);
+  REQUIRE_OPT_PTR(lse);
+  REQUIRE_PTR(ws);
+  const size_t need = kvs_attn_decode_workspace_size(dims, B);
+  REQUIRE(ws_bytes >= need, KVS_ERR_CAPACITY,
+          "kvs_attn_decode: workspace of %zu bytes, %zu needed", ws_bytes, need);
+  kvs::AttnDecodeArgs a;
+  a.q = q; a.L = dims->L; a.Hq = dims->H_q; a.Hkv = dims->H_kv; a.B = B; a.d = dims->d;
+  a.page_size = page_size; a.capacity = capacity_pages; a.max_pages = max_pages; a.w = w;
+  a.k_pages = k_pages; a.v_pages = v_pages; a.block_table = block_table; a.seq_lens = seq_lens;
+  a.pos = pos; a.ring_k = ring_k; a.ring_v = ring_v; a.o = o; a.lse = lse; a.ws = ws;
+  return cuda_status(kvs::launch_attn_decode(a, as_stream(stream)), "kvs_attn_decode");
 }
 
 }  // extern "C"

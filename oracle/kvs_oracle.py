@@ -427,6 +427,86 @@ def decode_prune(score, tau, w):
     return kept, window
 
 
+def rope(x, pos, inv_freq, rot_dim, interleaved):
+    """Position rotation: pair i of a token at position p turns by the angle p inv_freq[i].
+    Pairs are dimensions (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved;
+    dimensions from rot_dim on pass through.  x [..., N, d], pos [N]."""
+    x = np.asarray(x, dtype=np.float64)
+    out = x.copy()
+    for i in range(rot_dim // 2):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot_dim // 2)
+        t = np.asarray(pos, dtype=np.float64) * inv_freq[i]
+        out[..., a] = x[..., a] * np.cos(t) - x[..., b] * np.sin(t)
+        out[..., b] = x[..., b] * np.cos(t) + x[..., a] * np.sin(t)
+    return out
+
+
+def append_paged(k_new, v_new, tok_start, page_size, k_pages, v_pages, next_page, block_table,
+                 seq_lens):
+    """Append a ragged batch to a paged cache (reading: the storage of compact_paged and of
+    the decode step, whose new pages come from a shared counter; rows take theirs in row
+    order).  Sequence b's tokens tok_start[b] .. tok_start[b+1]-1 go behind the seq_lens
+    tokens of each of its rows; unused rows of a row's last new page become zero.
+    k_new, v_new [L][H_kv][N][d] (rotated already); block_table [L][H_kv][B][max_pages];
+    seq_lens [L][H_kv][B].  Returns new arrays, or the string "pool" or "table" when the
+    pool or a row's table is too small: then nothing is appended."""
+    L, H, B, max_pages = block_table.shape
+    kp, vp, bt, sl = k_pages.copy(), v_pages.copy(), block_table.copy(), seq_lens.copy()
+    nxt, full = int(next_page), None
+    for l in range(L):
+        for h in range(H):
+            for b in range(B):
+                for t in range(tok_start[b], tok_start[b + 1]):
+                    n = sl[l, h, b]
+                    if n // page_size >= max_pages:
+                        return "table"
+                    if n % page_size == 0:
+                        if nxt >= len(kp):
+                            full = "pool"
+                        else:
+                            kp[nxt], vp[nxt] = 0, 0
+                        bt[l, h, b, n // page_size] = nxt
+                        nxt += 1
+                    if full is None:
+                        kp[bt[l, h, b, n // page_size], n % page_size] = k_new[l, h, t]
+                        vp[bt[l, h, b, n // page_size], n % page_size] = v_new[l, h, t]
+                    sl[l, h, b] = n + 1
+    return full if full else (kp, vp, nxt, bt, sl)
+
+
+def attn_decode(q, k_pages, v_pages, page_size, block_table, seq_lens, ring_k=None, ring_v=None,
+                pos=None):
+    """Attention of one new token per sequence over its rows' paged tokens and window ring
+    [KVzap 3.2, Eq. 2: o = sum_i a_i v_i; limitation 3: head lengths differ].  q
+    [L][H_q][B][d]; the ring [L][H_kv][B][w][d] holds min(pos[b], w) tokens from slot 0 on.
+    Returns (o, lse, spread): spread = sum_i a_i |v_i| bounds what rounded weights can do.
+    A row without keys gives zeros and -inf."""
+    L, H_q, B, d = q.shape
+    H_kv = block_table.shape[1]
+    g = _group(H_q, H_kv)
+    o, lse_, spread = np.zeros(q.shape), np.full(q.shape[:3], -np.inf), np.zeros(q.shape)
+    for l in range(L):
+        for hq in range(H_q):
+            for b in range(B):
+                hk, n = hq // g, int(seq_lens[l, hq // g, b])
+                at = [(block_table[l, hk, b, i // page_size], i % page_size) for i in range(n)]
+                K = [k_pages[p, r] for p, r in at]
+                V = [v_pages[p, r] for p, r in at]
+                if ring_k is not None:
+                    held = min(int(pos[b]), ring_k.shape[3])
+                    K += list(ring_k[l, hk, b, :held])
+                    V += list(ring_v[l, hk, b, :held])
+                if not K:
+                    continue
+                K, V = np.array(K), np.array(V)
+                x = attention_logits(q[l, hq, b][None], K)[0]
+                m = x.max()
+                z = m + np.log(np.exp(x - m).sum())
+                a = np.exp(x - z)
+                o[l, hq, b], lse_[l, hq, b], spread[l, hq, b] = a @ V, z, a @ np.abs(V)
+    return o, lse_, spread
+
+
 # ----------------------------------------------------------------------------- formulas
 
 def kv_cache_bytes(L, T, H_kv, d, bytes_per_elem):
