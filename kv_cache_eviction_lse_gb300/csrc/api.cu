@@ -791,6 +791,8 @@ kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, i
           max_pages);
   REQUIRE((int64_t)dims->L * dims->H_q < INT32_MAX / 32 / (B > 0 ? B : 1), KVS_ERR_UNSUPPORTED,
           "kvs_attn_decode: too many rows");
+  REQUIRE((int64_t)max_pages * page_size + w < INT32_MAX - 65536, KVS_ERR_UNSUPPORTED,
+          "kvs_attn_decode: max_pages * page_size + w of a row above 2^31");
   if (B == 0) return ok();
   REQUIRE_PTR(q);
   REQUIRE_PTR(block_table);

@@ -113,6 +113,7 @@ def test_attend_refusals(C):
     assert attend(C, ps=0) == C.KVS_ERR_UNSUPPORTED
     assert attend(C, ps=5000) == C.KVS_ERR_UNSUPPORTED
     assert attend(C, mp=0) == C.KVS_ERR_SHAPE
+    assert attend(C, mp=1 << 27, ps=16) == C.KVS_ERR_UNSUPPORTED
     assert attend(C, C.dims(40000, 40000, 40000, 128)) == C.KVS_ERR_UNSUPPORTED
     need = C.kvs_attn_decode_workspace_size(C.dims(1, 4, 2, 128), 2)
     assert need > 0 and attend(C, wsb=need - 1) == C.KVS_ERR_CAPACITY
