@@ -36,6 +36,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;        // keys
 constexpr int kMaxBlocks = 160;  // of the persistent grid; sizes the workspace
+constexpr int kJoinThreads = 256;
 constexpr int kMaxChunks = 256;  // of rows, in the scan of their tiles
 constexpr float kSlack = 8.f;    // log2 of how far a weight may exceed the reference
 
@@ -43,8 +44,10 @@ __host__ __device__ constexpr int stages(int d) { return d == 128 ? 3 : 6; }
 __host__ __device__ constexpr int stage_bytes(int d) { return 2 * kTile * d * 2; }
 constexpr int kRingBytes = stages(128) * stage_bytes(128);  // per warp, either d
 
-// A partial result of a row segment: O^T fragments [d / 16 * 4 * NG][32 lanes], then the
-// reference and the sum of each of the 8 NG heads.
+constexpr int kCachedRows = 1024;  // whose lengths a block keeps in shared memory
+
+// A partial result of a row segment: O^T fragments [d / 16 * 4 * NG][32 lanes], then (in
+// the workspace) the reference and the sum of each of the 8 NG heads.
 __host__ __device__ constexpr int frags(int d, int ng) { return d / 16 * 4 * ng; }
 __host__ __device__ constexpr int part_floats(int d, int ng) { return frags(d, ng) * 32 + 16 * ng; }
 
@@ -83,13 +86,8 @@ __device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0
 // The keys of a row: paged tokens, and with the ring's.
 struct Keys { int paged, all; };
 
-__device__ __forceinline__ Keys row_keys(const AttnDecodeArgs& a, int row, bool report) {
-  const int room = a.max_pages * a.page_size;
-  int n = a.seq_lens[row];
-  if (n < 0 || n > room) {
-    if (report) atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
-    n = n < 0 ? 0 : room;
-  }
+__device__ __forceinline__ Keys row_keys(const AttnDecodeArgs& a, int row) {
+  const int n = max(0, min(a.seq_lens[row], a.max_pages * a.page_size));
   const int held = a.w > 0 ? max(0, min(a.pos[row % a.B], a.w)) : 0;
   return {n, n + held};
 }
@@ -98,35 +96,37 @@ __device__ __forceinline__ Keys row_keys(const AttnDecodeArgs& a, int row, bool 
 struct Cursor {
   int row, group, tile;   // group: which 8 NG of the row's query heads
   Keys keys;              // of the row
-  int base, paged, all;   // lane i: the lengths of row base + i
+  int base;
+  Keys mine;              // lane i: of row base + i
 
-  __device__ __forceinline__ void fetch(const AttnDecodeArgs& a, int rows, int lane) {
-    Keys k = {0, 0};
-    if (base + lane < rows) k = row_keys(a, base + lane, false);
-    paged = k.paged;
-    all = k.all;
+  __device__ __forceinline__ void fetch(const AttnDecodeArgs& a, int rows, const Keys* cached,
+                                        int lane) {
+    mine = {0, 0};
+    if (base + lane < rows)
+      mine = rows <= kCachedRows ? cached[base + lane] : row_keys(a, base + lane);
   }
   __device__ __forceinline__ void enter(int r) {
     row = r;
-    keys.paged = __shfl_sync(0xffffffffu, paged, r - base);
-    keys.all = __shfl_sync(0xffffffffu, all, r - base);
+    keys.paged = __shfl_sync(0xffffffffu, mine.paged, r - base);
+    keys.all = __shfl_sync(0xffffffffu, mine.all, r - base);
   }
   __device__ __forceinline__ bool at_row_end() const { return (tile + 1) * kTile >= keys.all; }
-  // the next tile; there is one
-  __device__ __forceinline__ void advance(const AttnDecodeArgs& a, int rows, int groups, int lane) {
-    if (!at_row_end()) { ++tile; return; }
+  // the next tile (there is one); true if it is another row's
+  __device__ __forceinline__ bool advance(const AttnDecodeArgs& a, int rows, int groups,
+                                          const Keys* cached, int lane) {
+    if (!at_row_end()) { ++tile; return false; }
     tile = 0;
-    if (++group < groups) return;
+    if (++group < groups) return true;
     group = 0;
     int from = row - base + 1;
     for (;;) {
-      const uint32_t some = __ballot_sync(0xffffffffu, all > 0) &
+      const uint32_t some = __ballot_sync(0xffffffffu, mine.all > 0) &
                             (from < 32 ? 0xffffffffu << from : 0u);
-      if (some) { enter(base + __ffs(some) - 1); return; }
+      if (some) { enter(base + __ffs(some) - 1); return true; }
       base += 32;
       from = 0;
-      if (base >= rows) return;  // not reached while tiles remain
-      fetch(a, rows, lane);
+      if (base >= rows) return true;  // not reached while tiles remain
+      fetch(a, rows, cached, lane);
     }
   }
 };
@@ -147,56 +147,82 @@ template <int D, int NG>
 __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
     const __grid_constant__ AttnDecodeArgs a, int rows, int groups, int ps_shift) {
   constexpr int S = stages(D), KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
-  static_assert(PF * 4 <= kRingBytes, "a partial fits the ring");
+  static_assert(NF * 32 * 4 <= kRingBytes, "a partial result fits the ring");
   extern __shared__ __align__(1024) uint8_t smem[];
+  Keys* cached = reinterpret_cast<Keys*>(smem + kWarps * kRingBytes);
   __shared__ long long prefix[kMaxChunks + 1];
+  __shared__ long long share_base, share_rem;  // tiles a warp; the first `rem` take one more
   __shared__ uint32_t live[kWarps][S];
-  // what each warp leaves behind: a row that began before its share (head) and one that
-  // goes on after it (tail); nullptr where there is none
-  __shared__ float *head_part[kWarps], *tail_part[kWarps];
-  __shared__ int head_vrow[kWarps], tail_vrow[kWarps], head_ends[kWarps];
+  // what each warp leaves behind: a row that began before its share (head, index w) and one
+  // that goes on after it (tail, index kWarps + w); the bit masks say where there is one
+  __shared__ const float* part[2 * kWarps];
+  __shared__ int vrow_of[2 * kWarps];
+  __shared__ float ref_s[2 * kWarps][NG * 8], sum_s[2 * kWarps][NG * 8];
+  __shared__ uint32_t heads_m, ends_m, tails_m;
   __shared__ long long head_first;  // the first tile of warp 0's first row
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.Hq / a.Hkv;
   asm volatile("griddepcontrol.launch_dependents;");
 
-  // --- tiles of all rows, by chunks of rows
+  // --- tiles of all rows, by chunks of rows; four chunks' loads at a time
   const int per = 32 * ((rows + 32 * kMaxChunks - 1) / (32 * kMaxChunks));
   const int chunks = (rows + per - 1) / per;
-  for (int c = warp; c < chunks; c += kWarps) {
-    const bool mine = c % gridDim.x == blockIdx.x;  // reports, and fills empty rows
-    long long sum = 0;
+  for (int c0 = warp; c0 < chunks; c0 += 4 * kWarps) {
+    long long sum[4] = {};
     for (int i = lane; i < per; i += 32) {
-      const int r = c * per + i;
-      const int n = r < rows ? row_keys(a, r, mine).all : -1;
-      sum += (max(n, 0) + kTile - 1) / kTile;
-      uint32_t empty = mine ? __ballot_sync(0xffffffffu, n == 0) : 0u;
-      for (; empty; empty &= empty - 1) {
-        const int er = c * per + (i - lane) + __ffs(empty) - 1;
-        for (int e = lane; e < g * (D / 8); e += 32)
-          reinterpret_cast<uint4*>(a.o + out_row(a, er, g, e / (D / 8)) * D)[e % (D / 8)] =
-              make_uint4(0, 0, 0, 0);
-        if (a.lse)
-          for (int h = lane; h < g; h += 32) a.lse[out_row(a, er, g, h)] = -INFINITY;
+      Keys k[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = (c0 + u * kWarps) * per + i;
+        k[u] = {0, -1};
+        if (c0 + u * kWarps < chunks && r < rows)
+          k[u] = row_keys(a, r);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = c0 + u * kWarps, r = c * per + i;
+        if (k[u].all < 0) k[u].all = 0;
+        else if (rows <= kCachedRows) cached[r] = k[u];
+        const uint32_t tiles = (k[u].all + kTile - 1) / kTile;
+        sum[u] += __reduce_add_sync(0xffffffffu, tiles & 0xffffu) +
+                  ((long long)__reduce_add_sync(0xffffffffu, tiles >> 16) << 16);
+        if (c >= chunks || c % gridDim.x != blockIdx.x) continue;
+        // the block that owns the chunk reports lengths out of range, and writes the outputs
+        // of rows without keys
+        if (r < rows) {
+          const int n = a.seq_lens[r];
+          if (n < 0 || n > a.max_pages * a.page_size)
+            atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
+        }
+        uint32_t empty = __ballot_sync(0xffffffffu, r < rows && k[u].all == 0);
+        for (; empty; empty &= empty - 1) {
+          const int er = r - lane + __ffs(empty) - 1;
+          for (int e = lane; e < g * (D / 8); e += 32)
+            reinterpret_cast<uint4*>(a.o + out_row(a, er, g, e / (D / 8)) * D)[e % (D / 8)] =
+                make_uint4(0, 0, 0, 0);
+          if (a.lse)
+            for (int h = lane; h < g; h += 32) a.lse[out_row(a, er, g, h)] = -INFINITY;
+        }
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) prefix[c + 1] = sum * groups;
+    for (int u = 0; u < 4; ++u)
+      if (lane == 0 && c0 + u * kWarps < chunks) prefix[c0 + u * kWarps + 1] = sum[u] * groups;
   }
-  if (lane == 0) {
-    head_part[warp] = tail_part[warp] = nullptr;
-    head_ends[warp] = 0;
+  if (tid == 0) {
+    heads_m = ends_m = tails_m = 0;
+    prefix[0] = 0;
   }
   __syncthreads();
   if (warp == 0) {
-    constexpr int kEach = kMaxChunks / 32;
-    long long v[kEach], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int c = lane * kEach + i;
-      sum += c < chunks ? prefix[c + 1] : 0;
-      v[i] = sum;
+    const int each = (chunks + 31) / 32;
+    long long sum = 0;
+    for (int i = 0; i < each; ++i) {
+      const int c = lane * each + i;
+      if (c < chunks) {
+        sum += prefix[c + 1];
+        prefix[c + 1] = sum;
+      }
     }
     long long before = sum;
 #pragma unroll
@@ -204,14 +230,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
       const long long y = __shfl_up_sync(0xffffffffu, before, o);
       if (lane >= o) before += y;
     }
+    const long long all = __shfl_sync(0xffffffffu, before, 31);
     before -= sum;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int c = lane * kEach + i;
-      if (c < chunks) prefix[c + 1] = before + v[i];
+    for (int i = 0; i < each; ++i)
+      if (lane * each + i < chunks) prefix[lane * each + i + 1] += before;
+    if (lane == 0) {
+      const int most = gridDim.x * kWarps;
+      if (all <= most) {
+        share_base = 1;
+        share_rem = 0;
+      } else {
+        share_base = all < INT32_MAX ? (uint32_t)all / (uint32_t)most : all / most;
+        share_rem = all - share_base * most;
+      }
     }
-    if (lane == 0) prefix[0] = 0;
   }
   __syncthreads();
   const long long total = prefix[chunks];
@@ -224,21 +256,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
   }
 
   if (gw < warps) {
-    const long long t0 = gw * total / warps, t1 = (gw + 1) * total / warps;
-    // --- the row of the share's first tile
-    int lo = 0, hi = chunks;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= t0) lo = mid; else hi = mid;
-    }
+    const long long t0 = gw * share_base + min((long long)gw, share_rem);
+    const long long t1 = t0 + share_base + (gw < share_rem);
+    // --- the row of the share's first tile: its chunk (the last that begins at or before
+    // it), then the row among the chunk's
+    const int each = (chunks + 31) / 32;
+    int chunk = each * (__popc(__ballot_sync(0xffffffffu, lane * each < chunks &&
+                                             prefix[min(lane * each, chunks)] <= t0)) - 1);
+    chunk += __popc(__ballot_sync(0xffffffffu, lane < each && chunk + lane < chunks &&
+                                  prefix[min(chunk + lane, chunks)] <= t0)) - 1;
     Cursor ld;
-    ld.base = lo * per;
-    long long at = prefix[lo];
-    int off;  // tiles from the row's first (of all its groups) to t0
-    long long row_first;
+    ld.base = chunk * per;
+    long long at = prefix[chunk];
     for (;;) {
-      ld.fetch(a, rows, lane);
-      const long long mine = (long long)((ld.all + kTile - 1) / kTile) * groups;
+      ld.fetch(a, rows, cached, lane);
+      const long long mine = (long long)((ld.mine.all + kTile - 1) / kTile) * groups;
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -249,53 +281,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
       if (past) {
         const int l = __ffs(past) - 1;
         ld.enter(ld.base + l);
-        row_first = at + __shfl_sync(0xffffffffu, incl - mine, l);
-        off = (int)(t0 - row_first);
+        at += __shfl_sync(0xffffffffu, incl - mine, l);
         break;
       }
       at += __shfl_sync(0xffffffffu, incl, 31);
       ld.base += 32;
     }
-    const int nt = (ld.keys.all + kTile - 1) / kTile;
-    ld.group = off / nt;
+    const int nt = (ld.keys.all + kTile - 1) / kTile, off = (int)(t0 - at);
+    ld.group = groups == 1 ? 0 : off / nt;
     ld.tile = off - ld.group * nt;
     Cursor cur = ld;
-    const long long first_vrow_tile = row_first + (long long)ld.group * nt;
+    if (tid == 0) head_first = t0 - ld.tile;
 
     uint8_t* ring = smem + warp * kRingBytes;
     const uint32_t ring_u = smem_u32(ring);
     long long to_load = t1 - t0;
 
-    // --- producer: lane i < 16 finds where key i of the tile lies
-    int page = -1, inside = 0;   // paged key: its page id and row in the page
-    int slot = -1;               // ring key: its slot
-    auto look_up = [&]() {
-      page = slot = -1;
-      const int key = ld.tile * kTile + lane;
-      if (lane < kTile && key < ld.keys.all) {
-        if (key < ld.keys.paged) {
-          const int idx = ps_shift >= 0 ? key >> ps_shift : key / a.page_size;
-          inside = key - idx * a.page_size;
-          page = a.block_table[(size_t)ld.row * a.max_pages + idx];
-          if (page < 0 || page >= a.capacity) {
-            atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
-            page = -1;
-          }
-        } else {
-          slot = key - ld.keys.paged;
-        }
+    // --- producer: lane i (and i + 16) finds where key i of the tile lies.  The lanes keep
+    // 32 entries of the row's block table from page tbase on; a load of more of them is
+    // used an iteration later
+    int tbase = 0, entry = -1;
+    int idx = 0, inside = 0;  // the key's page in the row, and its row in the page
+    auto look_up = [&](bool new_row) {
+      const int first = ld.tile * kTile, key = first + (lane & 15);
+      idx = ps_shift >= 0 ? key >> ps_shift : key / a.page_size;
+      inside = key - idx * a.page_size;
+      const int paged = min(kTile, ld.keys.paged - first);  // keys of the tile in pages
+      if (paged <= 0) return;
+      const int p0 = __shfl_sync(0xffffffffu, idx, 0);
+      const int p1 = __shfl_sync(0xffffffffu, idx, paged - 1);
+      if (new_row || p1 > tbase + 31) {
+        tbase = p0;
+        const int ahead = ld.keys.paged - 1 - first + (first - p0 * a.page_size);
+        const int have = ps_shift >= 0 ? ahead >> ps_shift : ahead / a.page_size;
+        entry = lane <= have ? a.block_table[(size_t)ld.row * a.max_pages + p0 + lane] : -1;
       }
     };
     auto issue = [&](int stage) {
       if (to_load > 0) {
-        // row index in the pool, or (negative) in the ring
-        long long at_row = -1;
-        bool in_ring = false;
-        if (page >= 0) {
-          at_row = (long long)page * a.page_size + inside;
-        } else if (slot >= 0) {
-          at_row = (long long)ld.row * a.w + slot;
-          in_ring = true;
+        const int key0 = ld.tile * kTile + (lane & 15);
+        const int page = __shfl_sync(0xffffffffu, entry, (idx - tbase) & 31);
+        long long at_row = -1;  // row in the pool, or in the ring
+        const bool in_ring = key0 >= ld.keys.paged;
+        if (key0 < ld.keys.all) {
+          if (in_ring)
+            at_row = (long long)ld.row * a.w + (key0 - ld.keys.paged);
+          else if ((uint32_t)page < (uint32_t)a.capacity)
+            at_row = (long long)page * a.page_size + inside;
+          else
+            atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
         }
         const uint32_t here = __ballot_sync(0xffffffffu, at_row >= 0);
         const uint32_t ringed = __ballot_sync(0xffffffffu, in_ring);
@@ -316,14 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
           cp_async16(to + kTile * D * 2, v + e, ok ? 16 : 0);
         }
         --to_load;
-        if (to_load > 0) {
-          ld.advance(a, rows, groups, lane);
-          look_up();
-        }
+        if (to_load > 0) look_up(ld.advance(a, rows, groups, cached, lane));
       }
       cp_async_commit();
     };
-    look_up();
+    look_up(true);
     for (int s = 0; s < S - 1; ++s) issue(s);
 
     // --- consumer
@@ -347,7 +378,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
     };
     start();
     bool began_here = cur.tile == 0;
-    if (tid == 0) head_first = first_vrow_tile;
     int stage = 0;
     for (long long t = t0; t < t1; ++t) {
       cp_async_wait<S - 2>();
@@ -459,40 +489,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
         } else {
           // a part: into the warp's own ring once nothing is in flight there any more, or
           // (the share goes on) into the workspace
-          float* part = warp_part(a.ws, gw, PF);
+          float* to = warp_part(a.ws, gw, PF);
           if (last) {
             cp_async_wait<0>();
             __syncwarp();
-            part = reinterpret_cast<float*>(ring);
+            to = reinterpret_cast<float*>(ring);
           }
+          const int id = began_here ? kWarps + warp : warp;
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) part[((j * KS + s) * 4 + i) * 32 + lane] = o[j][s][i];
+              for (int i = 0; i < 4; ++i) to[((j * KS + s) * 4 + i) * 32 + lane] = o[j][s][i];
             if (lane < 4) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                part[NF * 32 + j * 8 + lane * 2 + i] = m[j][i];
-                part[NF * 32 + (NG + j) * 8 + lane * 2 + i] = l[j][i];
+                ref_s[id][j * 8 + lane * 2 + i] = m[j][i];
+                sum_s[id][j * 8 + lane * 2 + i] = l[j][i];
               }
             }
           }
           if (lane == 0) {
-            const int vrow = cur.row * groups + cur.group;
-            if (began_here) {
-              tail_part[warp] = part;
-              tail_vrow[warp] = vrow;
-            } else {
-              head_part[warp] = part;
-              head_vrow[warp] = vrow;
-              head_ends[warp] = row_end;
-            }
+            part[id] = to;
+            vrow_of[id] = cur.row * groups + cur.group;
+            atomicOr(began_here ? &tails_m : &heads_m, 1u << warp);
+            if (!began_here && row_end) atomicOr(&ends_m, 1u << warp);
           }
         }
         if (!last) {
-          cur.advance(a, rows, groups, lane);
+          cur.advance(a, rows, groups, cached, lane);
           start();
           began_here = true;
         }
@@ -505,49 +531,70 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
   __syncthreads();
 
   // --- join the rows that cross shares inside the block: a chain of parts comes from the
-  // block before (from = -1) or begins with a warp's tail, and goes on through the next
-  // warps' heads until one ends the row
-  if (tid == 0) ends[blockIdx.x] = {-1, 0};
-  for (int from = -1; from < kWarps; ++from) {
-    const bool before = from < 0;
-    if (before ? head_part[0] == nullptr : tail_part[from] == nullptr) continue;
-    const float* part[kWarps + 1];
-    int n = 0;
-    int ended = 0;
-    if (!before) part[n++] = tail_part[from];
-    for (int e = from + 1; e < kWarps && head_part[e] != nullptr && !ended; ++e) {
-      part[n++] = head_part[e];
-      ended = head_ends[e];
+  // block before, or begins with a warp's tail, and goes on through the next warps' heads
+  // until one ends the row.  Bit 0 of `starts` is the chain from before, bit w + 1 the one
+  // that begins with warp w's tail
+  const uint32_t heads = heads_m, stop = ends_m | ~heads;
+  const uint32_t starts = (heads & 1) | (tails_m << 1);
+  if (tid == 0) {
+    Ends e = {-1, 0};
+    if ((heads & 1) && (ends_m & (stop & -stop))) {
+      // the warp of the row's first tile
+      const long long wide = share_rem * (share_base + 1);
+      const long long fw = head_first < wide ? head_first / (share_base + 1)
+                                             : share_rem + (head_first - wide) / share_base;
+      e = {vrow_of[0], (int)(fw / kWarps)};
     }
-    const int vrow = before ? head_vrow[0] : tail_vrow[from];
-    const int row = vrow / groups, group = vrow - row * groups;
-    // complete here, or a part for the second kernel
-    float* out = ended && !before ? nullptr : block_part(a.ws, blockIdx.x, before ? 0 : 1, PF);
-    for (int i = tid; i < NF * 32; i += kThreads) {
-      const int reg = i >> 5, ln = i & 31;
-      const int j = reg / (KS * 4), s = reg / 4 % KS, c = reg & 3;
-      const int h = j * 8 + (ln & 3) * 2 + (c & 1);
-      const int dim = s * 16 + (ln >> 2) + (c >> 1) * 8;
-      float top = -INFINITY, sum = 0.f, acc = 0.f;
-      for (int p = 0; p < n; ++p) top = fmaxf(top, part[p][NF * 32 + h]);
-      for (int p = 0; p < n; ++p) {
-        const float f = fast_exp2(part[p][NF * 32 + h] - finite_ref(top));
-        acc += part[p][i] * f;
-        sum += part[p][NF * 32 + NG * 8 + h] * f;
+    ends[blockIdx.x] = e;
+  }
+  // a warp takes eight fragments of a chain at a time, all their loads in flight
+  constexpr int kUnits = NF / 8;
+  const int work = __popc(starts) * kUnits;
+  for (int u = warp; u < work; u += kWarps) {
+    uint32_t left = starts;
+    for (int c = u / kUnits; c > 0; --c) left &= left - 1;
+    const int from = __ffs(left) - 1;  // first head of the chain
+    const int len = __ffs(stop >> from) - 1;  // heads that go on (a stop is found: 8 bits of 32)
+    const bool ended = (ends_m >> (from + len)) & 1, before = from == 0;
+    const int n = len + (ended ? 1 : 0), tail = kWarps + from - 1;  // heads from .. from + n - 1
+    // heads of the lane's columns: even and odd fragments
+    const int f0 = u % kUnits * 8, h0 = f0 / (KS * 4) * 8 + (lane & 3) * 2;
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {}, acc[8] = {};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (!before) top[i] = ref_s[tail][h0 + i];
+      for (int p = from; p < from + n; ++p) top[i] = fmaxf(top[i], ref_s[p][h0 + i]);
+    }
+    auto add = [&](int id) {
+      float w[2];
+      const float* x = part[id] + f0 * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i] = fast_exp2(ref_s[id][h0 + i] - finite_ref(top[i]));
+        sum[i] += sum_s[id][h0 + i] * w[i];
       }
-      if (out) {
-        out[i] = acc;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += x[i * 32] * w[i & 1];
+    };
+    if (!before) add(tail);
+#pragma unroll 2
+    for (int p = from; p < from + n; ++p) add(p);
+    const int vrow = vrow_of[before ? 0 : tail], row = vrow / groups;
+    const int head = (vrow - row * groups) * NG * 8 + h0;
+    float* out = block_part(a.ws, blockIdx.x, before ? 0 : 1, PF);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int dim = (f0 + i) / 4 % KS * 16 + (lane >> 2) + (i >> 1 & 1) * 8;
+      if (ended && !before) {
+        if (head + (i & 1) < g)
+          store_out<D>(a, out_row(a, row, g, head + (i & 1)), dim, acc[i], top[i & 1], sum[i & 1]);
+      } else {  // a part for the second kernel
+        out[(f0 + i) * 32 + lane] = acc[i];
         if (dim == 0) {
-          out[NF * 32 + h] = top;
-          out[NF * 32 + NG * 8 + h] = sum;
+          out[NF * 32 + h0 + (i & 1)] = top[i & 1];
+          out[NF * 32 + NG * 8 + h0 + (i & 1)] = sum[i & 1];
         }
-      } else if (group * NG * 8 + h < g) {
-        store_out<D>(a, out_row(a, row, g, group * NG * 8 + h), dim, acc, top, sum);
       }
-    }
-    if (before && ended && tid == 0) {
-      const long long fw = ((head_first + 1) * warps - 1) / total;  // warp of the row's first tile
-      ends[blockIdx.x] = {vrow, (int)(fw / kWarps)};
     }
   }
 }
@@ -555,53 +602,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
 // Rows that cross blocks: block x joins the row that ends in block x of the first kernel,
 // from the tail of its first block and the heads of those after.
 template <int D, int NG>
-__global__ void __launch_bounds__(256) attn_decode_join_kernel(
+__global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
     const __grid_constant__ AttnDecodeArgs a, int groups) {
   constexpr int KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
-  __shared__ float weight[kMaxBlocks][NG * 8];
-  __shared__ float top_s[NG * 8], sum_s[NG * 8];
+  constexpr int kFirst = 8;  // parts whose loads start before the weights are known
+  __shared__ float ref_s[kMaxBlocks][NG * 8], sum_s[kMaxBlocks][NG * 8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Ends end = static_cast<const Ends*>(a.ws)[blockIdx.x];
   if (end.vrow < 0) return;
-  const int g = a.Hq / a.Hkv, n = blockIdx.x - end.first + 1;
-  const int row = end.vrow / groups, group = end.vrow - row * groups;
+  const int n = blockIdx.x - end.first + 1;
   auto part = [&](int p) { return block_part(a.ws, end.first + p, p == 0 ? 1 : 0, PF); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int h = warp; h < NG * 8; h += 8) {
-    float top = -INFINITY, sum = 0.f;
-    for (int p = lane; p < n; p += 32) top = fmaxf(top, part(p)[NF * 32 + h]);
+  const int f = blockIdx.y * kJoinThreads + threadIdx.x;
+  const int j = f / (32 * KS * 4), s = f / 128 % KS, c = f / 32 % 4, ln = f & 31;
+  const int h = j * 8 + (ln & 3) * 2 + (c & 1), dim = s * 16 + (ln >> 2) + (c >> 1) * 8;
+  float x[kFirst];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int p = lane; p < n; p += 32) {
-      const float f = fast_exp2(part(p)[NF * 32 + h] - finite_ref(top));
-      weight[p][h] = f;
-      sum += part(p)[NF * 32 + NG * 8 + h] * f;
-    }
-    sum = warp_sum(sum);
-    if (lane == 0) {
-      top_s[h] = top;
-      sum_s[h] = sum;
-    }
+  for (int p = 0; p < kFirst; ++p) x[p] = p < n ? part(p)[f] : 0.f;
+  for (int i = threadIdx.x; i < n * NG * 8; i += kJoinThreads) {
+    const float* q = part(i / (NG * 8)) + NF * 32 + i % (NG * 8);
+    ref_s[i / (NG * 8)][i % (NG * 8)] = q[0];
+    sum_s[i / (NG * 8)][i % (NG * 8)] = q[NG * 8];
   }
   __syncthreads();
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < NF * 32; i += gridDim.y * 256) {
-    const int reg = i >> 5, ln = i & 31;
-    const int j = reg / (KS * 4), s = reg / 4 % KS, c = reg & 3;
-    const int h = j * 8 + (ln & 3) * 2 + (c & 1);
-    float acc = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) acc += part(p)[i] * weight[p][h];
-    const float sum = sum_s[h];
-    if (group * NG * 8 + h < g) {
-      const int dim = s * 16 + (ln >> 2) + (c >> 1) * 8;
-      store_out<D>(a, out_row(a, row, g, group * NG * 8 + h), dim, acc, top_s[h], sum);
+  float top = -INFINITY;
+  for (int p = 0; p < n; ++p) top = fmaxf(top, ref_s[p][h]);
+  const float base = finite_ref(top);
+  float acc = 0.f, sum = 0.f;
+#pragma unroll
+  for (int p = 0; p < kFirst; ++p) {
+    if (p < n) {
+      const float w = fast_exp2(ref_s[p][h] - base);
+      acc += x[p] * w;
+      sum += sum_s[p][h] * w;
     }
   }
+#pragma unroll 8
+  for (int p = kFirst; p < n; ++p) {
+    const float w = fast_exp2(ref_s[p][h] - base);
+    acc += part(p)[f] * w;
+    sum += sum_s[p][h] * w;
+  }
+  const int g = a.Hq / a.Hkv, row = end.vrow / groups;
+  const int head = (end.vrow - row * groups) * NG * 8 + h;
+  if (head < g) store_out<D>(a, out_row(a, row, g, head), dim, acc, top, sum);
 }
 
 template <int D, int NG>
 cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s) {
-  constexpr int smem = kWarps * kRingBytes;
+  constexpr int smem = kWarps * kRingBytes + kCachedRows * (int)sizeof(Keys);
   static int nsm[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -629,8 +677,8 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
   if (e != cudaSuccess) return e;
   // the join's blocks come up while the first kernel runs and wait for its results
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, 2 * NG);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(blocks, frags(D, NG) * 32 / kJoinThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
