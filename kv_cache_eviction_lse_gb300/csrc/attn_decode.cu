@@ -86,10 +86,13 @@ __device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0
 // The keys of a row: paged tokens, and with the ring's.
 struct Keys { int paged, all; };
 
-__device__ __forceinline__ Keys row_keys(const AttnDecodeArgs& a, int row) {
-  const int n = max(0, min(a.seq_lens[row], a.max_pages * a.page_size));
-  const int held = a.w > 0 ? max(0, min(a.pos[row % a.B], a.w)) : 0;
-  return {n, n + held};
+__device__ __forceinline__ Keys keys_of(const AttnDecodeArgs& a, int len, int pos) {
+  const int n = max(0, min(len, a.max_pages * a.page_size));
+  return {n, n + max(0, min(pos, a.w))};
+}
+
+__device__ __forceinline__ int ring_pos(const AttnDecodeArgs& a, int row) {
+  return a.w > 0 ? a.pos[row % a.B] : 0;
 }
 
 // A place in the stream of tiles.  The lanes hold the lengths of the 32 rows from `base` on.
@@ -103,7 +106,8 @@ struct Cursor {
                                         int lane) {
     mine = {0, 0};
     if (base + lane < rows)
-      mine = rows <= kCachedRows ? cached[base + lane] : row_keys(a, base + lane);
+      mine = rows <= kCachedRows ? cached[base + lane]
+                                   : keys_of(a, a.seq_lens[base + lane], ring_pos(a, base + lane));
   }
   __device__ __forceinline__ void enter(int r) {
     row = r;
@@ -170,31 +174,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
   for (int c0 = warp; c0 < chunks; c0 += 4 * kWarps) {
     long long sum[4] = {};
     for (int i = lane; i < per; i += 32) {
-      Keys k[4];
+      int len[4], pos[4];  // all loads before the first use, from rows that are there
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int r = (c0 + u * kWarps) * per + i;
-        k[u] = {0, -1};
-        if (c0 + u * kWarps < chunks && r < rows)
-          k[u] = row_keys(a, r);
+        const int r = min((c0 + u * kWarps) * per + i, rows - 1);
+        len[u] = a.seq_lens[r];
+        pos[u] = ring_pos(a, r);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int c = c0 + u * kWarps, r = c * per + i;
-        if (k[u].all < 0) k[u].all = 0;
-        else if (rows <= kCachedRows) cached[r] = k[u];
-        const uint32_t tiles = (k[u].all + kTile - 1) / kTile;
+        const bool in = c < chunks && r < rows;
+        const Keys k = in ? keys_of(a, len[u], pos[u]) : Keys{0, 0};
+        if (in && rows <= kCachedRows) cached[r] = k;
+        const uint32_t tiles = (k.all + kTile - 1) / kTile;
         sum[u] += __reduce_add_sync(0xffffffffu, tiles & 0xffffu) +
                   ((long long)__reduce_add_sync(0xffffffffu, tiles >> 16) << 16);
         if (c >= chunks || c % gridDim.x != blockIdx.x) continue;
         // the block that owns the chunk reports lengths out of range, and writes the outputs
         // of rows without keys
-        if (r < rows) {
-          const int n = a.seq_lens[r];
-          if (n < 0 || n > a.max_pages * a.page_size)
-            atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
-        }
-        uint32_t empty = __ballot_sync(0xffffffffu, r < rows && k[u].all == 0);
+        if (in && (len[u] < 0 || len[u] > a.max_pages * a.page_size))
+          atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
+        uint32_t empty = __ballot_sync(0xffffffffu, in && k.all == 0);
         for (; empty; empty &= empty - 1) {
           const int er = r - lane + __ffs(empty) - 1;
           for (int e = lane; e < g * (D / 8); e += 32)
