@@ -32,35 +32,38 @@ namespace {
 
 constexpr int kErrAttnDecode = 9;  // a length or page id out of range
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;        // keys
 constexpr int kMaxBlocks = 160;  // of the persistent grid; sizes the workspace
+constexpr int kMaxWarps = 16;    // of a block
 constexpr int kJoinThreads = 256;
 constexpr int kMaxChunks = 256;  // of rows, in the scan of their tiles
+constexpr int kCachedRows = 512; // whose lengths a block keeps in shared memory
 constexpr float kSlack = 8.f;    // log2 of how far a weight may exceed the reference
 
-__host__ __device__ constexpr int stages(int d) { return d == 128 ? 3 : 6; }
+__host__ __device__ constexpr int stages(int d) { return d == 128 ? 2 : 4; }
 __host__ __device__ constexpr int stage_bytes(int d) { return 2 * kTile * d * 2; }
 constexpr int kRingBytes = stages(128) * stage_bytes(128);  // per warp, either d
-
-constexpr int kCachedRows = 1024;  // whose lengths a block keeps in shared memory
 
 // A partial result of a row segment: O^T fragments [d / 16 * 4 * NG][32 lanes], then (in
 // the workspace) the reference and the sum of each of the 8 NG heads.
 __host__ __device__ constexpr int frags(int d, int ng) { return d / 16 * 4 * ng; }
 __host__ __device__ constexpr int part_floats(int d, int ng) { return frags(d, ng) * 32 + 16 * ng; }
 
+// Warps of a block: as many as the rings and a partial result each fit beside (NG = 1), or
+// the registers allow.
+__host__ __device__ constexpr int warps_of(int ng) { return ng == 1 ? 10 : 8; }
+__host__ __device__ constexpr int warp_bytes(int d, int ng) {
+  return kRingBytes + frags(d, ng) * 32 * 4;
+}
+
 // Workspace: per block the row that ends there having begun in another block (or -1) and
-// that other block; per warp the part of a row that ends inside its share; per block the
-// parts of the rows that cross its borders (0: began before, 1: goes on after).
+// that other block; per block the parts of the rows that cross its borders (0: began
+// before, 1: goes on after).
 struct Ends { int vrow, first; };
 __host__ __device__ constexpr size_t ends_bytes() { return kMaxBlocks * sizeof(Ends); }
-__device__ float* warp_part(void* ws, int warp, int pf) {
-  return reinterpret_cast<float*>(static_cast<char*>(ws) + ends_bytes()) + (size_t)warp * pf;
-}
-__device__ float* block_part(void* ws, int block, int side, int pf) {
-  return warp_part(ws, kMaxBlocks * kWarps + 2 * block + side, pf);
+__device__ __forceinline__ float* block_part(void* ws, int block, int side, int pf) {
+  return reinterpret_cast<float*>(static_cast<char*>(ws) + ends_bytes()) +
+         (size_t)(2 * block + side) * pf;
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
@@ -106,7 +109,7 @@ struct Cursor {
                                         int lane) {
     mine = {0, 0};
     if (base + lane < rows)
-      mine = rows <= kCachedRows ? cached[base + lane]
+      mine = base + lane < kCachedRows ? cached[base + lane]
                                    : keys_of(a, a.seq_lens[base + lane], ring_pos(a, base + lane));
   }
   __device__ __forceinline__ void enter(int r) {
@@ -140,26 +143,44 @@ __device__ __forceinline__ size_t out_row(const AttnDecodeArgs& a, int row, int 
   return ((size_t)(row / a.B) * g + head) * a.B + row % a.B;
 }
 
+// Two fragments rows (dims dim .. dim + 15 of eight heads, in the layout of an accumulator)
+// to the outputs: a lane gets pairs of dimensions of head lane / 4.
+__device__ __forceinline__ void store_frag(bf16_t* out, const float* o, const float* inv,
+                                           bool mine) {
+  const uint32_t y0 = transpose8x8(pack2(o[0] * inv[0], o[1] * inv[1]));
+  const uint32_t y1 = transpose8x8(pack2(o[2] * inv[0], o[3] * inv[1]));
+  if (mine) {
+    *reinterpret_cast<uint32_t*>(out) = y0;
+    *reinterpret_cast<uint32_t*>(out + 8) = y1;
+  }
+}
+
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float lse_of(float ref, float sum) {
+  return sum == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
+}
+
 template <int D>
 __device__ __forceinline__ void store_out(const AttnDecodeArgs& a, size_t r, int dim, float acc,
                                           float top, float sum) {
-  a.o[r * D + dim] = (bf16_t)(pack2(sum == 0.f ? 0.f : acc / sum, 0.f) & 0xffffu);
-  if (a.lse && dim == 0) a.lse[r] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
+  a.o[r * D + dim] = (bf16_t)(pack2(acc * inverse(sum), 0.f) & 0xffffu);
+  if (a.lse && dim == 0) a.lse[r] = lse_of(top, sum);
 }
 
 template <int D, int NG>
-__global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
+__global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
     const __grid_constant__ AttnDecodeArgs a, int rows, int groups, int ps_shift) {
   constexpr int S = stages(D), KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
-  static_assert(NF * 32 * 4 <= kRingBytes, "a partial result fits the ring");
+  constexpr int kWarps = warps_of(NG);
+  static_assert(NF * 32 * 4 <= kRingBytes && kWarps <= kMaxWarps, "a partial result fits the ring");
   extern __shared__ __align__(1024) uint8_t smem[];
-  Keys* cached = reinterpret_cast<Keys*>(smem + kWarps * kRingBytes);
+  Keys* cached = reinterpret_cast<Keys*>(smem + kWarps * warp_bytes(D, NG));
   __shared__ long long prefix[kMaxChunks + 1];
   __shared__ long long share_base, share_rem;  // tiles a warp; the first `rem` take one more
   __shared__ uint32_t live[kWarps][S];
-  // what each warp leaves behind: a row that began before its share (head, index w) and one
-  // that goes on after it (tail, index kWarps + w); the bit masks say where there is one
-  __shared__ const float* part[2 * kWarps];
+  // what each warp leaves behind: a row that began before its share (head, index w, behind
+  // the ring) and one that goes on after it (tail, index kWarps + w, in the ring); the bit
+  // masks say where there is one
   __shared__ int vrow_of[2 * kWarps];
   __shared__ float ref_s[2 * kWarps][NG * 8], sum_s[2 * kWarps][NG * 8];
   __shared__ uint32_t heads_m, ends_m, tails_m;
@@ -168,46 +189,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
   const int g = a.Hq / a.Hkv;
   asm volatile("griddepcontrol.launch_dependents;");
 
-  // --- tiles of all rows, by chunks of rows; four chunks' loads at a time
+  // --- tiles of all rows, by chunks of rows; kScan chunks' loads at a time, from rows that
+  // are there, before the first use
+  constexpr int kScan = 4;
   const int per = 32 * ((rows + 32 * kMaxChunks - 1) / (32 * kMaxChunks));
   const int chunks = (rows + per - 1) / per;
-  for (int c0 = warp; c0 < chunks; c0 += 4 * kWarps) {
-    long long sum[4] = {};
+  for (int c0 = warp; c0 < chunks; c0 += kScan * kWarps) {
+    long long sum[kScan] = {};
     for (int i = lane; i < per; i += 32) {
-      int len[4], pos[4];  // all loads before the first use, from rows that are there
+      int len[kScan], pos[kScan];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kScan; ++u) {
         const int r = min((c0 + u * kWarps) * per + i, rows - 1);
         len[u] = a.seq_lens[r];
         pos[u] = ring_pos(a, r);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = c0 + u * kWarps, r = c * per + i;
-        const bool in = c < chunks && r < rows;
-        const Keys k = in ? keys_of(a, len[u], pos[u]) : Keys{0, 0};
-        if (in && rows <= kCachedRows) cached[r] = k;
-        const uint32_t tiles = (k.all + kTile - 1) / kTile;
-        sum[u] += __reduce_add_sync(0xffffffffu, tiles & 0xffffu) +
-                  ((long long)__reduce_add_sync(0xffffffffu, tiles >> 16) << 16);
-        if (c >= chunks || c % gridDim.x != blockIdx.x) continue;
-        // the block that owns the chunk reports lengths out of range, and writes the outputs
-        // of rows without keys
-        if (in && (len[u] < 0 || len[u] > a.max_pages * a.page_size))
-          atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
-        uint32_t empty = __ballot_sync(0xffffffffu, in && k.all == 0);
-        for (; empty; empty &= empty - 1) {
-          const int er = r - lane + __ffs(empty) - 1;
-          for (int e = lane; e < g * (D / 8); e += 32)
-            reinterpret_cast<uint4*>(a.o + out_row(a, er, g, e / (D / 8)) * D)[e % (D / 8)] =
-                make_uint4(0, 0, 0, 0);
-          if (a.lse)
-            for (int h = lane; h < g; h += 32) a.lse[out_row(a, er, g, h)] = -INFINITY;
-        }
+      for (int u = 0; u < kScan; ++u) {
+        const int r = (c0 + u * kWarps) * per + i;
+        const Keys k = keys_of(a, len[u], pos[u]);
+        if (r < min(rows, kCachedRows)) cached[r] = k;
+        // a row has fewer than 2^27 tiles: 32 of them add up in 32 bits
+        sum[u] += __reduce_add_sync(0xffffffffu, r < rows ? (k.all + kTile - 1u) / kTile : 0u);
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kScan; ++u)
       if (lane == 0 && c0 + u * kWarps < chunks) prefix[c0 + u * kWarps + 1] = sum[u] * groups;
   }
   if (tid == 0) {
@@ -294,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
     Cursor cur = ld;
     if (tid == 0) head_first = t0 - ld.tile;
 
-    uint8_t* ring = smem + warp * kRingBytes;
+    uint8_t* ring = smem + warp * warp_bytes(D, NG);
     const uint32_t ring_u = smem_u32(ring);
-    long long to_load = t1 - t0;
+    long long to_find = t1 - t0;
 
     // --- producer: lane i (and i + 16) finds where key i of the tile lies.  The lanes keep
     // 32 entries of the row's block table from page tbase on; a load of more of them is
@@ -318,8 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
         entry = lane <= have ? a.block_table[(size_t)ld.row * a.max_pages + p0 + lane] : -1;
       }
     };
-    auto issue = [&](int stage) {
-      if (to_load > 0) {
+    bool found = false, started = false;
+    auto issue = [&](int stage) {  // copies the tile that was looked up, looks up the next
+      if (found) {
         const int key0 = ld.tile * kTile + (lane & 15);
         const int page = __shfl_sync(0xffffffffu, entry, (idx - tbase) & 31);
         long long at_row = -1;  // row in the pool, or in the ring
@@ -350,13 +358,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
           cp_async16(to, k + e, ok ? 16 : 0);
           cp_async16(to + kTile * D * 2, v + e, ok ? 16 : 0);
         }
-        --to_load;
-        if (to_load > 0) look_up(ld.advance(a, rows, groups, cached, lane));
       }
       cp_async_commit();
+      found = to_find > 0;
+      if (found) {
+        --to_find;
+        look_up(started ? ld.advance(a, rows, groups, cached, lane) : true);
+        started = true;
+      }
     };
-    look_up(true);
-    for (int s = 0; s < S - 1; ++s) issue(s);
 
     // --- consumer
     const float scale = rsqrtf((float)D) * kLog2e;
@@ -379,11 +389,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
     };
     start();
     bool began_here = cur.tile == 0;
+    // the look-up leads the copy by one tile, the copy the arithmetic by S - 1
     int stage = 0;
-    for (long long t = t0; t < t1; ++t) {
-      cp_async_wait<S - 2>();
-      __syncwarp();
+    for (long long t = t0 - S; t < t1; ++t) {
+      if (t >= t0) {
+        cp_async_wait<S - 2>();
+        __syncwarp();
+      }
       issue(stage == 0 ? S - 1 : stage - 1);
+      if (t < t0) {
+        stage = stage == S - 1 ? 0 : stage + 1;
+        continue;
+      }
       const uint32_t kb = ring_u + stage * stage_bytes(D), vb = kb + kTile * D * 2;
       const uint32_t here = live[warp][stage];
       float x[NG][4] = {};
@@ -469,34 +486,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
             float inv[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              inv[i] = l[j][i] == 0.f ? 0.f : 1.f / l[j][i];
+              inv[i] = inverse(l[j][i]);
               const int head = (cur.group * NG + j) * 8 + (lane & 3) * 2 + i;
               if (a.lse && lane < 4 && head < g)
-                a.lse[out_row(a, cur.row, g, head)] =
-                    l[j][i] == 0.f ? -INFINITY : kLn2 * (m[j][i] + log2f(l[j][i]));
+                a.lse[out_row(a, cur.row, g, head)] = lse_of(m[j][i], l[j][i]);
             }
             const int head = (cur.group * NG + j) * 8 + (lane >> 2);
             bf16_t* out = a.o + out_row(a, cur.row, g, head) * D + (lane & 3) * 2;
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-              const uint32_t y0 = transpose8x8(pack2(o[j][s][0] * inv[0], o[j][s][1] * inv[1]));
-              const uint32_t y1 = transpose8x8(pack2(o[j][s][2] * inv[0], o[j][s][3] * inv[1]));
-              if (head < g) {
-                *reinterpret_cast<uint32_t*>(out + s * 16) = y0;
-                *reinterpret_cast<uint32_t*>(out + s * 16 + 8) = y1;
-              }
-            }
+            for (int s = 0; s < KS; ++s) store_frag(out + s * 16, o[j][s], inv, head < g);
           }
         } else {
-          // a part: into the warp's own ring once nothing is in flight there any more, or
-          // (the share goes on) into the workspace
-          float* to = warp_part(a.ws, gw, PF);
-          if (last) {
+          // a part: a tail into the ring, where nothing is in flight any more
+          const int id = began_here ? kWarps + warp : warp;
+          float* to = reinterpret_cast<float*>(ring + (began_here ? 0 : kRingBytes));
+          if (began_here) {
             cp_async_wait<0>();
             __syncwarp();
-            to = reinterpret_cast<float*>(ring);
           }
-          const int id = began_here ? kWarps + warp : warp;
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
 #pragma unroll
@@ -512,7 +519,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
             }
           }
           if (lane == 0) {
-            part[id] = to;
             vrow_of[id] = cur.row * groups + cur.group;
             atomicOr(began_here ? &tails_m : &heads_m, 1u << warp);
             if (!began_here && row_end) atomicOr(&ends_m, 1u << warp);
@@ -555,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
     uint32_t left = starts;
     for (int c = u / kUnits; c > 0; --c) left &= left - 1;
     const int from = __ffs(left) - 1;  // first head of the chain
-    const int len = __ffs(stop >> from) - 1;  // heads that go on (a stop is found: 8 bits of 32)
+    const int len = __ffs(stop >> from) - 1;  // heads that go on (a stop is found: 16 bits of 32)
     const bool ended = (ends_m >> (from + len)) & 1, before = from == 0;
     const int n = len + (ended ? 1 : 0), tail = kWarps + from - 1;  // heads from .. from + n - 1
     // heads of the lane's columns: even and odd fragments
@@ -568,7 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
     }
     auto add = [&](int id) {
       float w[2];
-      const float* x = part[id] + f0 * 32 + lane;
+      const float* x = reinterpret_cast<const float*>(
+          smem + (id < kWarps ? id * warp_bytes(D, NG) + kRingBytes
+                              : (id - kWarps) * warp_bytes(D, NG))) + f0 * 32 + lane;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         w[i] = fast_exp2(ref_s[id][h0 + i] - finite_ref(top[i]));
@@ -580,20 +588,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
     if (!before) add(tail);
 #pragma unroll 2
     for (int p = from; p < from + n; ++p) add(p);
-    const int vrow = vrow_of[before ? 0 : tail], row = vrow / groups;
-    const int head = (vrow - row * groups) * NG * 8 + h0;
-    float* out = block_part(a.ws, blockIdx.x, before ? 0 : 1, PF);
+    if (ended && !before) {
+      const int vrow = vrow_of[tail], row = vrow / groups, group = vrow - row * groups;
+      const float inv[2] = {inverse(sum[0]), inverse(sum[1])};
+      if (a.lse && lane < 4 && f0 % (KS * 4) == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int dim = (f0 + i) / 4 % KS * 16 + (lane >> 2) + (i >> 1 & 1) * 8;
-      if (ended && !before) {
-        if (head + (i & 1) < g)
-          store_out<D>(a, out_row(a, row, g, head + (i & 1)), dim, acc[i], top[i & 1], sum[i & 1]);
-      } else {  // a part for the second kernel
-        out[(f0 + i) * 32 + lane] = acc[i];
-        if (dim == 0) {
-          out[NF * 32 + h0 + (i & 1)] = top[i & 1];
-          out[NF * 32 + NG * 8 + h0 + (i & 1)] = sum[i & 1];
+        for (int i = 0; i < 2; ++i)
+          if (group * NG * 8 + h0 + i < g)
+            a.lse[out_row(a, row, g, group * NG * 8 + h0 + i)] = lse_of(top[i], sum[i]);
+      }
+      const int head = group * NG * 8 + f0 / (KS * 4) * 8 + (lane >> 2);
+      bf16_t* out = a.o + out_row(a, row, g, head) * D + f0 / 4 % KS * 16 + (lane & 3) * 2;
+      store_frag(out, acc, inv, head < g);
+      store_frag(out + 16, acc + 4, inv, head < g);
+    } else {  // a part for the second kernel
+      float* out = block_part(a.ws, blockIdx.x, before ? 0 : 1, PF);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out[(f0 + i) * 32 + lane] = acc[i];
+      if (lane < 4 && f0 % (KS * 4) == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          out[NF * 32 + h0 + i] = top[i];
+          out[NF * 32 + NG * 8 + h0 + i] = sum[i];
         }
       }
     }
@@ -601,13 +617,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(
 }
 
 // Rows that cross blocks: block x joins the row that ends in block x of the first kernel,
-// from the tail of its first block and the heads of those after.
+// from the tail of its first block and the heads of those after.  Rows without keys, which
+// no block of the first kernel meets, are written here too.
 template <int D, int NG>
 __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
-    const __grid_constant__ AttnDecodeArgs a, int groups) {
+    const __grid_constant__ AttnDecodeArgs a, int rows, int groups) {
   constexpr int KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
   constexpr int kFirst = 8;  // parts whose loads start before the weights are known
   __shared__ float ref_s[kMaxBlocks][NG * 8], sum_s[kMaxBlocks][NG * 8];
+  const int g = a.Hq / a.Hkv;
+  // while the first kernel runs: the outputs of rows without keys, and lengths out of range
+  const int every = gridDim.x * gridDim.y * kJoinThreads;
+  for (int r = (blockIdx.y * gridDim.x + blockIdx.x) * kJoinThreads + threadIdx.x; r < rows;
+       r += every) {
+    const int len = a.seq_lens[r];
+    if (len < 0 || len > a.max_pages * a.page_size)
+      atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
+    if (keys_of(a, len, ring_pos(a, r)).all == 0) {
+      for (int h = 0; h < g; ++h) {
+        uint4* out = reinterpret_cast<uint4*>(a.o + out_row(a, r, g, h) * D);
+        for (int e = 0; e < D / 8; ++e) out[e] = make_uint4(0, 0, 0, 0);
+        if (a.lse) a.lse[out_row(a, r, g, h)] = -INFINITY;
+      }
+    }
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Ends end = static_cast<const Ends*>(a.ws)[blockIdx.x];
   if (end.vrow < 0) return;
@@ -643,14 +676,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
     acc += part(p)[f] * w;
     sum += sum_s[p][h] * w;
   }
-  const int g = a.Hq / a.Hkv, row = end.vrow / groups;
+  const int row = end.vrow / groups;
   const int head = (end.vrow - row * groups) * NG * 8 + h;
   if (head < g) store_out<D>(a, out_row(a, row, g, head), dim, acc, top, sum);
 }
 
 template <int D, int NG>
 cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s) {
-  constexpr int smem = kWarps * kRingBytes + kCachedRows * (int)sizeof(Keys);
+  constexpr int kWarps = warps_of(NG);
+  constexpr int smem = kWarps * warp_bytes(D, NG) + kCachedRows * (int)sizeof(Keys);
   static int nsm[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -673,7 +707,7 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
   if ((a.page_size & (a.page_size - 1)) == 0)
     for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
   count_launches(2);
-  attn_decode_kernel<D, NG><<<blocks, kThreads, smem, s>>>(a, rows, groups, shift);
+  attn_decode_kernel<D, NG><<<blocks, kWarps * 32, smem, s>>>(a, rows, groups, shift);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join's blocks come up while the first kernel runs and wait for its results
@@ -686,7 +720,7 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, NG>, a, groups);
+  return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, NG>, a, rows, groups);
 }
 
 }  // namespace
@@ -694,7 +728,7 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
 size_t attn_decode_workspace_bytes(int rows, int group, int d) {
   (void)rows;
   const int ng = group <= 8 ? 1 : 2;
-  return ends_bytes() + (size_t)kMaxBlocks * (kWarps + 2) * part_floats(d, ng) * sizeof(float);
+  return ends_bytes() + (size_t)kMaxBlocks * 2 * part_floats(d, ng) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t s) {
