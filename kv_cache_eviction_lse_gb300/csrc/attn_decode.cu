@@ -194,15 +194,18 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
   constexpr int kScan = 4;
   const int per = 32 * ((rows + 32 * kMaxChunks - 1) / (32 * kMaxChunks));
   const int chunks = (rows + per - 1) / per;
+  const int b_step = a.w > 0 ? kWarps * per % a.B : 0;
   for (int c0 = warp; c0 < chunks; c0 += kScan * kWarps) {
     long long sum[kScan] = {};
     for (int i = lane; i < per; i += 32) {
       int len[kScan], pos[kScan];
+      int b = a.w > 0 ? (c0 * per + i) % a.B : 0;  // sequence of the row
 #pragma unroll
       for (int u = 0; u < kScan; ++u) {
-        const int r = min((c0 + u * kWarps) * per + i, rows - 1);
-        len[u] = a.seq_lens[r];
-        pos[u] = ring_pos(a, r);
+        len[u] = a.seq_lens[min((c0 + u * kWarps) * per + i, rows - 1)];
+        pos[u] = a.w > 0 ? a.pos[b] : 0;
+        b += b_step;
+        if (b >= a.B) b -= a.B;
       }
 #pragma unroll
       for (int u = 0; u < kScan; ++u) {
@@ -275,29 +278,36 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
                                   prefix[min(chunk + lane, chunks)] <= t0)) - 1;
     Cursor ld;
     ld.base = chunk * per;
-    long long at = prefix[chunk];
+    const long long into = t0 - prefix[chunk];
+    long long rel = groups == 1 ? into : into / groups;  // tiles of one group
+    uint32_t before;
     for (;;) {
       ld.fetch(a, rows, cached, lane);
-      const long long mine = (long long)((ld.mine.all + kTile - 1) / kTile) * groups;
-      long long incl = mine;
+      const uint32_t mine = (ld.mine.all + kTile - 1) / kTile;
+      uint32_t incl = mine;  // 32 rows of fewer than 2^27 tiles
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, at + incl > t0);
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > rel);
       if (past) {
         const int l = __ffs(past) - 1;
         ld.enter(ld.base + l);
-        at += __shfl_sync(0xffffffffu, incl - mine, l);
+        before = __shfl_sync(0xffffffffu, incl - mine, l);
         break;
       }
-      at += __shfl_sync(0xffffffffu, incl, 31);
+      rel -= __shfl_sync(0xffffffffu, incl, 31);
       ld.base += 32;
     }
-    const int nt = (ld.keys.all + kTile - 1) / kTile, off = (int)(t0 - at);
-    ld.group = groups == 1 ? 0 : off / nt;
-    ld.tile = off - ld.group * nt;
+    ld.group = 0;
+    ld.tile = (int)(rel - before);
+    if (groups > 1) {  // the row's tiles come once for each group
+      const int nt = (ld.keys.all + kTile - 1) / kTile;
+      const long long off = into - (into / groups - ld.tile) * groups;
+      ld.group = (int)(off / nt);
+      ld.tile = (int)(off - (long long)ld.group * nt);
+    }
     Cursor cur = ld;
     if (tid == 0) head_first = t0 - ld.tile;
 
@@ -554,62 +564,71 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
     }
     ends[blockIdx.x] = e;
   }
-  // a warp takes eight fragments of a chain at a time, all their loads in flight
+  // a warp takes a chain, or with few chains a slice of one, eight fragments at a time with
+  // all their loads in flight
   constexpr int kUnits = NF / 8;
-  const int work = __popc(starts) * kUnits;
-  for (int u = warp; u < work; u += kWarps) {
+  int slices = kUnits;
+  while (slices > NG && __popc(starts) * slices > kWarps) slices >>= 1;
+  const int work = __popc(starts) * slices;
+  for (int v = warp; v < work; v += kWarps) {
     uint32_t left = starts;
-    for (int c = u / kUnits; c > 0; --c) left &= left - 1;
+    for (int c = v / slices; c > 0; --c) left &= left - 1;
     const int from = __ffs(left) - 1;  // first head of the chain
     const int len = __ffs(stop >> from) - 1;  // heads that go on (a stop is found: 16 bits of 32)
     const bool ended = (ends_m >> (from + len)) & 1, before = from == 0;
     const int n = len + (ended ? 1 : 0), tail = kWarps + from - 1;  // heads from .. from + n - 1
-    // heads of the lane's columns: even and odd fragments
-    const int f0 = u % kUnits * 8, h0 = f0 / (KS * 4) * 8 + (lane & 3) * 2;
-    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {}, acc[8] = {};
+    const int u0 = v % slices * (kUnits / slices);
+    // heads of the lane's columns: even and odd fragments; a slice has one j
+    const int h0 = u0 * 8 / (KS * 4) * 8 + (lane & 3) * 2;
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (!before) top[i] = ref_s[tail][h0 + i];
       for (int p = from; p < from + n; ++p) top[i] = fmaxf(top[i], ref_s[p][h0 + i]);
     }
-    auto add = [&](int id) {
-      float w[2];
-      const float* x = reinterpret_cast<const float*>(
-          smem + (id < kWarps ? id * warp_bytes(D, NG) + kRingBytes
-                              : (id - kWarps) * warp_bytes(D, NG))) + f0 * 32 + lane;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        w[i] = fast_exp2(ref_s[id][h0 + i] - finite_ref(top[i]));
-        sum[i] += sum_s[id][h0 + i] * w[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += x[i * 32] * w[i & 1];
-    };
-    if (!before) add(tail);
-#pragma unroll 2
-    for (int p = from; p < from + n; ++p) add(p);
-    if (ended && !before) {
-      const int vrow = vrow_of[tail], row = vrow / groups, group = vrow - row * groups;
-      const float inv[2] = {inverse(sum[0]), inverse(sum[1])};
-      if (a.lse && lane < 4 && f0 % (KS * 4) == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (group * NG * 8 + h0 + i < g)
-            a.lse[out_row(a, row, g, group * NG * 8 + h0 + i)] = lse_of(top[i], sum[i]);
-      }
-      const int head = group * NG * 8 + f0 / (KS * 4) * 8 + (lane >> 2);
-      bf16_t* out = a.o + out_row(a, row, g, head) * D + f0 / 4 % KS * 16 + (lane & 3) * 2;
-      store_frag(out, acc, inv, head < g);
-      store_frag(out + 16, acc + 4, inv, head < g);
-    } else {  // a part for the second kernel
-      float* out = block_part(a.ws, blockIdx.x, before ? 0 : 1, PF);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) out[(f0 + i) * 32 + lane] = acc[i];
-      if (lane < 4 && f0 % (KS * 4) == 0) {
+    for (int u = u0; u < u0 + kUnits / slices; ++u) {
+      const int f0 = u * 8;
+      float acc[8] = {};
+      sum[0] = sum[1] = 0.f;
+      auto add = [&](int id) {
+        float w[2];
+        const float* x = reinterpret_cast<const float*>(
+            smem + (id < kWarps ? id * warp_bytes(D, NG) + kRingBytes
+                                : (id - kWarps) * warp_bytes(D, NG))) + f0 * 32 + lane;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          out[NF * 32 + h0 + i] = top[i];
-          out[NF * 32 + NG * 8 + h0 + i] = sum[i];
+          w[i] = fast_exp2(ref_s[id][h0 + i] - finite_ref(top[i]));
+          sum[i] += sum_s[id][h0 + i] * w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += x[i * 32] * w[i & 1];
+      };
+      if (!before) add(tail);
+#pragma unroll 2
+      for (int p = from; p < from + n; ++p) add(p);
+      if (ended && !before) {
+        const int vrow = vrow_of[tail], row = vrow / groups, group = vrow - row * groups;
+        const float inv[2] = {inverse(sum[0]), inverse(sum[1])};
+        if (a.lse && lane < 4 && f0 % (KS * 4) == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (group * NG * 8 + h0 + i < g)
+              a.lse[out_row(a, row, g, group * NG * 8 + h0 + i)] = lse_of(top[i], sum[i]);
+        }
+        const int head = group * NG * 8 + f0 / (KS * 4) * 8 + (lane >> 2);
+        bf16_t* out = a.o + out_row(a, row, g, head) * D + f0 / 4 % KS * 16 + (lane & 3) * 2;
+        store_frag(out, acc, inv, head < g);
+        store_frag(out + 16, acc + 4, inv, head < g);
+      } else {  // a part for the second kernel
+        float* out = block_part(a.ws, blockIdx.x, before ? 0 : 1, PF);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[(f0 + i) * 32 + lane] = acc[i];
+        if (lane < 4 && f0 % (KS * 4) == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            out[NF * 32 + h0 + i] = top[i];
+            out[NF * 32 + NG * 8 + h0 + i] = sum[i];
+          }
         }
       }
     }
