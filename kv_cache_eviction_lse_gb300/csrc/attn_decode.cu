@@ -175,8 +175,7 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
   static_assert(NF * 32 * 4 <= kRingBytes && kWarps <= kMaxWarps, "a partial result fits the ring");
   extern __shared__ __align__(1024) uint8_t smem[];
   Keys* cached = reinterpret_cast<Keys*>(smem + kWarps * warp_bytes(D, NG));
-  __shared__ long long prefix[kMaxChunks + 1];
-  __shared__ long long share_base, share_rem;  // tiles a warp; the first `rem` take one more
+  __shared__ long long chunk_tiles[kMaxChunks];
   __shared__ uint32_t live[kWarps][S];
   // what each warp leaves behind: a row that began before its share (head, index w, behind
   // the ring) and one that goes on after it (tail, index kWarps + w, in the ring); the bit
@@ -218,47 +217,30 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
     }
 #pragma unroll
     for (int u = 0; u < kScan; ++u)
-      if (lane == 0 && c0 + u * kWarps < chunks) prefix[c0 + u * kWarps + 1] = sum[u] * groups;
+      if (lane == 0 && c0 + u * kWarps < chunks) chunk_tiles[c0 + u * kWarps] = sum[u];
   }
-  if (tid == 0) {
-    heads_m = ends_m = tails_m = 0;
-    prefix[0] = 0;
-  }
+  if (tid == 0) heads_m = ends_m = tails_m = 0;
   __syncthreads();
-  if (warp == 0) {
-    const int each = (chunks + 31) / 32;
-    long long sum = 0;
-    for (int i = 0; i < each; ++i) {
-      const int c = lane * each + i;
-      if (c < chunks) {
-        sum += prefix[c + 1];
-        prefix[c + 1] = sum;
-      }
-    }
-    long long before = sum;
+  // --- every warp for itself (a second barrier would cost more): the sum over the chunks,
+  // its share of the stream, and the row where that begins
+  const int each = (chunks + 31) / 32;  // chunks of a lane
+  long long lane_tiles = 0;
+  for (int i = 0; i < each; ++i)
+    if (lane * each + i < chunks) lane_tiles += chunk_tiles[lane * each + i];
+  long long lanes_incl = lane_tiles;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += y;
-    }
-    const long long all = __shfl_sync(0xffffffffu, before, 31);
-    before -= sum;
-    for (int i = 0; i < each; ++i)
-      if (lane * each + i < chunks) prefix[lane * each + i + 1] += before;
-    if (lane == 0) {
-      const int most = gridDim.x * kWarps;
-      if (all <= most) {
-        share_base = 1;
-        share_rem = 0;
-      } else {
-        share_base = all < INT32_MAX ? (uint32_t)all / (uint32_t)most : all / most;
-        share_rem = all - share_base * most;
-      }
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, lanes_incl, o);
+    if (lane >= o) lanes_incl += y;
   }
-  __syncthreads();
-  const long long total = prefix[chunks];
-  const long long warps = min((long long)gridDim.x * kWarps, total);
+  const long long total = __shfl_sync(0xffffffffu, lanes_incl, 31) * groups;
+  const int most = gridDim.x * kWarps;
+  long long share_base = 1, share_rem = 0;  // tiles a warp; the first `rem` take one more
+  if (total > most) {
+    share_base = total <= UINT32_MAX ? (uint32_t)total / (uint32_t)most : total / most;
+    share_rem = total - share_base * most;
+  }
+  const long long warps = min((long long)most, total);
   const int gw = blockIdx.x * kWarps + warp;
   Ends* ends = static_cast<Ends*>(a.ws);
   if (blockIdx.x * kWarps >= warps) {
@@ -269,17 +251,13 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
   if (gw < warps) {
     const long long t0 = gw * share_base + min((long long)gw, share_rem);
     const long long t1 = t0 + share_base + (gw < share_rem);
-    // --- the row of the share's first tile: its chunk (the last that begins at or before
-    // it), then the row among the chunk's
-    const int each = (chunks + 31) / 32;
-    int chunk = each * (__popc(__ballot_sync(0xffffffffu, lane * each < chunks &&
-                                             prefix[min(lane * each, chunks)] <= t0)) - 1);
-    chunk += __popc(__ballot_sync(0xffffffffu, lane < each && chunk + lane < chunks &&
-                                  prefix[min(chunk + lane, chunks)] <= t0)) - 1;
+    const long long u0 = groups == 1 ? t0 : t0 / groups;  // in tiles of one group
+    const int l0 = __ffs(__ballot_sync(0xffffffffu, lanes_incl > u0)) - 1;
+    long long rel = u0 - __shfl_sync(0xffffffffu, lanes_incl - lane_tiles, l0);
+    int chunk = l0 * each;
+    while (rel >= chunk_tiles[chunk]) rel -= chunk_tiles[chunk++];
     Cursor ld;
     ld.base = chunk * per;
-    const long long into = t0 - prefix[chunk];
-    long long rel = groups == 1 ? into : into / groups;  // tiles of one group
     uint32_t before;
     for (;;) {
       ld.fetch(a, rows, cached, lane);
@@ -304,7 +282,7 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
     ld.tile = (int)(rel - before);
     if (groups > 1) {  // the row's tiles come once for each group
       const int nt = (ld.keys.all + kTile - 1) / kTile;
-      const long long off = into - (into / groups - ld.tile) * groups;
+      const long long off = t0 - (u0 - ld.tile) * groups;
       ld.group = (int)(off / nt);
       ld.tile = (int)(off - (long long)ld.group * nt);
     }
