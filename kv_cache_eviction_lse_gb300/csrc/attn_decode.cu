@@ -620,7 +620,7 @@ template <int D, int NG>
 __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
     const __grid_constant__ AttnDecodeArgs a, int rows, int groups) {
   constexpr int KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
-  constexpr int kFirst = 8;  // parts whose loads start before the weights are known
+  constexpr int kFirst = 24;  // parts whose loads start before the weights are known
   __shared__ float ref_s[kMaxBlocks][NG * 8], sum_s[kMaxBlocks][NG * 8];
   const int g = a.Hq / a.Hkv;
   // while the first kernel runs: the outputs of rows without keys, and lengths out of range

@@ -6,8 +6,10 @@
 // f is kept as turns per position in a 64-bit binary fraction, so p f mod 1 is one integer
 // product that wraps where the angle does: the angle of any 32-bit position is exact to
 // p 2^-65 turns and needs no range reduction (a 32-bit product would be off by 0.01 rad at
-// position 131072).  Its top 32 bits go to sincospif, the products are fp32, and each
-// result is rounded to bf16 once.
+// position 131072).  In [-pi, pi] the hardware's sine and cosine are good to 2^-21, far
+// below the bf16 rounding of the result (2^-8 relative), at a tenth of the instructions of
+// sincospif, which bounded batches of a few thousand rows (2079 tokens of 14 heads 6.5 us).
+// The products are fp32, and each result is rounded to bf16 once.
 //
 // Bound by HBM (or, for a few tokens, by latency): every row is read and written once, and
 // a thread that has the cosines and sines of its token's 8 pairs reuses them for the heads
@@ -70,8 +72,9 @@ __device__ __forceinline__ void angles(const RopeArgs& r, int u, int pos, float*
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint64_t phase = (uint64_t)(int64_t)pos * r.freq[8 * u + i];
-    const float half_turns = (float)(int32_t)(phase >> 32) * 0x1p-31f;
-    sincospif(half_turns, &s[i], &c[i]);
+    const float x = (float)(int32_t)(phase >> 32) * (3.14159265358979324f * 0x1p-31f);
+    c[i] = __cosf(x);
+    s[i] = __sinf(x);
   }
 }
 
@@ -128,6 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(const AppendA
   __shared__ long long sums[32];
   __shared__ int err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) err = 0;
   __syncthreads();
   auto fault = [&](int code) { atomicMax(&err, code); };
@@ -207,19 +211,25 @@ __device__ __forceinline__ int page_of(const AppendArgs& a, int r, int n, int fi
   return idx < have ? a.block_table[(size_t)r * a.max_pages + idx] : first + idx - have;
 }
 
+// Blocks 0 .. token_blocks * groups - 1 take tokens (block / groups) and every groups-th
+// slab: a head of the queries, or one of keys and values together.  The blocks behind them
+// clear page ends.  Nothing is written before the plan is known; the first slab's rows, the
+// angles and the token's sequence are ready by then.
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ RopeArgs r,
                                                           const __grid_constant__ AppendArgs a,
-                                                          int token_blocks) {
+                                                          int token_blocks, int groups) {
   constexpr int kPer = D / 16;
-  if (a.plan[0] != 0) return;
   const int rows = r.L * r.Hkv * a.B;
-  if ((int)blockIdx.x >= token_blocks) {
+  if ((int)blockIdx.x >= token_blocks * groups) {
     // one warp per row: the unused rows of the row's last page, where that page is new
-    const int row = (blockIdx.x - token_blocks) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (blockIdx.y != 0 || row >= rows) return;
-    const int b = row % a.B, n = a.plan[kPlanHeader + 2 * row];
+    const int row = (blockIdx.x - token_blocks * groups) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int b = row % a.B;
     const int m = a.tok_start ? a.tok_start[b + 1] - a.tok_start[b] : 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.plan[0] != 0) return;
+    const int n = a.plan[kPlanHeader + 2 * row];
     const int have = (n + a.page_size - 1) / a.page_size;
     const int used = (n + m) % a.page_size, last = (n + m) / a.page_size;
     if (used == 0 || last < have) return;
@@ -233,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     return;
   }
   const int u = threadIdx.x % kPer;
-  const int t = blockIdx.x * (kThreads / kPer) + threadIdx.x / kPer;
+  const int t = blockIdx.x / groups * (kThreads / kPer) + threadIdx.x / kPer;
   if (t >= r.N) return;
   // the token's sequence: the last b with tok_start[b] <= t
   int b = t, j = 0;
@@ -250,29 +260,50 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const Lane ln = lane_of(u, r.rot_dim, r.interleaved);
   float c[8], s[8];
   if (ln.rotate) angles(r, u, r.pos[t], c, s);
-  const int n_q = r.q ? r.L * r.Hq : 0, n_k = r.L * r.Hkv, n_all = n_q + 2 * n_k;
-  for (int slab = blockIdx.y; slab < n_all; slab += gridDim.y) {
-    const int kind = slab < n_q ? 0 : slab < n_q + n_k ? 1 : 2;
-    const int head = kind == 0 ? slab : kind == 1 ? slab - n_q : slab - n_q - n_k;
-    const size_t row = ((size_t)head * r.N + t) * D;
-    const uint4* in = reinterpret_cast<const uint4*>((kind == 0 ? r.q : kind == 1 ? r.k : a.v) + row);
-    uint4 x0 = in[ln.c0], x1 = in[ln.c1];
-    if (ln.rotate && kind < 2) rotate(x0, x1, c, s, r.interleaved);
-    uint4* out;
-    if (kind == 0) {
-      out = reinterpret_cast<uint4*>(r.q_out + row);
-    } else {
-      const int cr = head * a.B + b;
-      const int n = a.plan[kPlanHeader + 2 * cr], first = a.plan[kPlanHeader + 2 * cr + 1];
-      const int slot = n + j, idx = slot / a.page_size, off = slot % a.page_size;
-      const int pg = page_of(a, cr, n, first, idx);
-      // a new page enters the table with the first of its rows that this call writes
-      if (kind == 1 && u == 0 && off == 0) a.block_table[(size_t)cr * a.max_pages + idx] = pg;
-      out = reinterpret_cast<uint4*>((kind == 1 ? a.k_pages : a.v_pages) +
-                                     ((size_t)pg * a.page_size + off) * D);
+  const int n_q = r.q ? r.L * r.Hq : 0, n_all = n_q + r.L * r.Hkv;
+  auto row_at = [&](int head) { return ((size_t)head * r.N + t) * D; };
+  uint4 x0, x1, v0 = {}, v1 = {};
+  auto load = [&](int slab) {
+    const bool is_q = slab < n_q;
+    const size_t row = row_at(is_q ? slab : slab - n_q);
+    const uint4* in = reinterpret_cast<const uint4*>((is_q ? r.q : r.k) + row);
+    x0 = in[ln.c0];
+    x1 = in[ln.c1];
+    if (!is_q) {
+      v0 = reinterpret_cast<const uint4*>(a.v + row)[ln.c0];
+      v1 = reinterpret_cast<const uint4*>(a.v + row)[ln.c1];
     }
-    out[ln.c0] = x0;
-    out[ln.c1] = x1;
+  };
+  int slab = blockIdx.x % groups;
+  if (slab < n_all) load(slab);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.plan[0] != 0) return;
+  while (slab < n_all) {
+    const int at = slab;
+    uint4 y0 = x0, y1 = x1;
+    const uint4 w0 = v0, w1 = v1;
+    slab += groups;
+    if (slab < n_all) load(slab);  // the next rows come while these are turned and stored
+    if (ln.rotate) rotate(y0, y1, c, s, r.interleaved);
+    if (at < n_q) {
+      uint4* out = reinterpret_cast<uint4*>(r.q_out + row_at(at));
+      out[ln.c0] = y0;
+      out[ln.c1] = y1;
+      continue;
+    }
+    const int cr = (at - n_q) * a.B + b;
+    const int2 plan = reinterpret_cast<const int2*>(a.plan + kPlanHeader)[cr];
+    const int slot = plan.x + j, idx = slot / a.page_size, off = slot - idx * a.page_size;
+    const int pg = page_of(a, cr, plan.x, plan.y, idx);
+    // a new page enters the table with the first of its rows that this call writes
+    if (u == 0 && off == 0) a.block_table[(size_t)cr * a.max_pages + idx] = pg;
+    const size_t to = ((size_t)pg * a.page_size + off) * D;
+    uint4* out = reinterpret_cast<uint4*>(a.k_pages + to);
+    out[ln.c0] = y0;
+    out[ln.c1] = y1;
+    out = reinterpret_cast<uint4*>(a.v_pages + to);
+    out[ln.c0] = w0;
+    out[ln.c1] = w1;
   }
 }
 
@@ -308,17 +339,23 @@ cudaError_t launch_append(const RopeArgs& r, const AppendArgs& a, cudaStream_t s
   append_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, rows, r.N);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || r.N == 0) return e;
-  const int slabs = (r.q ? r.L * r.Hq : 0) + 2 * r.L * r.Hkv;
+  const int slabs = (r.q ? r.L * r.Hq : 0) + r.L * r.Hkv;
   const int per_block = kThreads / (r.d / 16);
-  const int blocks = (r.N + per_block - 1) / per_block;
+  const int blocks = (r.N + per_block - 1) / per_block, groups = slab_groups(blocks, slabs);
   const int clear = a.page_size > 1 ? (rows + kThreads / 32 - 1) / (kThreads / 32) : 0;
-  const dim3 grid(blocks + clear, slab_groups(blocks, slabs));
+  // its blocks come up beside the plan's and wait for it
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks * groups + clear);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   count_launches(1);
-  if (r.d == 128)
-    append_kernel<128><<<grid, kThreads, 0, s>>>(r, a, blocks);
-  else
-    append_kernel<64><<<grid, kThreads, 0, s>>>(r, a, blocks);
-  return cudaGetLastError();
+  return r.d == 128 ? cudaLaunchKernelEx(&cfg, append_kernel<128>, r, a, blocks, groups)
+                    : cudaLaunchKernelEx(&cfg, append_kernel<64>, r, a, blocks, groups);
 }
 
 cudaError_t rope_device_error(int* code, bool clear, cudaStream_t s) {
