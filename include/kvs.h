@@ -517,7 +517,8 @@ kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const in
  * over the keys of KV head hq / g.  A row without keys gives o = 0 and lse = -inf.  The
  * softmax weights are rounded to bf16 before they multiply V on the tensor cores; sums
  * and statistics are fp32 and o is stored as bf16.  Results do not depend on the order in
- * which blocks run.
+ * which blocks run; where a long row is split, and with it the rounding of the sums, goes by
+ * the sizes of the call and the lengths of its rows.
  * A length outside [0, max_pages * page_size] is taken as the nearest bound and keys of a
  * page id outside [0, capacity_pages) are left out; either sets the device error word (9).
  *

@@ -35,6 +35,7 @@ constexpr int kErrAttnDecode = 9;  // a length or page id out of range
 constexpr int kTile = 16;        // keys
 constexpr int kMaxBlocks = 160;  // of the persistent grid; sizes the workspace
 constexpr int kMaxWarps = 16;    // of a block
+constexpr int kRowWarps = 4;     // of a block that has one row
 constexpr int kJoinThreads = 256;
 constexpr int kMaxChunks = 256;  // of rows, in the scan of their tiles
 constexpr int kCachedRows = 512; // whose lengths a block keeps in shared memory
@@ -167,6 +168,230 @@ __device__ __forceinline__ void store_out(const AttnDecodeArgs& a, size_t r, int
   if (a.lse && dim == 0) a.lse[r] = lse_of(top, sum);
 }
 
+// Eight fragments (32 dimensions of eight heads) from f0 on, summed up: to the outputs.
+template <int D, int NG>
+__device__ __forceinline__ void store_unit(const AttnDecodeArgs& a, int row, int group, int g,
+                                           int f0, const float* acc, const float* top,
+                                           const float* sum, int lane) {
+  constexpr int KS = D / 16;
+  const float inv[2] = {inverse(sum[0]), inverse(sum[1])};
+  const int h0 = (group * NG + f0 / (KS * 4)) * 8;
+  if (a.lse && lane < 4 && f0 % (KS * 4) == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (h0 + lane * 2 + i < g) a.lse[out_row(a, row, g, h0 + lane * 2 + i)] = lse_of(top[i], sum[i]);
+  }
+  const int head = h0 + (lane >> 2);
+  bf16_t* out = a.o + out_row(a, row, g, head) * D + f0 / 4 % KS * 16 + (lane & 3) * 2;
+  store_frag(out, acc, inv, head < g);
+  store_frag(out + 16, acc + 4, inv, head < g);
+}
+
+// The copies of a warp: finds where the keys of a tile lie, and brings their rows of K and V
+// into a stage of its ring.  Lane i (and i + 16) has key i of the tile.  The lanes keep 32
+// entries of the row's block table from page tbase on; a load of more of them is used an
+// iteration later.
+template <int D>
+struct Copies {
+  const AttnDecodeArgs& a;
+  const int ps_shift, lane;  // log2 of the page size, or -1
+  const uint32_t ring_u;
+  uint32_t* live;            // per stage: which of its keys are there
+  int tbase = 0, entry = -1;
+  int idx = 0, inside = 0;   // the key's page in the row, and its row in the page
+
+  __device__ __forceinline__ void look_up(int row, int tile, const Keys& keys, bool new_row) {
+    const int first = tile * kTile, key = first + (lane & 15);
+    idx = ps_shift >= 0 ? key >> ps_shift : key / a.page_size;
+    inside = key - idx * a.page_size;
+    const int paged = min(kTile, keys.paged - first);  // keys of the tile in pages
+    if (paged <= 0) return;
+    const int p0 = __shfl_sync(0xffffffffu, idx, 0);
+    const int p1 = __shfl_sync(0xffffffffu, idx, paged - 1);
+    if (new_row || p1 > tbase + 31) {
+      tbase = p0;
+      const int ahead = keys.paged - 1 - p0 * a.page_size;
+      const int have = ps_shift >= 0 ? ahead >> ps_shift : ahead / a.page_size;
+      entry = lane <= have ? a.block_table[(size_t)row * a.max_pages + p0 + lane] : -1;
+    }
+  }
+
+  __device__ __forceinline__ void copy(int row, int tile, const Keys& keys, int stage) {
+    const int key0 = tile * kTile + (lane & 15);
+    const int page = __shfl_sync(0xffffffffu, entry, (idx - tbase) & 31);
+    long long at_row = -1;  // row in the pool, or in the ring
+    const bool in_ring = key0 >= keys.paged;
+    if (key0 < keys.all) {
+      if (in_ring)
+        at_row = (long long)row * a.w + (key0 - keys.paged);
+      else if ((uint32_t)page < (uint32_t)a.capacity)
+        at_row = (long long)page * a.page_size + inside;
+      else
+        atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, at_row >= 0);
+    const uint32_t ringed = __ballot_sync(0xffffffffu, in_ring);
+    if (lane == 0) live[stage] = here;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a step
+    const int c = lane % kLanes;
+    const uint32_t dst = ring_u + stage * stage_bytes(D);
+#pragma unroll
+    for (int i = 0; i < kTile / kRows; ++i) {
+      const int key = i * kRows + lane / kLanes;
+      const long long r = __shfl_sync(0xffffffffu, at_row, key);
+      const bool ok = (here >> key) & 1, rg = (ringed >> key) & 1;
+      const size_t e = ok ? (size_t)r * D + c * 8 : 0;
+      const bf16_t* k = rg ? a.ring_k : a.k_pages;
+      const bf16_t* v = rg ? a.ring_v : a.v_pages;
+      const uint32_t to = dst + key * (D * 2) + ((c ^ (key & 7)) << 4);
+      cp_async16(to, k + e, ok ? 16 : 0);
+      cp_async16(to + kTile * D * 2, v + e, ok ? 16 : 0);
+    }
+  }
+};
+
+// The softmax state of a warp for the 8 NG query heads of a group, in the layout of the
+// accumulators: keys or dimensions lane / 4 (+ 8), heads 2 (lane % 4) + {0, 1} of each 8.
+template <int D, int NG>
+struct Heads {
+  static constexpr int KS = D / 16;
+  uint32_t q[NG][KS][2];
+  float o[NG][KS][4], m[NG][2], l[NG][2];
+
+  __device__ __forceinline__ void start(const AttnDecodeArgs& a, int row, int group, int g,
+                                        int lane) {
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      const int head = (group * NG + j) * 8 + (lane >> 2);
+      const bf16_t* src = a.q + out_row(a, row, g, head) * D + (lane & 3) * 2;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        q[j][s][0] = head < g ? *reinterpret_cast<const uint32_t*>(src + s * 16) : 0u;
+        q[j][s][1] = head < g ? *reinterpret_cast<const uint32_t*>(src + s * 16 + 8) : 0u;
+        o[j][s][0] = o[j][s][1] = o[j][s][2] = o[j][s][3] = 0.f;
+      }
+      m[j][0] = m[j][1] = -INFINITY;
+      l[j][0] = l[j][1] = 0.f;
+    }
+  }
+
+  // One tile in shared memory (K at kb, V behind it) whose keys `here` are there.
+  __device__ __forceinline__ void tile(uint32_t kb, uint32_t here, int lane) {
+    const float scale = rsqrtf((float)D) * kLog2e;
+    float x[NG][4] = {};
+    {
+      const int key = ((lane >> 3) & 1) * 8 + (lane & 7);
+      const uint32_t row_u = kb + key * (D * 2);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint32_t k[4];
+        ldmatrix_x4(row_u + (((s * 2 + (lane >> 4)) ^ (key & 7)) << 4), k[0], k[1], k[2], k[3]);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) mma_bf16_16816(x[j], k, q[j][s][0], q[j][s][1]);
+      }
+    }
+    bool raise = false;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = (lane >> 2) + (i >> 1) * 8;
+        x[j][i] = (here >> key) & 1 ? x[j][i] * scale : -INFINITY;
+        raise |= x[j][i] > m[j][i & 1] + kSlack;
+      }
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float top = fmaxf(x[j][i], x[j][i + 2]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          top = fmaxf(m[j][i], top);
+          const float c = fast_exp2(m[j][i] - finite_ref(top));
+          m[j][i] = top;
+          l[j][i] *= c;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            o[j][s][i] *= c;
+            o[j][s][i + 2] *= c;
+          }
+        }
+      }
+    }
+    uint32_t pf[NG][2];
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      float p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = fast_exp2(x[j][i] - finite_ref(m[j][i & 1]));
+      l[j][0] += p[0] + p[2];
+      l[j][1] += p[1] + p[3];
+      pf[j][0] = transpose8x8(pack2(p[0], p[1]));
+      pf[j][1] = transpose8x8(pack2(p[2], p[3]));
+    }
+    const int key = (lane >> 4) * 8 + (lane & 7);
+    const uint32_t row_u = kb + (kTile + key) * (D * 2);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      uint32_t v[4];
+      ldmatrix_x4_trans(row_u + (((s * 2 + ((lane >> 3) & 1)) ^ (key & 7)) << 4), v);
+#pragma unroll
+      for (int j = 0; j < NG; ++j) mma_bf16_16816(o[j][s], v, pf[j][0], pf[j][1]);
+    }
+  }
+
+  // the sums over the lanes of a column
+  __device__ __forceinline__ void fold() {
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[j][i] += __shfl_xor_sync(0xffffffffu, l[j][i], 4);
+        l[j][i] += __shfl_xor_sync(0xffffffffu, l[j][i], 8);
+        l[j][i] += __shfl_xor_sync(0xffffffffu, l[j][i], 16);
+      }
+  }
+
+  __device__ __forceinline__ void store(const AttnDecodeArgs& a, int row, int group, int g,
+                                        int lane) const {
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      float inv[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        inv[i] = inverse(l[j][i]);
+        const int head = (group * NG + j) * 8 + (lane & 3) * 2 + i;
+        if (a.lse && lane < 4 && head < g) a.lse[out_row(a, row, g, head)] = lse_of(m[j][i], l[j][i]);
+      }
+      const int head = (group * NG + j) * 8 + (lane >> 2);
+      bf16_t* out = a.o + out_row(a, row, g, head) * D + (lane & 3) * 2;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) store_frag(out + s * 16, o[j][s], inv, head < g);
+    }
+  }
+
+  // a part: fragments to `to`, references and sums of the 8 NG heads
+  __device__ __forceinline__ void leave(float* to, float* ref, float* sum, int lane) const {
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[((j * KS + s) * 4 + i) * 32 + lane] = o[j][s][i];
+      if (lane < 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ref[j * 8 + lane * 2 + i] = m[j][i];
+          sum[j * 8 + lane * 2 + i] = l[j][i];
+        }
+      }
+    }
+  }
+};
+
 template <int D, int NG>
 __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
     const __grid_constant__ AttnDecodeArgs a, int rows, int groups, int ps_shift) {
@@ -293,89 +518,21 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
     const uint32_t ring_u = smem_u32(ring);
     long long to_find = t1 - t0;
 
-    // --- producer: lane i (and i + 16) finds where key i of the tile lies.  The lanes keep
-    // 32 entries of the row's block table from page tbase on; a load of more of them is
-    // used an iteration later
-    int tbase = 0, entry = -1;
-    int idx = 0, inside = 0;  // the key's page in the row, and its row in the page
-    auto look_up = [&](bool new_row) {
-      const int first = ld.tile * kTile, key = first + (lane & 15);
-      idx = ps_shift >= 0 ? key >> ps_shift : key / a.page_size;
-      inside = key - idx * a.page_size;
-      const int paged = min(kTile, ld.keys.paged - first);  // keys of the tile in pages
-      if (paged <= 0) return;
-      const int p0 = __shfl_sync(0xffffffffu, idx, 0);
-      const int p1 = __shfl_sync(0xffffffffu, idx, paged - 1);
-      if (new_row || p1 > tbase + 31) {
-        tbase = p0;
-        const int ahead = ld.keys.paged - 1 - first + (first - p0 * a.page_size);
-        const int have = ps_shift >= 0 ? ahead >> ps_shift : ahead / a.page_size;
-        entry = lane <= have ? a.block_table[(size_t)ld.row * a.max_pages + p0 + lane] : -1;
-      }
-    };
+    Copies<D> copies{a, ps_shift, lane, ring_u, live[warp]};
     bool found = false, started = false;
     auto issue = [&](int stage) {  // copies the tile that was looked up, looks up the next
-      if (found) {
-        const int key0 = ld.tile * kTile + (lane & 15);
-        const int page = __shfl_sync(0xffffffffu, entry, (idx - tbase) & 31);
-        long long at_row = -1;  // row in the pool, or in the ring
-        const bool in_ring = key0 >= ld.keys.paged;
-        if (key0 < ld.keys.all) {
-          if (in_ring)
-            at_row = (long long)ld.row * a.w + (key0 - ld.keys.paged);
-          else if ((uint32_t)page < (uint32_t)a.capacity)
-            at_row = (long long)page * a.page_size + inside;
-          else
-            atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
-        }
-        const uint32_t here = __ballot_sync(0xffffffffu, at_row >= 0);
-        const uint32_t ringed = __ballot_sync(0xffffffffu, in_ring);
-        if (lane == 0) live[warp][stage] = here;
-        constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a step
-        const int c = lane % kLanes;
-        const uint32_t dst = ring_u + stage * stage_bytes(D);
-#pragma unroll
-        for (int i = 0; i < kTile / kRows; ++i) {
-          const int key = i * kRows + lane / kLanes;
-          const long long r = __shfl_sync(0xffffffffu, at_row, key);
-          const bool ok = (here >> key) & 1, rg = (ringed >> key) & 1;
-          const size_t e = ok ? (size_t)r * D + c * 8 : 0;
-          const bf16_t* k = rg ? a.ring_k : a.k_pages;
-          const bf16_t* v = rg ? a.ring_v : a.v_pages;
-          const uint32_t to = dst + key * (D * 2) + ((c ^ (key & 7)) << 4);
-          cp_async16(to, k + e, ok ? 16 : 0);
-          cp_async16(to + kTile * D * 2, v + e, ok ? 16 : 0);
-        }
-      }
+      if (found) copies.copy(ld.row, ld.tile, ld.keys, stage);
       cp_async_commit();
       found = to_find > 0;
       if (found) {
         --to_find;
-        look_up(started ? ld.advance(a, rows, groups, cached, lane) : true);
+        const bool new_row = started ? ld.advance(a, rows, groups, cached, lane) : true;
+        copies.look_up(ld.row, ld.tile, ld.keys, new_row);
         started = true;
       }
     };
-
-    // --- consumer
-    const float scale = rsqrtf((float)D) * kLog2e;
-    uint32_t qf[NG][KS][2];
-    float o[NG][KS][4], m[NG][2], l[NG][2];
-    auto start = [&]() {
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        const int head = (cur.group * NG + j) * 8 + (lane >> 2);
-        const bf16_t* q = a.q + out_row(a, cur.row, g, head) * D + (lane & 3) * 2;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          qf[j][s][0] = head < g ? *reinterpret_cast<const uint32_t*>(q + s * 16) : 0u;
-          qf[j][s][1] = head < g ? *reinterpret_cast<const uint32_t*>(q + s * 16 + 8) : 0u;
-          o[j][s][0] = o[j][s][1] = o[j][s][2] = o[j][s][3] = 0.f;
-        }
-        m[j][0] = m[j][1] = -INFINITY;
-        l[j][0] = l[j][1] = 0.f;
-      }
-    };
-    start();
+    Heads<D, NG> heads;
+    heads.start(a, cur.row, cur.group, g, lane);
     bool began_here = cur.tile == 0;
     // the look-up leads the copy by one tile, the copy the arithmetic by S - 1
     int stage = 0;
@@ -389,136 +546,36 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
         stage = stage == S - 1 ? 0 : stage + 1;
         continue;
       }
-      const uint32_t kb = ring_u + stage * stage_bytes(D), vb = kb + kTile * D * 2;
-      const uint32_t here = live[warp][stage];
-      float x[NG][4] = {};
-      {
-        const int key = ((lane >> 3) & 1) * 8 + (lane & 7);
-        const uint32_t row_u = kb + key * (D * 2);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          uint32_t k[4];
-          ldmatrix_x4(row_u + (((s * 2 + (lane >> 4)) ^ (key & 7)) << 4), k[0], k[1], k[2], k[3]);
-#pragma unroll
-          for (int j = 0; j < NG; ++j) mma_bf16_16816(x[j], k, qf[j][s][0], qf[j][s][1]);
-        }
-      }
-      bool raise = false;
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = (lane >> 2) + (i >> 1) * 8;
-          x[j][i] = (here >> key) & 1 ? x[j][i] * scale : -INFINITY;
-          raise |= x[j][i] > m[j][i & 1] + kSlack;
-        }
-      }
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float top = fmaxf(x[j][i], x[j][i + 2]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(m[j][i], top);
-            const float c = fast_exp2(m[j][i] - finite_ref(top));
-            m[j][i] = top;
-            l[j][i] *= c;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-              o[j][s][i] *= c;
-              o[j][s][i + 2] *= c;
-            }
-          }
-        }
-      }
-      uint32_t pf[NG][2];
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        float p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = fast_exp2(x[j][i] - finite_ref(m[j][i & 1]));
-        l[j][0] += p[0] + p[2];
-        l[j][1] += p[1] + p[3];
-        pf[j][0] = transpose8x8(pack2(p[0], p[1]));
-        pf[j][1] = transpose8x8(pack2(p[2], p[3]));
-      }
-      {
-        const int key = (lane >> 4) * 8 + (lane & 7);
-        const uint32_t row_u = vb + key * (D * 2);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          uint32_t v[4];
-          ldmatrix_x4_trans(row_u + (((s * 2 + ((lane >> 3) & 1)) ^ (key & 7)) << 4), v);
-#pragma unroll
-          for (int j = 0; j < NG; ++j) mma_bf16_16816(o[j][s], v, pf[j][0], pf[j][1]);
-        }
-      }
+      heads.tile(ring_u + stage * stage_bytes(D), live[warp][stage], lane);
       stage = stage == S - 1 ? 0 : stage + 1;
 
       const bool row_end = cur.at_row_end(), last = t + 1 == t1;
-      if (row_end || last) {
-#pragma unroll
-        for (int j = 0; j < NG; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            l[j][i] += __shfl_xor_sync(0xffffffffu, l[j][i], 4);
-            l[j][i] += __shfl_xor_sync(0xffffffffu, l[j][i], 8);
-            l[j][i] += __shfl_xor_sync(0xffffffffu, l[j][i], 16);
-          }
-        if (row_end && began_here) {
-#pragma unroll
-          for (int j = 0; j < NG; ++j) {
-            float inv[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              inv[i] = inverse(l[j][i]);
-              const int head = (cur.group * NG + j) * 8 + (lane & 3) * 2 + i;
-              if (a.lse && lane < 4 && head < g)
-                a.lse[out_row(a, cur.row, g, head)] = lse_of(m[j][i], l[j][i]);
-            }
-            const int head = (cur.group * NG + j) * 8 + (lane >> 2);
-            bf16_t* out = a.o + out_row(a, cur.row, g, head) * D + (lane & 3) * 2;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) store_frag(out + s * 16, o[j][s], inv, head < g);
-          }
-        } else {
-          // a part: a tail into the ring, where nothing is in flight any more
-          const int id = began_here ? kWarps + warp : warp;
-          float* to = reinterpret_cast<float*>(ring + (began_here ? 0 : kRingBytes));
-          if (began_here) {
-            cp_async_wait<0>();
-            __syncwarp();
-          }
-#pragma unroll
-          for (int j = 0; j < NG; ++j) {
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) to[((j * KS + s) * 4 + i) * 32 + lane] = o[j][s][i];
-            if (lane < 4) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                ref_s[id][j * 8 + lane * 2 + i] = m[j][i];
-                sum_s[id][j * 8 + lane * 2 + i] = l[j][i];
-              }
-            }
-          }
-          if (lane == 0) {
-            vrow_of[id] = cur.row * groups + cur.group;
-            atomicOr(began_here ? &tails_m : &heads_m, 1u << warp);
-            if (!began_here && row_end) atomicOr(&ends_m, 1u << warp);
-          }
-        }
-        if (!last) {
-          cur.advance(a, rows, groups, cached, lane);
-          start();
-          began_here = true;
-        }
-      } else {
+      if (!row_end && !last) {
         ++cur.tile;
+        continue;
+      }
+      heads.fold();
+      if (row_end && began_here) {
+        heads.store(a, cur.row, cur.group, g, lane);
+      } else {
+        // a part: a tail into the ring, where nothing is in flight any more
+        const int id = began_here ? kWarps + warp : warp;
+        if (began_here) {
+          cp_async_wait<0>();
+          __syncwarp();
+        }
+        heads.leave(reinterpret_cast<float*>(ring + (began_here ? 0 : kRingBytes)), ref_s[id],
+                    sum_s[id], lane);
+        if (lane == 0) {
+          vrow_of[id] = cur.row * groups + cur.group;
+          atomicOr(began_here ? &tails_m : &heads_m, 1u << warp);
+          if (!began_here && row_end) atomicOr(&ends_m, 1u << warp);
+        }
+      }
+      if (!last) {
+        cur.advance(a, rows, groups, cached, lane);
+        heads.start(a, cur.row, cur.group, g, lane);
+        began_here = true;
       }
     }
     cp_async_wait<0>();
@@ -585,18 +642,8 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
 #pragma unroll 2
       for (int p = from; p < from + n; ++p) add(p);
       if (ended && !before) {
-        const int vrow = vrow_of[tail], row = vrow / groups, group = vrow - row * groups;
-        const float inv[2] = {inverse(sum[0]), inverse(sum[1])};
-        if (a.lse && lane < 4 && f0 % (KS * 4) == 0) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (group * NG * 8 + h0 + i < g)
-              a.lse[out_row(a, row, g, group * NG * 8 + h0 + i)] = lse_of(top[i], sum[i]);
-        }
-        const int head = group * NG * 8 + f0 / (KS * 4) * 8 + (lane >> 2);
-        bf16_t* out = a.o + out_row(a, row, g, head) * D + f0 / 4 % KS * 16 + (lane & 3) * 2;
-        store_frag(out, acc, inv, head < g);
-        store_frag(out + 16, acc + 4, inv, head < g);
+        const int vrow = vrow_of[tail], row = vrow / groups;
+        store_unit<D, NG>(a, row, vrow - row * groups, g, f0, acc, top, sum, lane);
       } else {  // a part for the second kernel
         float* out = block_part(a.ws, blockIdx.x, before ? 0 : 1, PF);
 #pragma unroll
@@ -678,10 +725,158 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
   if (head < g) store_out<D>(a, out_row(a, row, g, head), dim, acc, top, sum);
 }
 
+// The same for rows that cannot be long: a block, or a cluster of blocks, per row and group
+// of heads, with equal contiguous shares of the row's tiles per warp.  No scan over other
+// rows, no workspace and no second kernel: a block's warps meet in its shared memory, a
+// cluster's blocks read one another's.
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  float x;
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
+  return x;
+}
+
+template <int D, int NG>
+__global__ void __launch_bounds__(kRowWarps * 32, NG == 1 ? 3 : 2) attn_decode_row_kernel(
+    const __grid_constant__ AttnDecodeArgs a, int groups, int ps_shift) {
+  constexpr int S = stages(D), KS = D / 16, NF = frags(D, NG), W = kRowWarps, H = NG * 8;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint32_t live[W][S];
+  __shared__ float ref_s[W + 1][H], sum_s[W + 1][H];  // of the warps, and of the block
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.Hq / a.Hkv;
+  const int blocks = cluster_size(), rank = blockIdx.x % blocks;
+  const int vrow = blockIdx.x / blocks, row = vrow / groups, group = vrow - row * groups;
+  const int len = a.seq_lens[row];
+  const Keys keys = keys_of(a, len, ring_pos(a, row));
+  if (tid == 0 && rank == 0 && keys.paged != len) atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
+  uint8_t* ring = smem + warp * kRingBytes;
+  const uint32_t ring_u = smem_u32(ring);
+  Heads<D, NG> heads;
+  heads.start(a, row, group, g, lane);
+  {
+    const uint32_t tiles = (keys.all + kTile - 1u) / kTile;  // below 2^27, of up to 32 warps
+    const uint32_t me = rank * W + warp, all = blocks * W;
+    const int t0 = me * tiles / all, t1 = (me + 1) * tiles / all;
+    Copies<D> copies{a, ps_shift, lane, ring_u, live[warp]};
+    int stage = 0;
+    for (int t = t0 - S; t < t1; ++t) {
+      if (t >= t0) {
+        cp_async_wait<S - 2>();
+        __syncwarp();
+      }
+      const int next = t + S;  // the look-up leads the copy by one tile, as in the stream
+      if (next > t0 && next - 1 < t1)
+        copies.copy(row, next - 1, keys, stage == 0 ? S - 1 : stage - 1);
+      cp_async_commit();
+      if (next < t1) copies.look_up(row, next, keys, next == t0);
+      if (t >= t0) heads.tile(ring_u + stage * stage_bytes(D), live[warp][stage], lane);
+      stage = stage == S - 1 ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+  }
+  heads.fold();
+  heads.leave(reinterpret_cast<float*>(ring), ref_s[warp], sum_s[warp], lane);
+  __syncthreads();
+  // --- the block's warps, eight fragments a warp at a time; the result over warp 0's part
+  constexpr int kUnits = NF / 8;
+  for (int u = warp; u < kUnits; u += W) {
+    const int f0 = u * 8, h0 = f0 / (KS * 4) * 8 + (lane & 3) * 2;
+    float top[2], sum[2] = {}, acc[8] = {};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      top[i] = ref_s[0][h0 + i];
+      for (int p = 1; p < W; ++p) top[i] = fmaxf(top[i], ref_s[p][h0 + i]);
+    }
+#pragma unroll
+    for (int p = 0; p < W; ++p) {
+      const float* x = reinterpret_cast<const float*>(smem + p * kRingBytes) + f0 * 32 + lane;
+      float w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i] = fast_exp2(ref_s[p][h0 + i] - finite_ref(top[i]));
+        sum[i] += sum_s[p][h0 + i] * w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += x[i * 32] * w[i & 1];
+    }
+    if (blocks == 1) {
+      store_unit<D, NG>(a, row, group, g, f0, acc, top, sum, lane);
+    } else {
+      float* x = reinterpret_cast<float*>(smem) + f0 * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i * 32] = acc[i];
+      if (lane < 4 && f0 % (KS * 4) == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ref_s[W][h0 + i] = top[i];
+          sum_s[W][h0 + i] = sum[i];
+        }
+      }
+    }
+  }
+  if (blocks == 1) return;
+  // --- the cluster's blocks: unit u by block u % blocks
+  cluster_sync();
+  for (int u = rank + blocks * warp; u < kUnits; u += blocks * W) {
+    const int f0 = u * 8, h0 = f0 / (KS * 4) * 8 + (lane & 3) * 2;
+    const uint32_t ref_u = smem_u32(&ref_s[W][h0]), sum_u = smem_u32(&sum_s[W][h0]);
+    const uint32_t x_u = smem_u32(smem) + (f0 * 32 + lane) * 4;
+    float ref[2][8], sum[2] = {}, top[2] = {-INFINITY, -INFINITY}, acc[8] = {};
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ref[i][p] = p < blocks ? ld_cluster(ref_u + 4 * i, p) : -INFINITY;
+        top[i] = fmaxf(top[i], ref[i][p]);
+      }
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      if (p >= blocks) break;
+      float w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i] = fast_exp2(ref[i][p] - finite_ref(top[i]));
+        sum[i] += ld_cluster(sum_u + 4 * i, p) * w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += ld_cluster(x_u + i * 128, p) * w[i & 1];
+    }
+    store_unit<D, NG>(a, row, group, g, f0, acc, top, sum, lane);
+  }
+  cluster_sync();  // no block leaves while another reads its shared memory
+}
+
+// Blocks of a cluster per row where the row kernel takes a call, else 0 (the stream).  The
+// actual lengths are on the device, so the rule goes by what a row may hold: at most 16
+// tiles a warp, or 6 where even clusters of 8 leave SMs idle.  Rows 30 to 100 % full, row
+// kernel against stream (us): 8 rows of 58 tiles 7.0 / 9.4, of 241 tiles 11.4 / 10.1;
+// 32 rows of 126 tiles 9.1 / 11.9; 128 rows of 15 tiles 7.0 / 11.5, of 61 tiles 13.3 / 16.3,
+// of 246 tiles 37.4 / 33.0; 512 rows of 16 tiles 12.9 / 17.2, of 63 tiles 32.0 / 32.3, of
+// 249 tiles 101 / 87.
+int row_cluster(long long vrows, long long row_tiles) {
+  int c = 1;
+  while (c < 8 && vrows * c * 2 <= 152 * 3) c *= 2;
+  const int most = vrows * c >= 152 ? 16 : 6;
+  return row_tiles <= c * kRowWarps * most ? c : 0;
+}
+
 template <int D, int NG>
 cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s) {
   constexpr int kWarps = warps_of(NG);
   constexpr int smem = kWarps * warp_bytes(D, NG) + kCachedRows * (int)sizeof(Keys);
+  constexpr int row_smem = kRowWarps * kRingBytes;
   static int nsm[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -692,31 +887,45 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(attn_decode_kernel<D, NG>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attn_decode_row_kernel<D, NG>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, row_smem);
     if (e != cudaSuccess) return e;
     nsm[dev & 63] = n < kMaxBlocks ? n : kMaxBlocks;
   }
-  // no more blocks than tiles could need
-  const long long keys = (long long)a.max_pages * a.page_size + a.w;
-  const long long most = (long long)rows * groups * ((keys + kTile - 1) / kTile);
-  const long long want = (most + kWarps - 1) / kWarps;
-  const int blocks = (int)(want < nsm[dev & 63] ? want : nsm[dev & 63]);
   int shift = -1;
   if ((a.page_size & (a.page_size - 1)) == 0)
     for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const long long vrows = (long long)rows * groups;
+  const long long row_tiles = ((long long)a.max_pages * a.page_size + a.w + kTile - 1) / kTile;
+  const int cluster = row_cluster(vrows, row_tiles);
+  if (cluster > 0) {
+    cfg.gridDim = dim3((unsigned)(vrows * cluster));
+    cfg.blockDim = dim3(kRowWarps * 32);
+    cfg.dynamicSmemBytes = row_smem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, attn_decode_row_kernel<D, NG>, a, groups, shift);
+  }
+  // no more blocks than tiles could need
+  const long long want = (vrows * row_tiles + kWarps - 1) / kWarps;
+  const int blocks = (int)(want < nsm[dev & 63] ? want : nsm[dev & 63]);
   count_launches(2);
   attn_decode_kernel<D, NG><<<blocks, kWarps * 32, smem, s>>>(a, rows, groups, shift);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join's blocks come up while the first kernel runs and wait for its results
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, frags(D, NG) * 32 / kJoinThreads);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, NG>, a, rows, groups);
 }
 
