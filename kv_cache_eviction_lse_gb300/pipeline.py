@@ -10,6 +10,8 @@ method happens here, only call sequencing and buffer management.
   KVpop target    (c4)      lse (causal self-attention) -> future_sum -> top-k per budget
                             -> compact
   KVzap           (c5)      surrogate (+ fused threshold) -> compact
+  decode          (c7)      [rope ->] surrogate -> decode step [-> attention over the
+                            row's pages and window ring]
 """
 from __future__ import annotations
 
@@ -384,9 +386,14 @@ class DecodePipeline:
     """c7: one decode step of `batch` sequences per call: the KVzap-Linear score of the
     arriving token (the surrogate over the batch's hidden states), then the window-
     boundary decision and append (kvs_decode_step).  State (ring, pages, positions)
-    lives on the device and advances with every step; `reset` starts over."""
+    lives on the device and advances with every step; `reset` starts over.
 
-    def __init__(self, wl: Workload, x: dict, max_steps=4096):
+    attention: the step a model takes, with the arriving tokens' queries x["q"]
+    [L][H_q][B][d]: queries and keys are rotated at their positions (kvs_rope; rope_base is
+    the base of the frequencies, by default that of Llama-3), the rotated key is decided and
+    stored, and the new token attends over its rows' pages and ring (kvs_attn_decode)."""
+
+    def __init__(self, wl: Workload, x: dict, max_steps=4096, attention=False, rope_base=5e5):
         self.wl, self.x = wl, x
         dev = x["h"].device
         L, H, B, d, w = x["h"].shape[0], wl.H_kv, wl.batch, wl.d, wl.w
@@ -405,6 +412,16 @@ class DecodePipeline:
         self.next_page = torch.zeros(1, dtype=torch.int32, device=dev)
         self.block_table = torch.full((L, H, B, self.max_pages), -1, dtype=torch.int32, device=dev)
         self.seq_lens = torch.zeros((L, H, B), dtype=torch.int32, device=dev)
+        self.attention = attention
+        if attention:
+            if w < 1:
+                raise ValueError("attention needs a window: the new token attends to itself")
+            self.inv_freq = rope_base ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)
+            self.q_rot = torch.empty_like(x["q"])
+            self.k_rot = torch.empty_like(x["k"])
+            self.o = torch.empty_like(x["q"])
+            self.lse = _empty((L, wl.H_q, B), torch.float32, dev)
+            self.aws = _empty((C.kvs_attn_decode_workspace_size(self.dm, B),), torch.uint8, dev)
         self.reset()
 
     def reset(self):
@@ -418,19 +435,35 @@ class DecodePipeline:
         wl, x = self.wl, self.x
         C.kvs_surrogate(self.dm, x["h"], self.B, x["W"], x["b"], self.score)
 
+    def _rotate(self):
+        wl, x = self.wl, self.x
+        C.kvs_rope(self.dm, self.B, self.pos, wl.d, self.inv_freq, False, x["q"], self.q_rot, x["k"],
+                   self.k_rot)
+
+    def _attend(self):
+        wl = self.wl
+        C.kvs_attn_decode(self.dm, self.B, self.q_rot, wl.page_size, self.k_pages, self.v_pages,
+                          self.capacity, self.block_table, self.max_pages, self.seq_lens, wl.w,
+                          self.pos, self.ring_k, self.ring_v, self.o, self.lse, self.aws,
+                          self.aws.numel())
+
     def _decide(self):
         wl, x = self.wl, self.x
-        C.kvs_decode_step(self.dm, self.B, wl.w, self.pos, self.score, x["k"], x["v"],
+        k = self.k_rot if self.attention else x["k"]
+        C.kvs_decode_step(self.dm, self.B, wl.w, self.pos, self.score, k, x["v"],
                           self.ring_score, self.ring_k, self.ring_v, wl.tau, wl.page_size,
                           self.k_pages, self.v_pages, self.capacity, self.next_page,
                           self.block_table, self.max_pages, self.seq_lens)
 
     def stages(self):
-        return [("kvs_surrogate", self._score), ("kvs_decode_step", self._decide)]
+        st = [("kvs_surrogate", self._score), ("kvs_decode_step", self._decide)]
+        if self.attention:
+            st = [("kvs_rope", self._rotate)] + st + [("kvs_attn_decode", self._attend)]
+        return st
 
     def step(self):
-        self._score()
-        self._decide()
+        for _, fn in self.stages():
+            fn()
 
 
 def make_pipeline(wl: Workload, x: dict, **kw):

@@ -361,6 +361,17 @@ def _generate_decode(wl: Workload, layers, device):
     return dict(h=h, W=W, b=b, k=k, v=v)
 
 
+def decode_queries(wl: Workload, layers=None, device="cpu") -> torch.Tensor:
+    """c7: the arriving tokens' queries [L][H_q][B][d], N(0,1), from generators of their own
+    (the other inputs of the workload do not depend on whether they are made)."""
+    parts = []
+    for l in _layers(wl, layers):
+        gen = torch.Generator(device=device)
+        gen.manual_seed(wl.seed(l) + 500_000_000)
+        parts.append(_bf16(_randn(gen, (wl.H_q, wl.batch, wl.d), device)))
+    return torch.stack(parts)
+
+
 def random_kv_inputs(L, H_kv, H_q, d, T, n_tail, n_q, seed, device="cpu", scale=1.0,
                      D_h=0):
     """Generic seeded inputs of arbitrary (ragged) shape for edge-case tests."""

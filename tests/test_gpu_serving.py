@@ -666,3 +666,52 @@ def test_pruning_decode_with_attention(C):
                 tol = 2.0 ** -8 * np.abs(a @ Vr) + (2.0 ** -8 + 2e-5) * (a @ np.abs(Vr))
                 assert (np.abs(f64(o)[0, hq, b] - a @ Vr) <= tol).all()
     assert C.kvs_device_error(clear=True) == 0
+
+
+def test_decode_pipeline_with_attention(C):
+    """The decode pipeline's own path: rotated keys in ring and pages, decided by the
+    surrogate, attended over; a captured step replays like the eager one."""
+    from kv_cache_eviction_lse_gb300 import pipeline, workloads as W
+    wl = W.WORKLOADS["c7"].scaled(L=2, H_q=4, H_kv=2, D_h=512, batch=3, w=6, tau=-4.0)
+    x = W.generate(wl, device="cuda")
+    x["q"] = W.decode_queries(wl, device="cuda")
+    p = pipeline.make_pipeline(wl, x, max_steps=64, attention=True)
+    f, steps = p.inv_freq.numpy(), 30
+    outs, keys = [], []
+    for t in range(steps):
+        p.step()
+        torch.cuda.synchronize()
+        outs.append((p.o.clone(), p.lse.clone()))
+        check_rotated(p.q_rot, x["q"], np.full(wl.batch, t), wl.d, f, False, "q")
+        check_rotated(p.k_rot, x["k"], np.full(wl.batch, t), wl.d, f, False, "k")
+        assert torch.equal(p.ring_k[:, :, :, t % wl.w], p.k_rot)
+        keys.append(p.k_rot.clone())
+        if t in (0, 4, 5, 6, 7, steps - 1):
+            want, lse, spread = O.attn_decode(
+                f64(p.q_rot), f64(p.k_pages), f64(p.v_pages), wl.page_size,
+                p.block_table.cpu().numpy(), p.seq_lens.cpu().numpy(), f64(p.ring_k), f64(p.ring_v),
+                p.pos.cpu().numpy())
+            assert np.isfinite(lse).all()
+            assert np.abs(p.lse.cpu().double().numpy() - lse).max() <= 1e-4
+            err = np.abs(f64(p.o) - want)
+            assert (err <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 1e-4) * spread).all()
+    assert C.kvs_device_error(clear=True) == 0
+    # rows that pass the threshold hold every token that left the ring, rotated at its own place
+    kept = (p.score >= wl.tau).cpu().numpy()
+    n = p.seq_lens.cpu().numpy()
+    assert 0 < kept.sum() < kept.size and np.array_equal(n, np.where(kept, steps - wl.w, 0))
+    for r in zip(*np.nonzero(kept)):
+        ids = p.block_table[r][: -(-int(n[r]) // wl.page_size)].long()
+        got = p.k_pages[ids].reshape(-1, wl.d)[: int(n[r])]
+        assert torch.equal(got, torch.stack([k[r] for k in keys[: int(n[r])]]))
+    p.reset()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.step()
+    p.reset()
+    for t in range(steps):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(p.o, outs[t][0]) and torch.equal(p.lse, outs[t][1]), t
+    with pytest.raises(ValueError):
+        pipeline.make_pipeline(wl.scaled(w=0), x, attention=True)
