@@ -35,7 +35,7 @@ constexpr int kErrAttnDecode = 9;  // a length or page id out of range
 constexpr int kTile = 16;        // keys
 constexpr int kMaxBlocks = 160;  // of the persistent grid; sizes the workspace
 constexpr int kMaxWarps = 16;    // of a block
-constexpr int kRowWarps = 4;     // of a block that has one row
+constexpr int kMaxCluster = 8;   // blocks that share a row
 constexpr int kJoinThreads = 256;
 constexpr int kMaxChunks = 256;  // of rows, in the scan of their tiles
 constexpr int kCachedRows = 512; // whose lengths a block keeps in shared memory
@@ -746,10 +746,10 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
   return x;
 }
 
-template <int D, int NG>
-__global__ void __launch_bounds__(kRowWarps * 32, NG == 1 ? 3 : 2) attn_decode_row_kernel(
+template <int D, int NG, int W>
+__global__ void __launch_bounds__(W * 32, (NG == 1 ? 12 : 8) / W) attn_decode_row_kernel(
     const __grid_constant__ AttnDecodeArgs a, int groups, int ps_shift) {
-  constexpr int S = stages(D), KS = D / 16, NF = frags(D, NG), W = kRowWarps, H = NG * 8;
+  constexpr int S = stages(D), KS = D / 16, NF = frags(D, NG), H = NG * 8;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t live[W][S];
   __shared__ float ref_s[W + 1][H], sum_s[W + 1][H];  // of the warps, and of the block
@@ -858,25 +858,47 @@ __global__ void __launch_bounds__(kRowWarps * 32, NG == 1 ? 3 : 2) attn_decode_r
   cluster_sync();  // no block leaves while another reads its shared memory
 }
 
-// Blocks of a cluster per row where the row kernel takes a call, else 0 (the stream).  The
-// actual lengths are on the device, so the rule goes by what a row may hold: at most 16
-// tiles a warp, or 6 where even clusters of 8 leave SMs idle.  Rows 30 to 100 % full, row
-// kernel against stream (us): 8 rows of 58 tiles 7.0 / 9.4, of 241 tiles 11.4 / 10.1;
-// 32 rows of 126 tiles 9.1 / 11.9; 128 rows of 15 tiles 7.0 / 11.5, of 61 tiles 13.3 / 16.3,
-// of 246 tiles 37.4 / 33.0; 512 rows of 16 tiles 12.9 / 17.2, of 63 tiles 32.0 / 32.3, of
-// 249 tiles 101 / 87.
-int row_cluster(long long vrows, long long row_tiles) {
+// Warps of a block and blocks of a cluster per row where the row kernel takes a call, else
+// no warps (the stream).  The actual lengths are on the device, so the rule goes by what a
+// row may hold: at most 16 tiles a warp, or 6 where even clusters of 8 leave SMs idle.  Rows
+// 30 to 100 % full, row kernel against stream (us): 8 rows of 58 tiles 7.0 / 9.4, of 241
+// tiles 11.4 / 10.1; 32 rows of 126 tiles 9.1 / 11.9; 128 rows of 15 tiles 7.0 / 11.5, of 61
+// tiles 13.3 / 16.3, of 246 tiles 37.4 / 33.0; 512 rows of 16 tiles 12.9 / 17.2, of 63 tiles
+// 32.0 / 32.3, of 249 tiles 101 / 87.  Where there are enough short rows, blocks of two
+// warps, six on an SM, overlap one another's starts and joins better than three of four
+// warps: 2048 rows of 15 tiles 35.4 / 37.9, 16384 rows 203 / 239, 2048 rows of 4 tiles 16.7 /
+// 23.2; of 38 tiles 55.1 / 53.5.
+struct RowShape { int warps, cluster; };
+RowShape row_shape(long long vrows, long long row_tiles) {
+  if (vrows >= 152 * 6 && row_tiles <= 2 * 16) return {2, 1};
   int c = 1;
-  while (c < 8 && vrows * c * 2 <= 152 * 3) c *= 2;
+  while (c < kMaxCluster && vrows * c * 2 <= 152 * 3) c *= 2;
   const int most = vrows * c >= 152 ? 16 : 6;
-  return row_tiles <= c * kRowWarps * most ? c : 0;
+  return {row_tiles <= c * 4 * most ? 4 : 0, c};
+}
+
+template <int D, int NG, int W>
+cudaError_t launch_rows(const AttnDecodeArgs& a, long long vrows, int cluster, int groups, int shift,
+                        cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(vrows * cluster));
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = W * kRingBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, attn_decode_row_kernel<D, NG, W>, a, groups, shift);
 }
 
 template <int D, int NG>
 cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s) {
   constexpr int kWarps = warps_of(NG);
   constexpr int smem = kWarps * warp_bytes(D, NG) + kCachedRows * (int)sizeof(Keys);
-  constexpr int row_smem = kRowWarps * kRingBytes;
   static int nsm[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -888,32 +910,22 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
       e = cudaFuncSetAttribute(attn_decode_kernel<D, NG>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_decode_row_kernel<D, NG>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, row_smem);
+      e = cudaFuncSetAttribute(attn_decode_row_kernel<D, NG, 4>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kRingBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attn_decode_row_kernel<D, NG, 2>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kRingBytes);
     if (e != cudaSuccess) return e;
     nsm[dev & 63] = n < kMaxBlocks ? n : kMaxBlocks;
   }
   int shift = -1;
   if ((a.page_size & (a.page_size - 1)) == 0)
     for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const long long vrows = (long long)rows * groups;
   const long long row_tiles = ((long long)a.max_pages * a.page_size + a.w + kTile - 1) / kTile;
-  const int cluster = row_cluster(vrows, row_tiles);
-  if (cluster > 0) {
-    cfg.gridDim = dim3((unsigned)(vrows * cluster));
-    cfg.blockDim = dim3(kRowWarps * 32);
-    cfg.dynamicSmemBytes = row_smem;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    count_launches(1);
-    return cudaLaunchKernelEx(&cfg, attn_decode_row_kernel<D, NG>, a, groups, shift);
-  }
+  const RowShape shape = row_shape(vrows, row_tiles);
+  if (shape.warps == 4) return launch_rows<D, NG, 4>(a, vrows, shape.cluster, groups, shift, s);
+  if (shape.warps == 2) return launch_rows<D, NG, 2>(a, vrows, shape.cluster, groups, shift, s);
   // no more blocks than tiles could need
   const long long want = (vrows * row_tiles + kWarps - 1) / kWarps;
   const int blocks = (int)(want < nsm[dev & 63] ? want : nsm[dev & 63]);
@@ -922,8 +934,13 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join's blocks come up while the first kernel runs and wait for its results
+  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, frags(D, NG) * 32 / kJoinThreads);
   cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, NG>, a, rows, groups);

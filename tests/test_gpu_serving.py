@@ -449,6 +449,7 @@ ATTEND = {
     "long row": dict(L=1, Hq=4, H=1, B=1, d=128, ps=16, n=5003),
     "long among short": dict(L=1, Hq=8, H=2, B=6, d=64, ps=16, n=[3, 4000, 0, 1, 0, 700]),
     "many rows": dict(L=3, Hq=32, H=16, B=40, d=64, ps=16, n=np.arange(40) % 19),
+    "many rows, groups of 9": dict(L=1, Hq=144, H=16, B=60, d=128, ps=16, n=np.arange(60) % 37),
     "large logits": dict(L=1, Hq=4, H=2, B=2, d=128, ps=16, n=[300, 40], scale=30.0),
 }
 
