@@ -452,8 +452,8 @@ kvs_status kvs_compact_paged_multi(const kvs_dims* dims, const kvs_bf16* k, cons
  *                              before the call returns (a captured graph keeps the values)
  *   q, q_out   [L][H_q][N][d]  bf16; both NULL to leave queries out
  *   k, k_out   [L][H_kv][N][d] bf16; both NULL to leave keys out
- * An output is its input (rotation in place) or does not overlap it.  Requires rot_dim a
- * multiple of 16 with 0 <= rot_dim <= d.
+ * An output is its input (rotation in place) or does not overlap it; no two tensors overlap
+ * otherwise.  Requires rot_dim a multiple of 16 with 0 <= rot_dim <= d.
  * ------------------------------------------------------------------------------- */
 kvs_status kvs_rope(const kvs_dims* dims, int32_t N, const int32_t* pos, int32_t rot_dim,
                     const double* inv_freq, int32_t interleaved, const kvs_bf16* q,
@@ -491,7 +491,7 @@ kvs_status kvs_rope(const kvs_dims* dims, int32_t N, const int32_t* pos, int32_t
  *   seq_lens, seq_lens_out [L][H_kv][B] int32; may be the same
  *   ws        scratch of kvs_append_paged_workspace_size() bytes; calls that may overlap
  *             on the GPU need their own
- * No two rows may own the same page.
+ * No two rows may own the same page, and no tensors overlap but where said.
  * ------------------------------------------------------------------------------- */
 size_t kvs_append_paged_workspace_size(const kvs_dims* dims, int32_t B);
 kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const int32_t* tok_start,

@@ -880,6 +880,9 @@ RowShape row_shape(long long vrows, long long row_tiles) {
 template <int D, int NG, int W>
 cudaError_t launch_rows(const AttnDecodeArgs& a, long long vrows, int cluster, int groups, int shift,
                         cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_row_kernel<D, NG, W>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, W * kRingBytes);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(vrows * cluster));
   cfg.blockDim = dim3(W * 32);
@@ -903,20 +906,10 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (!nsm[dev & 63]) {
-    int n = 0;
-    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_decode_kernel<D, NG>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_decode_row_kernel<D, NG, 4>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kRingBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_decode_row_kernel<D, NG, 2>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kRingBytes);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!nsm[dev]) {
+    e = cudaDeviceGetAttribute(&nsm[dev], cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    nsm[dev & 63] = n < kMaxBlocks ? n : kMaxBlocks;
   }
   int shift = -1;
   if ((a.page_size & (a.page_size - 1)) == 0)
@@ -928,7 +921,11 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
   if (shape.warps == 2) return launch_rows<D, NG, 2>(a, vrows, shape.cluster, groups, shift, s);
   // no more blocks than tiles could need
   const long long want = (vrows * row_tiles + kWarps - 1) / kWarps;
-  const int blocks = (int)(want < nsm[dev & 63] ? want : nsm[dev & 63]);
+  const int sms = nsm[dev] < kMaxBlocks ? nsm[dev] : kMaxBlocks;
+  const int blocks = (int)(want < sms ? want : sms);
+  e = cudaFuncSetAttribute(attn_decode_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem);
+  if (e != cudaSuccess) return e;
   count_launches(2);
   attn_decode_kernel<D, NG><<<blocks, kWarps * 32, smem, s>>>(a, rows, groups, shift);
   e = cudaGetLastError();

@@ -318,6 +318,59 @@ def test_append_taken_back(C):
         assert torch.equal(again[n], plain[n]), n
 
 
+def test_append_and_attend_captured_and_replayed(C):
+    """A captured pair of calls with the state in place: every replay appends the next token
+    behind the last and attends over all of them, as the same calls do without a graph; on
+    the legacy default stream too."""
+    L, Hq, H, B, d, ps, steps = 1, 8, 2, 3, 128, 4, 11
+    gen = torch.Generator().manual_seed(21)
+    dm, f, mp = C.dims(L, Hq, H, d), freqs(d), 8
+    rnd = lambda *s: torch.randn(*s, generator=gen).to(torch.bfloat16)  # noqa: E731
+    toks = [(rnd(L, Hq, B, d), rnd(L, H, B, d), rnd(L, H, B, d)) for _ in range(steps)]
+    runs = {}
+    for how in ("graph", "eager", "default stream"):
+        g = dict(kp=torch.zeros(L * H * B * mp, ps, d, dtype=torch.bfloat16, device="cuda"),
+                 vp=torch.zeros(L * H * B * mp, ps, d, dtype=torch.bfloat16, device="cuda"),
+                 bt=torch.full((L, H, B, mp), -1, dtype=torch.int32, device="cuda"),
+                 sl=torch.zeros(L, H, B, dtype=torch.int32, device="cuda"),
+                 nxt=torch.zeros(1, dtype=torch.int32, device="cuda"),
+                 pos=torch.full((B,), 100, dtype=torch.int32, device="cuda"))
+        q, k, v = (t.cuda() for t in toks[0])
+        qo, o = torch.empty_like(q), torch.empty_like(q)
+        na, nd = C.kvs_append_paged_workspace_size(dm, B), C.kvs_attn_decode_workspace_size(dm, B)
+        wa = torch.empty(na, dtype=torch.uint8, device="cuda")
+        wd = torch.empty(nd, dtype=torch.uint8, device="cuda")
+        stream = 0 if how == "default stream" else None
+
+        def step():
+            C.kvs_append_paged(dm, B, B, None, g["pos"], d, f, False, q, qo, k, v, ps, g["kp"],
+                               g["vp"], len(g["kp"]), g["nxt"], g["nxt"], g["bt"], mp, g["sl"],
+                               g["sl"], wa, na, stream=stream)
+            C.kvs_attn_decode(dm, B, qo, ps, g["kp"], g["vp"], len(g["kp"]), g["bt"], mp, g["sl"], 0,
+                              None, None, None, o, None, wd, nd, stream=stream)
+        if how == "graph":
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        outs = []
+        for t in toks:
+            for x, y in zip((q, k, v), t):
+                x.copy_(y)
+            torch.cuda.synchronize()
+            graph.replay() if how == "graph" else step()
+            torch.cuda.synchronize()
+            g["pos"] += 1
+            outs.append(o.cpu())
+        assert (g["sl"] == steps).all() and int(g["nxt"]) == L * H * B * -(-steps // ps)
+        runs[how] = outs
+    assert C.kvs_device_error(clear=True) == 0
+    for how in ("eager", "default stream"):
+        assert all(torch.equal(a, b) for a, b in zip(runs["graph"], runs[how])), how
+    # the first token attends to itself alone
+    first = toks[0][2].repeat_interleave(Hq // H, 1)
+    assert torch.equal(runs["graph"][0], first)
+
+
 def test_offsets_past_32_bits(C):
     """A pool of over 2^31 elements with the row's pages at its end: appended there, and read
     back by the attention."""
