@@ -413,45 +413,53 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
   const int g = a.Hq / a.Hkv;
   asm volatile("griddepcontrol.launch_dependents;");
 
-  // --- tiles of all rows, by chunks of rows; kScan chunks' loads at a time, from rows that
-  // are there, before the first use
-  constexpr int kScan = 4;
-  const int per = 32 * ((rows + 32 * kMaxChunks - 1) / (32 * kMaxChunks));
-  const int chunks = (rows + per - 1) / per;
-  const int b_step = a.w > 0 ? kWarps * per % a.B : 0;
-  for (int c0 = warp; c0 < chunks; c0 += kScan * kWarps) {
-    long long sum[kScan] = {};
-    for (int i = lane; i < per; i += 32) {
-      int len[kScan], pos[kScan];
-      int b = a.w > 0 ? (c0 * per + i) % a.B : 0;  // sequence of the row
-#pragma unroll
-      for (int u = 0; u < kScan; ++u) {
-        len[u] = a.seq_lens[min((c0 + u * kWarps) * per + i, rows - 1)];
-        pos[u] = a.w > 0 ? a.pos[b] : 0;
-        b += b_step;
-        if (b >= a.B) b -= a.B;
-      }
-#pragma unroll
-      for (int u = 0; u < kScan; ++u) {
-        const int r = (c0 + u * kWarps) * per + i;
-        const Keys k = keys_of(a, len[u], pos[u]);
-        if (r < min(rows, kCachedRows)) cached[r] = k;
-        // a row has fewer than 2^27 tiles: 32 of them add up in 32 bits
-        sum[u] += __reduce_add_sync(0xffffffffu, r < rows ? (k.all + kTile - 1u) / kTile : 0u);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kScan; ++u)
-      if (lane == 0 && c0 + u * kWarps < chunks) chunk_tiles[c0 + u * kWarps] = sum[u];
-  }
   if (tid == 0) heads_m = ends_m = tails_m = 0;
-  __syncthreads();
-  // --- every warp for itself (a second barrier would cost more): the sum over the chunks,
-  // its share of the stream, and the row where that begins
+  const int per = 32 * ((rows + 32 * kMaxChunks - 1) / (32 * kMaxChunks));  // rows of a chunk
+  const int chunks = (rows + per - 1) / per;
   const int each = (chunks + 31) / 32;  // chunks of a lane
-  long long lane_tiles = 0;
-  for (int i = 0; i < each; ++i)
-    if (lane * each + i < chunks) lane_tiles += chunk_tiles[lane * each + i];
+  const bool few = rows <= 32;          // then every warp has all lengths in its lanes
+  Keys lane_keys = {0, 0};
+  long long lane_tiles = 0;             // of the lane's row, or its chunks
+  if (few) {
+    if (lane < rows) lane_keys = keys_of(a, a.seq_lens[lane], ring_pos(a, lane));
+    lane_tiles = (lane_keys.all + kTile - 1) / kTile;
+    __syncthreads();
+  } else {
+    // --- tiles of all rows, by chunks of rows; kScan chunks' loads at a time, from rows that
+    // are there, before the first use
+    constexpr int kScan = 4;
+    const int b_step = a.w > 0 ? kWarps * per % a.B : 0;
+    for (int c0 = warp; c0 < chunks; c0 += kScan * kWarps) {
+      long long sum[kScan] = {};
+      for (int i = lane; i < per; i += 32) {
+        int len[kScan], pos[kScan];
+        int b = a.w > 0 ? (c0 * per + i) % a.B : 0;  // sequence of the row
+#pragma unroll
+        for (int u = 0; u < kScan; ++u) {
+          len[u] = a.seq_lens[min((c0 + u * kWarps) * per + i, rows - 1)];
+          pos[u] = a.w > 0 ? a.pos[b] : 0;
+          b += b_step;
+          if (b >= a.B) b -= a.B;
+        }
+#pragma unroll
+        for (int u = 0; u < kScan; ++u) {
+          const int r = (c0 + u * kWarps) * per + i;
+          const Keys k = keys_of(a, len[u], pos[u]);
+          if (r < min(rows, kCachedRows)) cached[r] = k;
+          // a row has fewer than 2^27 tiles: 32 of them add up in 32 bits
+          sum[u] += __reduce_add_sync(0xffffffffu, r < rows ? (k.all + kTile - 1u) / kTile : 0u);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kScan; ++u)
+        if (lane == 0 && c0 + u * kWarps < chunks) chunk_tiles[c0 + u * kWarps] = sum[u];
+    }
+    __syncthreads();
+    for (int i = 0; i < each; ++i)
+      if (lane * each + i < chunks) lane_tiles += chunk_tiles[lane * each + i];
+  }
+  // --- every warp for itself (a second barrier would cost more): the sum over the lanes,
+  // its share of the stream, and the row where that begins
   long long lanes_incl = lane_tiles;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -479,32 +487,35 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
     const long long u0 = groups == 1 ? t0 : t0 / groups;  // in tiles of one group
     const int l0 = __ffs(__ballot_sync(0xffffffffu, lanes_incl > u0)) - 1;
     long long rel = u0 - __shfl_sync(0xffffffffu, lanes_incl - lane_tiles, l0);
-    int chunk = l0 * each;
-    while (rel >= chunk_tiles[chunk]) rel -= chunk_tiles[chunk++];
     Cursor ld;
-    ld.base = chunk * per;
-    uint32_t before;
-    for (;;) {
-      ld.fetch(a, rows, cached, lane);
-      const uint32_t mine = (ld.mine.all + kTile - 1) / kTile;
-      uint32_t incl = mine;  // 32 rows of fewer than 2^27 tiles
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, incl > rel);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        ld.enter(ld.base + l);
-        before = __shfl_sync(0xffffffffu, incl - mine, l);
-        break;
-      }
-      rel -= __shfl_sync(0xffffffffu, incl, 31);
-      ld.base += 32;
-    }
     ld.group = 0;
-    ld.tile = (int)(rel - before);
+    if (few) {
+      ld.base = 0;
+      ld.mine = lane_keys;
+      ld.enter(l0);
+    } else {
+      int chunk = l0 * each;
+      while (rel >= chunk_tiles[chunk]) rel -= chunk_tiles[chunk++];
+      for (ld.base = chunk * per;; ld.base += 32) {
+        ld.fetch(a, rows, cached, lane);
+        const uint32_t mine = (ld.mine.all + kTile - 1) / kTile;
+        uint32_t incl = mine;  // 32 rows of fewer than 2^27 tiles
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, incl > rel);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          ld.enter(ld.base + l);
+          rel -= __shfl_sync(0xffffffffu, incl - mine, l);
+          break;
+        }
+        rel -= __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    ld.tile = (int)rel;
     if (groups > 1) {  // the row's tiles come once for each group
       const int nt = (ld.keys.all + kTile - 1) / kTile;
       const long long off = t0 - (u0 - ld.tile) * groups;
