@@ -41,6 +41,7 @@ constexpr int kErrAttnDecode = 9;  // a length or page id out of range
 constexpr int kTile = 16;        // keys
 constexpr int kMaxBlocks = 160;  // of the persistent grid; sizes the workspace
 constexpr int kMaxWarps = 16;    // of a block
+constexpr long long kL2Bytes = 129ll << 20;
 constexpr int kMaxCluster = 8;   // blocks that share a row
 constexpr int kJoinThreads = 256;
 constexpr int kMaxChunks = 256;  // of rows, in the scan of their tiles
@@ -71,6 +72,26 @@ __host__ __device__ constexpr size_t ends_bytes() { return kMaxBlocks * sizeof(E
 __device__ __forceinline__ float* block_part(void* ws, int block, int side, int pf) {
   return reinterpret_cast<float*>(static_cast<char*>(ws) + ends_bytes()) +
          (size_t)(2 * block + side) * pf;
+}
+
+// 16-byte async copy global -> shared under an L2 policy (src_bytes = 0 writes zeros without
+// reading).  A call that may read more than half of L2 marks keys and values as the first to
+// leave it: they are not read again before the next step, and what is (lengths, tables,
+// queries, a part of the keys of a loop over layers) stays.  131072-token document 33.8 ->
+// 31.3 us, 64 rings 35.5 -> 33.2; 27 MB that stay in L2 from call to call would take 11.2
+// instead of 10.3.
+__device__ __forceinline__ uint64_t l2_policy(bool once) {
+  uint64_t p;
+  if (once)
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int src_bytes,
+                                           uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n" ::"r"(dst),
+               "l"(src), "r"(src_bytes), "l"(policy));
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
@@ -241,6 +262,7 @@ struct Copies {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a step
     const int c = lane % kLanes;
     const uint32_t dst = ring_u + stage * stage_bytes(D);
+    const uint64_t policy = l2_policy(a.read_once);
 #pragma unroll
     for (int i = 0; i < kTile / kRows; ++i) {
       const int key = i * kRows + lane / kLanes;
@@ -250,8 +272,8 @@ struct Copies {
       const bf16_t* k = rg ? a.ring_k : a.k_pages;
       const bf16_t* v = rg ? a.ring_v : a.v_pages;
       const uint32_t to = dst + key * (D * 2) + ((c ^ (key & 7)) << 4);
-      cp_async16(to, k + e, ok ? 16 : 0);
-      cp_async16(to + kTile * D * 2, v + e, ok ? 16 : 0);
+      cp_async16(to, k + e, ok ? 16 : 0, policy);
+      cp_async16(to + kTile * D * 2, v + e, ok ? 16 : 0, policy);
     }
   }
 };
@@ -916,7 +938,7 @@ cudaError_t launch_rows(const AttnDecodeArgs& a, long long vrows, int cluster, i
 }
 
 template <int D, int NG>
-cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s) {
+cudaError_t launch(AttnDecodeArgs a, int rows, int groups, cudaStream_t s) {
   constexpr int kWarps = warps_of(NG);
   constexpr int smem = kWarps * warp_bytes(D, NG) + kCachedRows * (int)sizeof(Keys);
   static int nsm[64] = {};
@@ -933,6 +955,7 @@ cudaError_t launch(const AttnDecodeArgs& a, int rows, int groups, cudaStream_t s
     for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
   const long long vrows = (long long)rows * groups;
   const long long row_tiles = ((long long)a.max_pages * a.page_size + a.w + kTile - 1) / kTile;
+  a.read_once = (long long)rows * row_tiles * stage_bytes(D) > kL2Bytes / 2;
   const RowShape shape = row_shape(vrows, row_tiles);
   if (shape.warps == 4) return launch_rows<D, NG, 4>(a, vrows, shape.cluster, groups, shift, s);
   if (shape.warps == 2) return launch_rows<D, NG, 2>(a, vrows, shape.cluster, groups, shift, s);

@@ -22,6 +22,7 @@ struct AttnDecodeArgs {
   bf16_t* o = nullptr;              // [L][Hq][B][d]
   float* lse = nullptr;             // [L][Hq][B] or null
   void* ws = nullptr;
+  bool read_once = false;           // set at launch: keys and values leave L2 first
 };
 
 size_t attn_decode_workspace_bytes(int rows, int group, int d);
