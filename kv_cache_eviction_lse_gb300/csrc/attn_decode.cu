@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
 
   if (gw < warps) {
     const long long t0 = gw * share_base + min((long long)gw, share_rem);
-    const long long t1 = t0 + share_base + (gw < share_rem);
+    long long t1 = t0 + share_base + (gw < share_rem);
     const long long u0 = groups == 1 ? t0 : t0 / groups;  // in tiles of one group
     const int l0 = __ffs(__ballot_sync(0xffffffffu, lanes_incl > u0)) - 1;
     long long rel = u0 - __shfl_sync(0xffffffffu, lanes_incl - lane_tiles, l0);
@@ -541,11 +541,17 @@ __global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
           break;
         }
         rel -= __shfl_sync(0xffffffffu, incl, 31);
+        if (ld.base + 32 >= rows) {  // only if the lengths changed since the scan: no work
+          t1 = t0;
+          rel = 0;
+          ld.enter(ld.base);
+          break;
+        }
       }
     }
     ld.tile = (int)rel;
     if (groups > 1) {  // the row's tiles come once for each group
-      const int nt = (ld.keys.all + kTile - 1) / kTile;
+      const int nt = max(1, (ld.keys.all + kTile - 1) / kTile);
       const long long off = t0 - (u0 - ld.tile) * groups;
       ld.group = (int)(off / nt);
       ld.tile = (int)(off - (long long)ld.group * nt);

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 // One block decides the whole append: every row's new tokens, its first new page by an
 // exclusive sum over the rows, and whether all of it fits.
-__global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(const AppendArgs a, int rows,
+__global__ void __launch_bounds__(kPlanThreads, 1) append_plan_kernel(const AppendArgs a, int rows,
                                                                    int N) {
   __shared__ long long sums[32];
   __shared__ int err;
@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(const AppendA
   if (err == 0) {
     for (int r = r0; r < r1; ++r) {
       const int n = a.seq_lens[r], m = tokens(r % a.B);
+      a.plan[kPlanHeader + 2 * r] = n;
       if (n < 0 || n > room) { fault(kErrAppend); continue; }
       if (m == 0) continue;
       if (n + (long long)m > room) { fault(kErrTableFull); continue; }
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(const AppendA
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    long long w = sums[lane];
+    long long w = lane < kPlanThreads / 32 ? sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, w, o);
@@ -189,14 +190,13 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(const AppendA
   const int code = err;
   long long first = next + (warp ? sums[warp - 1] : 0) + incl - mine;
   for (int r = r0; r < r1; ++r) {
-    const int n = a.seq_lens[r];
-    int m = 0;
-    if (code == 0) {
-      m = tokens(r % a.B);
-      a.plan[kPlanHeader + 2 * r] = n;
-      a.plan[kPlanHeader + 2 * r + 1] = (int)first;
-      first += (n + (long long)m + ps - 1) / ps - (n + ps - 1) / ps;
+    if (code) {
+      a.seq_lens_out[r] = a.seq_lens[r];
+      continue;
     }
+    const int n = a.plan[kPlanHeader + 2 * r], m = tokens(r % a.B);
+    a.plan[kPlanHeader + 2 * r + 1] = (int)first;
+    first += (n + (long long)m + ps - 1) / ps - (n + ps - 1) / ps;
     a.seq_lens_out[r] = n + m;
   }
   if (tid == 0) {
@@ -204,6 +204,14 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(const AppendA
     a.next_page_out[0] = code ? next : (int)(next + total);
     if (code) atomicCAS(&g_append_error, 0, code);
   }
+}
+
+// The plan has checked every page and table index; this holds also if another stream changes
+// the tables or token starts while the call runs, which nothing can make right.
+__device__ __forceinline__ bool inside(const AppendArgs& a, int idx, int page) {
+  if ((uint32_t)idx < (uint32_t)a.max_pages && (uint32_t)page < (uint32_t)a.capacity) return true;
+  atomicCAS(&g_append_error, 0, kErrAppend);
+  return false;
 }
 
 // The page of a slot of a row: one that the row had, or one of its new ones.
@@ -235,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
     const int used = (n + m) % a.page_size, last = (n + m) / a.page_size;
     if (used == 0 || last < have) return;
     const int pg = a.plan[kPlanHeader + 2 * row + 1] + last - have;
+    if (!inside(a, last, pg)) return;
     const size_t at = ((size_t)pg * a.page_size + used) * D;
     const int chunks = (a.page_size - used) * (D / 8);
     for (int c = threadIdx.x & 31; c < chunks; c += 32) {
@@ -295,7 +304,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
     const int cr = (at - n_q) * a.B + b;
     const int2 plan = reinterpret_cast<const int2*>(a.plan + kPlanHeader)[cr];
     const int slot = plan.x + j, idx = slot / a.page_size, off = slot - idx * a.page_size;
+    if (!inside(a, idx, 0)) continue;
     const int pg = page_of(a, cr, plan.x, plan.y, idx);
+    if (!inside(a, idx, pg)) continue;
     // a new page enters the table with the first of its rows that this call writes
     if (u == 0 && off == 0) a.block_table[(size_t)cr * a.max_pages + idx] = pg;
     const size_t to = ((size_t)pg * a.page_size + off) * D;
