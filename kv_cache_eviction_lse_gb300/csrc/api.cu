@@ -764,7 +764,7 @@ kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const in
   a.v = v; a.B = B; a.page_size = page_size; a.max_pages = max_pages; a.capacity = capacity_pages;
   a.tok_start = tok_start; a.k_pages = k_pages; a.v_pages = v_pages;
   a.next_page = next_page; a.next_page_out = next_page_out; a.block_table = block_table;
-  a.seq_lens = seq_lens; a.seq_lens_out = seq_lens_out; a.plan = static_cast<int*>(ws);
+  a.seq_lens = seq_lens; a.seq_lens_out = seq_lens_out; a.plan = ws;
   return cuda_status(kvs::launch_append(r, a, as_stream(stream)), "kvs_append_paged");
 }
 

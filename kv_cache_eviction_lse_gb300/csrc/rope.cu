@@ -31,9 +31,24 @@ constexpr int kErrAppend = 8;     // token starts, lengths or page ids out of ra
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
 
-// The plan of an append in the workspace: a status word (0 = append), then the length
-// and the first new page of every row.
-constexpr int kPlanHeader = 4;
+// The plan of an append in the workspace: the page counter before it, what each block of
+// rows found (pages to take, error code), and per row its length and the pages that the rows
+// before it in its block take.
+constexpr int kPlanBlocks = 256;
+struct PlanHead { int next, pad[3]; };
+struct PlanBlock { long long pages; int code; };
+struct PlanView {
+  PlanHead* head;
+  PlanBlock* blocks;
+  int2* rows;
+  __device__ explicit PlanView(void* ws)
+      : head(static_cast<PlanHead*>(ws)), blocks(reinterpret_cast<PlanBlock*>(head + 1)),
+        rows(reinterpret_cast<int2*>(blocks + kPlanBlocks)) {}
+};
+
+__device__ __forceinline__ int tokens_of(const AppendArgs& a, int b) {
+  return a.tok_start ? a.tok_start[b + 1] - a.tok_start[b] : 1;
+}
 
 __device__ __forceinline__ void unpack8(const uint4& u, float* x) {
   x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x);
@@ -125,10 +140,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
 }
 
-// One block decides the whole append: every row's new tokens, its first new page by an
-// exclusive sum over the rows, and whether all of it fits.
+// The plan, by up to kPlanBlocks blocks of rows: what every row has and how many new pages the
+// rows before it in its block take.  Whether the whole append fits is known when all blocks
+// are done; the append's blocks put that together from their records (see decide).
 __global__ void __launch_bounds__(kPlanThreads, 1) append_plan_kernel(const AppendArgs a, int rows,
-                                                                   int N) {
+                                                                      int N, int per) {
   __shared__ long long sums[32];
   __shared__ int err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -136,35 +152,32 @@ __global__ void __launch_bounds__(kPlanThreads, 1) append_plan_kernel(const Appe
   if (tid == 0) err = 0;
   __syncthreads();
   auto fault = [&](int code) { atomicMax(&err, code); };
-  auto tokens = [&](int b) { return a.tok_start ? a.tok_start[b + 1] - a.tok_start[b] : 1; };
-  if (a.tok_start) {
-    for (int b = tid; b < a.B; b += kPlanThreads)
-      if (a.tok_start[b] < 0 || a.tok_start[b + 1] < a.tok_start[b]) fault(kErrAppend);
-    if (tid == 0 && (a.tok_start[0] != 0 || a.tok_start[a.B] > N)) fault(kErrAppend);
+  const PlanView plan(a.plan);
+  if (blockIdx.x == 0 && tid == 0) {
+    const int next = a.next_page[0];
+    plan.head->next = next;
+    if (next < 0) fault(kErrAppend);
+    if (a.tok_start && (a.tok_start[0] != 0 || a.tok_start[a.B] > N)) fault(kErrAppend);
   }
-  const int next = a.next_page[0];
-  if (tid == 0 && next < 0) fault(kErrAppend);
-  __syncthreads();
   const int ps = a.page_size;
   // slots and page counts stay within 32 bits
   const long long room = min((long long)a.max_pages * ps, (long long)INT32_MAX - 8192);
-  const int per = (rows + kPlanThreads - 1) / kPlanThreads;
-  const long long lo = (long long)tid * per;
-  const int r0 = (int)(lo < rows ? lo : rows), r1 = (int)(lo + per < rows ? lo + per : rows);
+  const long long lo = ((long long)blockIdx.x * kPlanThreads + tid) * per;
+  const int r0 = (int)min(lo, (long long)rows), r1 = (int)min(lo + per, (long long)rows);
   long long mine = 0;
-  if (err == 0) {
-    for (int r = r0; r < r1; ++r) {
-      const int n = a.seq_lens[r], m = tokens(r % a.B);
-      a.plan[kPlanHeader + 2 * r] = n;
-      if (n < 0 || n > room) { fault(kErrAppend); continue; }
-      if (m == 0) continue;
-      if (n + (long long)m > room) { fault(kErrTableFull); continue; }
-      if (n % ps) {
-        const int pg = a.block_table[(size_t)r * a.max_pages + n / ps];
-        if (pg < 0 || pg >= a.capacity) fault(kErrAppend);
-      }
-      mine += (n + (long long)m + ps - 1) / ps - (n + ps - 1) / ps;
+  for (int r = r0; r < r1; ++r) {
+    const int n = a.seq_lens[r], b = r % a.B;
+    const int from = a.tok_start ? a.tok_start[b] : 0, to = a.tok_start ? a.tok_start[b + 1] : 1;
+    plan.rows[r] = {n, (int)mine};
+    if (n < 0 || n > room || from < 0 || to < from) { fault(kErrAppend); continue; }
+    const int m = to - from;
+    if (m == 0) continue;
+    if (n + (long long)m > room) { fault(kErrTableFull); continue; }
+    if (n % ps) {
+      const int pg = a.block_table[(size_t)r * a.max_pages + n / ps];
+      if (pg < 0 || pg >= a.capacity) fault(kErrAppend);
     }
+    mine += (n + (long long)m + ps - 1) / ps - (n + ps - 1) / ps;
   }
   long long incl = mine;
 #pragma unroll
@@ -174,36 +187,62 @@ __global__ void __launch_bounds__(kPlanThreads, 1) append_plan_kernel(const Appe
   }
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  if (warp == 0) {
-    long long w = lane < kPlanThreads / 32 ? sums[lane] : 0;
+  long long others = sums[lane];  // of the warps; every warp for itself
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    sums[lane] = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, others, o);
+    if (lane >= o) others += y;
   }
+  const long long warps_before = __shfl_sync(0xffffffffu, others, warp ? warp - 1 : 0);
+  const int before = (int)(incl - mine + (warp ? warps_before : 0));
+  for (int r = r0; r < r1; ++r) plan.rows[r].y += before;
+  if (tid == 31) plan.blocks[blockIdx.x] = {others, err};
+}
+
+// What an append's block knows of the whole plan: a code (0 = append), the pages that it takes
+// and, per plan block, the first new page of its rows.
+struct Decision {
+  int code;
+  long long total;
+};
+
+// Called by all threads of a block, after the plan; base [kPlanBlocks] in shared memory.
+__device__ __forceinline__ Decision decide(const AppendArgs& a, const PlanView& plan, int blocks,
+                                           int* base) {
+  const int next = plan.head->next;
+  if (blocks == 1) {
+    const PlanBlock b = plan.blocks[0];
+    base[0] = next;  // the same by every thread, so that none waits for another
+    const bool fits = b.pages == 0 || next + b.pages <= a.capacity;
+    return {b.code ? b.code : fits ? 0 : kErrPoolFull, b.pages};
+  }
+  __shared__ long long sums[kThreads / 32];
+  __shared__ int code_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  PlanBlock mine = {0, 0};
+  if (tid < blocks) mine = plan.blocks[tid];
+  long long incl = mine.pages;
+  int code = mine.code;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  code = __reduce_max_sync(0xffffffffu, code);
+  if (tid == 0) code_s = 0;
+  if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  const long long total = sums[31];
-  if (tid == 0 && total > 0 && next + total > a.capacity) fault(kErrPoolFull);
+  if (lane == 0 && code) atomicMax(&code_s, code);
+  long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  static_assert(kPlanBlocks == kThreads, "a thread per plan block");
+  base[tid] = (int)(next + before + incl - mine.pages);
   __syncthreads();
-  const int code = err;
-  long long first = next + (warp ? sums[warp - 1] : 0) + incl - mine;
-  for (int r = r0; r < r1; ++r) {
-    if (code) {
-      a.seq_lens_out[r] = a.seq_lens[r];
-      continue;
-    }
-    const int n = a.plan[kPlanHeader + 2 * r], m = tokens(r % a.B);
-    a.plan[kPlanHeader + 2 * r + 1] = (int)first;
-    first += (n + (long long)m + ps - 1) / ps - (n + ps - 1) / ps;
-    a.seq_lens_out[r] = n + m;
-  }
-  if (tid == 0) {
-    a.plan[0] = code;
-    a.next_page_out[0] = code ? next : (int)(next + total);
-    if (code) atomicCAS(&g_append_error, 0, code);
-  }
+  const bool fits = total == 0 || next + total <= a.capacity;
+  return {code_s ? code_s : fits ? 0 : kErrPoolFull, total};
 }
 
 // The plan has checked every page and table index; this holds also if another stream changes
@@ -222,31 +261,40 @@ __device__ __forceinline__ int page_of(const AppendArgs& a, int r, int n, int fi
 
 // Blocks 0 .. token_blocks * groups - 1 take tokens (block / groups) and every groups-th
 // slab: a head of the queries, or one of keys and values together.  The blocks behind them
-// clear page ends.  Nothing is written before the plan is known; the first slab's rows, the
-// angles and the token's sequence are ready by then.
+// take a row a warp: its new length and the end of its last page.  Nothing is written before
+// the plan is known; the first slab's rows, the angles and the token's sequence are ready by
+// then.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ RopeArgs r,
-                                                          const __grid_constant__ AppendArgs a,
-                                                          int token_blocks, int groups) {
+                                                             const __grid_constant__ AppendArgs a,
+                                                             int token_blocks, int groups,
+                                                             int plan_blocks, int plan_shift) {
   constexpr int kPer = D / 16;
+  __shared__ int base[kPlanBlocks];
+  const PlanView plan(a.plan);
   const int rows = r.L * r.Hkv * a.B;
   if ((int)blockIdx.x >= token_blocks * groups) {
-    // one warp per row: the unused rows of the row's last page, where that page is new
-    const int row = (blockIdx.x - token_blocks * groups) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int b = row % a.B;
-    const int m = a.tok_start ? a.tok_start[b + 1] - a.tok_start[b] : 1;
+    const int block = blockIdx.x - token_blocks * groups, lane = threadIdx.x & 31;
+    const int row = block * (kThreads / 32) + (threadIdx.x >> 5);
+    const int m = row < rows ? tokens_of(a, row % a.B) : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (a.plan[0] != 0) return;
-    const int n = a.plan[kPlanHeader + 2 * row];
-    const int have = (n + a.page_size - 1) / a.page_size;
-    const int used = (n + m) % a.page_size, last = (n + m) / a.page_size;
+    const Decision d = decide(a, plan, plan_blocks, base);
+    if (block == 0 && threadIdx.x == 0) {
+      a.next_page_out[0] = plan.head->next + (d.code ? 0 : (int)d.total);
+      if (d.code) atomicCAS(&g_append_error, 0, d.code);
+    }
+    if (row >= rows) return;
+    const int2 p = plan.rows[row];
+    if (lane == 0) a.seq_lens_out[row] = d.code ? p.x : p.x + m;
+    if (d.code) return;
+    const int have = (p.x + a.page_size - 1) / a.page_size;
+    const int used = (p.x + m) % a.page_size, last = (p.x + m) / a.page_size;
     if (used == 0 || last < have) return;
-    const int pg = a.plan[kPlanHeader + 2 * row + 1] + last - have;
+    const int pg = base[row >> plan_shift] + p.y + last - have;  // the unused rows of a new page
     if (!inside(a, last, pg)) return;
     const size_t at = ((size_t)pg * a.page_size + used) * D;
     const int chunks = (a.page_size - used) * (D / 8);
-    for (int c = threadIdx.x & 31; c < chunks; c += 32) {
+    for (int c = lane; c < chunks; c += 32) {
       reinterpret_cast<uint4*>(a.k_pages + at)[c] = make_uint4(0, 0, 0, 0);
       reinterpret_cast<uint4*>(a.v_pages + at)[c] = make_uint4(0, 0, 0, 0);
     }
@@ -254,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
   }
   const int u = threadIdx.x % kPer;
   const int t = blockIdx.x / groups * (kThreads / kPer) + threadIdx.x / kPer;
-  if (t >= r.N) return;
-  // the token's sequence: the last b with tok_start[b] <= t
+  // the token's sequence: the last b with tok_start[b] <= t; none for padding behind the last
+  bool live = t < r.N;
   int b = t, j = 0;
   if (a.tok_start) {
-    if (t >= a.tok_start[a.B]) return;  // behind the last sequence
+    live = live && t < a.tok_start[a.B];
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -269,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
   }
   const Lane ln = lane_of(u, r.rot_dim, r.interleaved);
   float c[8], s[8];
-  if (ln.rotate) angles(r, u, r.pos[t], c, s);
-  const int n_q = r.q ? r.L * r.Hq : 0, n_all = n_q + r.L * r.Hkv;
+  if (live && ln.rotate) angles(r, u, r.pos[t], c, s);
+  const int n_q = r.q ? r.L * r.Hq : 0, n_all = live ? n_q + r.L * r.Hkv : 0;
   auto row_at = [&](int head) { return ((size_t)head * r.N + t) * D; };
   uint4 x0, x1, v0 = {}, v1 = {};
   auto load = [&](int slab) {
@@ -287,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
   int slab = blockIdx.x % groups;
   if (slab < n_all) load(slab);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (a.plan[0] != 0) return;
+  if (decide(a, plan, plan_blocks, base).code) return;
   while (slab < n_all) {
     const int at = slab;
     uint4 y0 = x0, y1 = x1;
@@ -302,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
       continue;
     }
     const int cr = (at - n_q) * a.B + b;
-    const int2 plan = reinterpret_cast<const int2*>(a.plan + kPlanHeader)[cr];
-    const int slot = plan.x + j, idx = slot / a.page_size, off = slot - idx * a.page_size;
+    const int2 p = plan.rows[cr];
+    const int slot = p.x + j, idx = slot / a.page_size, off = slot - idx * a.page_size;
     if (!inside(a, idx, 0)) continue;
-    const int pg = page_of(a, cr, plan.x, plan.y, idx);
+    const int pg = page_of(a, cr, p.x, base[cr >> plan_shift] + p.y, idx);
     if (!inside(a, idx, pg)) continue;
     // a new page enters the table with the first of its rows that this call writes
     if (u == 0 && off == 0) a.block_table[(size_t)cr * a.max_pages + idx] = pg;
@@ -331,7 +379,7 @@ int slab_groups(int token_blocks, int slabs, int waves) {
 }  // namespace
 
 size_t append_workspace_bytes(int rows) {
-  return ((size_t)kPlanHeader + 2 * (size_t)rows) * sizeof(int);
+  return sizeof(PlanHead) + kPlanBlocks * sizeof(PlanBlock) + (size_t)rows * sizeof(int2);
 }
 
 cudaError_t launch_rope(const RopeArgs& r, cudaStream_t s) {
@@ -350,17 +398,22 @@ cudaError_t launch_rope(const RopeArgs& r, cudaStream_t s) {
 
 cudaError_t launch_append(const RopeArgs& r, const AppendArgs& a, cudaStream_t s) {
   const int rows = r.L * r.Hkv * a.B;
-  count_launches(1);
-  append_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, rows, r.N);
+  int plan_shift = 10;  // rows of a plan block: kPlanThreads times a power of two
+  static_assert(kPlanThreads == 1 << 10, "a row a thread at least");
+  while (((rows - 1) >> plan_shift) >= kPlanBlocks) ++plan_shift;
+  const int plan_blocks = ((rows - 1) >> plan_shift) + 1, per = 1 << (plan_shift - 10);
+  count_launches(2);
+  append_plan_kernel<<<plan_blocks, kPlanThreads, 0, s>>>(a, rows, r.N, per);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || r.N == 0) return e;
+  if (e != cudaSuccess) return e;
   const int slabs = (r.q ? r.L * r.Hq : 0) + r.L * r.Hkv;
   const int per_block = kThreads / (r.d / 16);
-  const int blocks = (r.N + per_block - 1) / per_block, groups = slab_groups(blocks, slabs, 4);
-  const int clear = a.page_size > 1 ? (rows + kThreads / 32 - 1) / (kThreads / 32) : 0;
+  const int blocks = (r.N + per_block - 1) / per_block;
+  const int groups = blocks ? slab_groups(blocks, slabs, 4) : 1;
+  const int row_blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
   // its blocks come up beside the plan's and wait for it
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks * groups + clear);
+  cfg.gridDim = dim3(blocks * groups + row_blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -368,9 +421,10 @@ cudaError_t launch_append(const RopeArgs& r, const AppendArgs& a, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  count_launches(1);
-  return r.d == 128 ? cudaLaunchKernelEx(&cfg, append_kernel<128>, r, a, blocks, groups)
-                    : cudaLaunchKernelEx(&cfg, append_kernel<64>, r, a, blocks, groups);
+  return r.d == 128 ? cudaLaunchKernelEx(&cfg, append_kernel<128>, r, a, blocks, groups,
+                                         plan_blocks, plan_shift)
+                    : cudaLaunchKernelEx(&cfg, append_kernel<64>, r, a, blocks, groups,
+                                         plan_blocks, plan_shift);
 }
 
 cudaError_t rope_device_error(int* code, bool clear, cudaStream_t s) {

@@ -34,7 +34,7 @@ struct AppendArgs {
   int* block_table = nullptr;       // [rows][max_pages]
   const int* seq_lens = nullptr;    // [rows]
   int* seq_lens_out = nullptr;
-  int* plan = nullptr;              // workspace of append_workspace_bytes()
+  void* plan = nullptr;             // workspace of append_workspace_bytes()
 };
 
 size_t append_workspace_bytes(int rows);
