@@ -28,13 +28,13 @@ constexpr int kErrPoolFull = 4;   // as kvs_decode_step
 constexpr int kErrTableFull = 5;
 constexpr int kErrAppend = 8;     // token starts, lengths or page ids out of range
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPlanThreads = 1024;
 
 // The plan of an append in the workspace: the page counter before it, what each block of
 // rows found (pages to take, error code), and per row its length and the pages that the rows
 // before it in its block take.
-constexpr int kPlanBlocks = 256;
+constexpr int kPlanBlocks = 128;
 struct PlanHead { int next, pad[3]; };
 struct PlanBlock { long long pages; int code; };
 struct PlanView {
@@ -265,7 +265,7 @@ __device__ __forceinline__ int page_of(const AppendArgs& a, int r, int n, int fi
 // the plan is known; the first slab's rows, the angles and the token's sequence are ready by
 // then.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ RopeArgs r,
+__global__ void __launch_bounds__(kThreads, 7) append_kernel(const __grid_constant__ RopeArgs r,
                                                              const __grid_constant__ AppendArgs a,
                                                              int token_blocks, int groups,
                                                              int plan_blocks, int plan_shift) {
@@ -368,11 +368,11 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
 }
 
 // Blocks per group of tokens: a thread walks several heads with one set of angles, in about
-// `waves` times the 8 blocks of an SM.  A 16384-token prompt of 2 layers turns in 102.2,
-// 100.4, 99.2 and 171 us with 2, 4, 8 and 32; a chunk of 8192 tokens in 4 layers is
-// appended in 130.6, 127.7, 132.7 and 206 us.
+// `waves` times the 16 blocks of an SM.  A 16384-token prompt of 2 layers turns in 102.2,
+// 100.4, 99.2 and 171 us with 2, 4, 8 and 32; a chunk of 8192 tokens in 4 layers is appended
+// in 126.7, 128.2 and 131.6 us with 2, 3 and 6.
 int slab_groups(int token_blocks, int slabs, int waves) {
-  int groups = (152 * 8 * waves + token_blocks - 1) / token_blocks;
+  int groups = (152 * 16 * waves + token_blocks - 1) / token_blocks;
   return groups < 1 ? 1 : groups > slabs ? slabs : groups > 65535 ? 65535 : groups;
 }
 
@@ -409,7 +409,7 @@ cudaError_t launch_append(const RopeArgs& r, const AppendArgs& a, cudaStream_t s
   const int slabs = (r.q ? r.L * r.Hq : 0) + r.L * r.Hkv;
   const int per_block = kThreads / (r.d / 16);
   const int blocks = (r.N + per_block - 1) / per_block;
-  const int groups = blocks ? slab_groups(blocks, slabs, 4) : 1;
+  const int groups = blocks ? slab_groups(blocks, slabs, 2) : 1;
   const int row_blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
   // its blocks come up beside the plan's and wait for it
   cudaLaunchConfig_t cfg = {};

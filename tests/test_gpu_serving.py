@@ -300,10 +300,45 @@ def test_append_refused_on_the_device(C):
     c = append_case(C, **base)
     c["nxt"][0] = -1
     refused(C, c, 8)
+    # thousands of rows, planned by several blocks: a short pool, a bad length in the last row
+    many = dict(L=5, Hq=16, H=16, B=30, d=64, ps=2, m=[1] * 30, nmax=5, single=True, seed=6)
+    refused(C, append_case(C, extra=-1, **many), 4)
+    c = append_case(C, **many)
+    c["sl"][4, 15, 29] = -1
+    refused(C, c, 8)
     # and the same call with a pool that is large enough goes through
     c = append_case(C, **base)
     check_append(c, call_append(c))
     assert C.kvs_device_error(clear=True) == 0
+
+
+def test_append_to_more_rows_than_plan_threads(C):
+    """135168 rows, more than one a thread of the plan: every row's first token takes the page
+    of the row's number; the next two calls fill it and take another."""
+    L, H, B, d, ps = 33, 64, 64, 64, 2
+    rows, dm = L * H * B, C.dims(L, H, H, d)
+    kp = torch.zeros(2 * rows, ps, d, dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    bt = torch.full((L, H, B, 2), -1, dtype=torch.int32, device="cuda")
+    sl = torch.zeros(L, H, B, dtype=torch.int32, device="cuda")
+    nxt = torch.zeros(1, dtype=torch.int32, device="cuda")
+    nb = C.kvs_append_paged_workspace_size(dm, B)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    toks = []
+    for i in range(3):
+        k = torch.randn(L, H, B, d, generator=gen, device="cuda").to(torch.bfloat16)
+        toks.append(k)
+        C.kvs_append_paged(dm, B, B, None, None, 0, None, False, None, None, k, -k, ps, kp, vp,
+                           2 * rows, nxt, nxt, bt, 2, sl, sl, ws, nb)
+    assert C.kvs_device_error(clear=True) == 0
+    first = torch.arange(rows, dtype=torch.int32, device="cuda").view(L, H, B)
+    assert torch.equal(bt[..., 0], first) and torch.equal(bt[..., 1], first + rows)
+    assert (sl == 3).all() and int(nxt) == 2 * rows
+    got = kp.view(2, L, H, B, ps, d)
+    for i, (page, r) in enumerate(((0, 0), (0, 1), (1, 0))):
+        assert torch.equal(got[page, :, :, :, r], toks[i])
+    assert not got[1, :, :, :, 1].any() and torch.equal(vp, -kp)
 
 
 def test_append_taken_back(C):
