@@ -289,17 +289,17 @@ def _here(stream):
 def _arg(t, dtype, n, name, dev):
     """Device pointer of a tensor argument that must hold at least n elements of dtype and
     lie on the current device."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
+    if t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype or t.numel() < n:
         raise ValueError(f"kvs: {name} must hold at least {n} elements of {dtype}, got "
                          f"{t.numel()} of {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"kvs: tensor arguments must be CUDA tensors on the current device "
                          f"({name} is on {t.device})")
-    if not t.is_contiguous():
-        raise ValueError(f"kvs: tensor arguments must be contiguous ({name} is not)")
-    return t.data_ptr()
+    raise ValueError(f"kvs: tensor arguments must be contiguous ({name} is not)")
 
 
 def _freqs(inv_freq, rot_dim):
