@@ -772,32 +772,39 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
 
 // The same for rows that cannot be long: a block, or a cluster of blocks, per row and group
 // of heads, with equal contiguous shares of the row's tiles per warp.  No scan over other
-// rows, no workspace and no second kernel: a block's warps meet in its shared memory, a
-// cluster's blocks read one another's.
+// rows, no workspace and no second kernel: a block's warps meet in its shared memory, and a
+// cluster's blocks send their parts to the one that sums them up.
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t n;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
   return n;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-  float x;
+// to the same place in the shared memory of another block of the cluster
+__device__ __forceinline__ void st_cluster(const float* to, uint32_t rank, float x) {
   uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
-  return x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(to)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
 }
+
+// What a block of a cluster is sent: eight fragments and eight heads' references and sums,
+// from each block for each unit that it owns (units u with u % blocks == rank).  Units and
+// blocks are powers of two up to 8, so max(units, blocks) parts arrive at most.
+struct Sent { float x[8 * 32], ref[8], sum[8]; };
 
 template <int D, int NG, int W>
 __global__ void __launch_bounds__(W * 32, (NG == 1 ? 12 : 8) / W) attn_decode_row_kernel(
     const __grid_constant__ AttnDecodeArgs a, int groups, int ps_shift) {
   constexpr int S = stages(D), KS = D / 16, NF = frags(D, NG), H = NG * 8;
+  static_assert(NF / 8 <= kMaxCluster && (NF & (NF - 1)) == 0, "units fit what is sent");
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t live[W][S];
-  __shared__ float ref_s[W + 1][H], sum_s[W + 1][H];  // of the warps, and of the block
+  __shared__ float ref_s[W][H], sum_s[W][H];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.Hq / a.Hkv;
   const int blocks = cluster_size(), rank = blockIdx.x % blocks;
@@ -805,6 +812,8 @@ __global__ void __launch_bounds__(W * 32, (NG == 1 ? 12 : 8) / W) attn_decode_ro
   const int len = a.seq_lens[row];
   const Keys keys = keys_of(a, len, ring_pos(a, row));
   if (tid == 0 && rank == 0 && keys.paged != len) atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
+  Sent* sent = reinterpret_cast<Sent*>(smem + W * kRingBytes);
+  if (blocks > 1) cluster_arrive();  // this block has started: its shared memory may be written
   uint8_t* ring = smem + warp * kRingBytes;
   const uint32_t ring_u = smem_u32(ring);
   Heads<D, NG> heads;
@@ -834,7 +843,8 @@ __global__ void __launch_bounds__(W * 32, (NG == 1 ? 12 : 8) / W) attn_decode_ro
   heads.fold();
   heads.leave(reinterpret_cast<float*>(ring), ref_s[warp], sum_s[warp], lane);
   __syncthreads();
-  // --- the block's warps, eight fragments a warp at a time; the result over warp 0's part
+  if (blocks > 1) cluster_wait();
+  // --- the block's warps, eight fragments a warp at a time
   constexpr int kUnits = NF / 8;
   for (int u = warp; u < kUnits; u += W) {
     const int f0 = u * 8, h0 = f0 / (KS * 4) * 8 + (lane & 3) * 2;
@@ -859,48 +869,42 @@ __global__ void __launch_bounds__(W * 32, (NG == 1 ? 12 : 8) / W) attn_decode_ro
     if (blocks == 1) {
       store_unit<D, NG>(a, row, group, g, f0, acc, top, sum, lane);
     } else {
-      float* x = reinterpret_cast<float*>(smem) + f0 * 32 + lane;
+      Sent& to = sent[u / blocks * blocks + rank];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i * 32] = acc[i];
-      if (lane < 4 && f0 % (KS * 4) == 0) {
+      for (int i = 0; i < 8; ++i) st_cluster(&to.x[i * 32 + lane], u % blocks, acc[i]);
+      if (lane < 4) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          ref_s[W][h0 + i] = top[i];
-          sum_s[W][h0 + i] = sum[i];
+          st_cluster(&to.ref[lane * 2 + i], u % blocks, top[i]);
+          st_cluster(&to.sum[lane * 2 + i], u % blocks, sum[i]);
         }
       }
     }
   }
   if (blocks == 1) return;
-  // --- the cluster's blocks: unit u by block u % blocks
-  cluster_sync();
+  // --- the cluster's blocks, each unit by the block that owns it
+  cluster_arrive();
+  cluster_wait();
   for (int u = rank + blocks * warp; u < kUnits; u += blocks * W) {
-    const int f0 = u * 8, h0 = f0 / (KS * 4) * 8 + (lane & 3) * 2;
-    const uint32_t ref_u = smem_u32(&ref_s[W][h0]), sum_u = smem_u32(&sum_s[W][h0]);
-    const uint32_t x_u = smem_u32(smem) + (f0 * 32 + lane) * 4;
-    float ref[2][8], sum[2] = {}, top[2] = {-INFINITY, -INFINITY}, acc[8] = {};
+    const Sent* from = sent + u / blocks * blocks;
+    const int h = (lane & 3) * 2;
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {}, acc[8] = {};
+    for (int p = 0; p < blocks; ++p)
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        ref[i][p] = p < blocks ? ld_cluster(ref_u + 4 * i, p) : -INFINITY;
-        top[i] = fmaxf(top[i], ref[i][p]);
-      }
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      if (p >= blocks) break;
+      for (int i = 0; i < 2; ++i) top[i] = fmaxf(top[i], from[p].ref[h + i]);
+#pragma unroll 4
+    for (int p = 0; p < blocks; ++p) {
       float w[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        w[i] = fast_exp2(ref[i][p] - finite_ref(top[i]));
-        sum[i] += ld_cluster(sum_u + 4 * i, p) * w[i];
+        w[i] = fast_exp2(from[p].ref[h + i] - finite_ref(top[i]));
+        sum[i] += from[p].sum[h + i] * w[i];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += ld_cluster(x_u + i * 128, p) * w[i & 1];
+      for (int i = 0; i < 8; ++i) acc[i] += from[p].x[i * 32 + lane] * w[i & 1];
     }
-    store_unit<D, NG>(a, row, group, g, f0, acc, top, sum, lane);
+    store_unit<D, NG>(a, row, group, g, u * 8, acc, top, sum, lane);
   }
-  cluster_sync();  // no block leaves while another reads its shared memory
 }
 
 // Warps of a block and blocks of a cluster per row where the row kernel takes a call, else
@@ -925,13 +929,14 @@ RowShape row_shape(long long vrows, long long row_tiles) {
 template <int D, int NG, int W>
 cudaError_t launch_rows(const AttnDecodeArgs& a, long long vrows, int cluster, int groups, int shift,
                         cudaStream_t s) {
+  const int smem = W * kRingBytes + (cluster > 1 ? kMaxCluster * (int)sizeof(Sent) : 0);
   cudaError_t e = cudaFuncSetAttribute(attn_decode_row_kernel<D, NG, W>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, W * kRingBytes);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(vrows * cluster));
   cfg.blockDim = dim3(W * 32);
-  cfg.dynamicSmemBytes = W * kRingBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
