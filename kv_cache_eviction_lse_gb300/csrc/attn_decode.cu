@@ -80,16 +80,13 @@ __device__ __forceinline__ float* block_part(void* ws, int block, int side, int 
 // queries, a part of the keys of a loop over layers) stays.  131072-token document 33.8 ->
 // 31.3 us, 64 rings 35.5 -> 33.2; 27 MB that stay in L2 from call to call would take 11.2
 // instead of 10.3.
-__device__ __forceinline__ uint64_t l2_policy(bool once) {
+__device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t p;
-  if (once)
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-  else
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int src_bytes,
-                                           uint64_t policy) {
+__device__ __forceinline__ void cp_async16_once(uint32_t dst, const void* src, int src_bytes,
+                                                uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n" ::"r"(dst),
                "l"(src), "r"(src_bytes), "l"(policy));
 }
@@ -262,7 +259,7 @@ struct Copies {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a step
     const int c = lane % kLanes;
     const uint32_t dst = ring_u + stage * stage_bytes(D);
-    const uint64_t policy = l2_policy(a.read_once);
+    const uint64_t policy = read_once_policy();
 #pragma unroll
     for (int i = 0; i < kTile / kRows; ++i) {
       const int key = i * kRows + lane / kLanes;
@@ -272,8 +269,13 @@ struct Copies {
       const bf16_t* k = rg ? a.ring_k : a.k_pages;
       const bf16_t* v = rg ? a.ring_v : a.v_pages;
       const uint32_t to = dst + key * (D * 2) + ((c ^ (key & 7)) << 4);
-      cp_async16(to, k + e, ok ? 16 : 0, policy);
-      cp_async16(to + kTile * D * 2, v + e, ok ? 16 : 0, policy);
+      if (a.read_once) {
+        cp_async16_once(to, k + e, ok ? 16 : 0, policy);
+        cp_async16_once(to + kTile * D * 2, v + e, ok ? 16 : 0, policy);
+      } else {
+        cp_async16(to, k + e, ok ? 16 : 0);
+        cp_async16(to + kTile * D * 2, v + e, ok ? 16 : 0);
+      }
     }
   }
 };
@@ -913,13 +915,13 @@ __global__ void __launch_bounds__(W * 32, (NG == 1 ? 12 : 8) / W) attn_decode_ro
 // 30 to 100 % full, row kernel against stream (us): 8 rows of 58 tiles 7.0 / 9.4, of 241
 // tiles 11.4 / 10.1; 32 rows of 126 tiles 9.1 / 11.9; 128 rows of 15 tiles 7.0 / 11.5, of 61
 // tiles 13.3 / 16.3, of 246 tiles 37.4 / 33.0; 512 rows of 16 tiles 12.9 / 17.2, of 63 tiles
-// 32.0 / 32.3, of 249 tiles 101 / 87.  Where there are enough short rows, blocks of two
-// warps, six on an SM, overlap one another's starts and joins better than three of four
-// warps: 2048 rows of 15 tiles 35.4 / 37.9, 16384 rows 203 / 239, 2048 rows of 4 tiles 16.7 /
-// 23.2; of 38 tiles 55.1 / 53.5.
+// 32.0 / 32.3, of 249 tiles 101 / 87.  More short rows than three blocks an SM take blocks of
+// two warps, six on an SM, which overlap one another's starts and joins better than three of
+// four warps: 512 rows of 14 tiles 12.5 / 13.4, 2048 rows of 15 tiles 35.4 / 37.9, 16384 rows
+// 203 / 239, 2048 rows of 4 tiles 16.7 / 23.2; of 38 tiles 55.1 / 53.5.
 struct RowShape { int warps, cluster; };
 RowShape row_shape(long long vrows, long long row_tiles) {
-  if (vrows >= 152 * 6 && row_tiles <= 2 * 16) return {2, 1};
+  if (vrows > 152 * 3 && row_tiles <= 2 * 16) return {2, 1};
   int c = 1;
   while (c < kMaxCluster && vrows * c * 2 <= 152 * 3) c *= 2;
   const int most = vrows * c >= 152 ? 16 : 6;

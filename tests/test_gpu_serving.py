@@ -638,10 +638,11 @@ def test_attend_graph_replays_follow_the_state(C, room):
     assert C.kvs_device_error(clear=True) == 0
 
 
-def test_two_calls_at_once(C):
+@pytest.mark.parametrize("room", [0, 100000], ids=["tight", "wide"])
+def test_two_calls_at_once(C, room):
     """Calls on two streams with workspaces of their own do not disturb each other."""
-    cases = [attend_case(C, L=1, Hq=8, H=2, B=4, d=128, ps=16, n=[2000, 5, 900, 64], seed=s)
-             for s in (1, 2)]
+    cases = [attend_case(C, L=1, Hq=8, H=2, B=4, d=128, ps=16, n=[2000, 5, 900, 64], seed=s,
+                         room=room) for s in (1, 2)]
     alone = [call_attend(c) for c in cases]
     runs = []
     for c in cases:
