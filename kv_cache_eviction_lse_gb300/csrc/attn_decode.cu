@@ -57,9 +57,11 @@ constexpr int kRingBytes = stages(128) * stage_bytes(128);  // per warp, either 
 __host__ __device__ constexpr int frags(int d, int ng) { return d / 16 * 4 * ng; }
 __host__ __device__ constexpr int part_floats(int d, int ng) { return frags(d, ng) * 32 + 16 * ng; }
 
-// Warps of a block: as many as the rings and a partial result each fit beside (NG = 1), or
-// the registers allow.
-__host__ __device__ constexpr int warps_of(int ng) { return ng == 1 ? 10 : 8; }
+// Warps of a block: as many as the rings and a partial result each fit beside, or the
+// registers allow (d = 128, NG = 2).
+__host__ __device__ constexpr int warps_of(int d, int ng) {
+  return d == 64 ? (ng == 1 ? 12 : 10) : ng == 1 ? 10 : 8;
+}
 __host__ __device__ constexpr int warp_bytes(int d, int ng) {
   return kRingBytes + frags(d, ng) * 32 * 4;
 }
@@ -423,10 +425,10 @@ struct Heads {
 };
 
 template <int D, int NG>
-__global__ void __launch_bounds__(warps_of(NG) * 32, 1) attn_decode_kernel(
+__global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
     const __grid_constant__ AttnDecodeArgs a, int rows, int groups, int ps_shift) {
   constexpr int S = stages(D), KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
-  constexpr int kWarps = warps_of(NG);
+  constexpr int kWarps = warps_of(D, NG);
   static_assert(NF * 32 * 4 <= kRingBytes && kWarps <= kMaxWarps, "a partial result fits the ring");
   extern __shared__ __align__(1024) uint8_t smem[];
   Keys* cached = reinterpret_cast<Keys*>(smem + kWarps * warp_bytes(D, NG));
@@ -952,7 +954,7 @@ cudaError_t launch_rows(const AttnDecodeArgs& a, long long vrows, int cluster, i
 
 template <int D, int NG>
 cudaError_t launch(AttnDecodeArgs a, int rows, int groups, cudaStream_t s) {
-  constexpr int kWarps = warps_of(NG);
+  constexpr int kWarps = warps_of(D, NG);
   constexpr int smem = kWarps * warp_bytes(D, NG) + kCachedRows * (int)sizeof(Keys);
   static int nsm[64] = {};
   int dev = 0;
@@ -968,7 +970,7 @@ cudaError_t launch(AttnDecodeArgs a, int rows, int groups, cudaStream_t s) {
     for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
   const long long vrows = (long long)rows * groups;
   const long long row_tiles = ((long long)a.max_pages * a.page_size + a.w + kTile - 1) / kTile;
-  a.read_once = (long long)rows * row_tiles * stage_bytes(D) > kL2Bytes / 2;
+  a.read_once = groups == 1 && (long long)rows * row_tiles * stage_bytes(D) > kL2Bytes / 2;
   const RowShape shape = row_shape(vrows, row_tiles);
   if (shape.warps == 4) return launch_rows<D, NG, 4>(a, vrows, shape.cluster, groups, shift, s);
   if (shape.warps == 2) return launch_rows<D, NG, 2>(a, vrows, shape.cluster, groups, shift, s);
