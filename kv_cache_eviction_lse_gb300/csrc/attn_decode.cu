@@ -6,14 +6,14 @@
 // (g flop/B; the tensor cores take over 200).
 //
 // Rows differ in length by the pruning, so the work is cut by tiles, not by rows: all rows'
-// tiles of 16 keys form one stream, every warp of a persistent grid takes an equal
+// tiles of 16 keys (32 at d = 64) form one stream, every warp of a persistent grid takes an equal
 // contiguous share, and a row that crosses a share's border is joined from partial sums
 // (running maximum, sum and weighted values): within a block through shared memory, between
 // blocks by a second kernel.  Shares depend on the lengths alone, so results do too.  Rows
 // that cannot be long take a block or cluster each instead (see row_shape).
 //
-// A warp streams its tiles through a private ring of two cp.async stages (four at d = 64;
-// 128-byte swizzle, no block barrier), across row borders: the loads of the next rows are in
+// A warp streams its tiles through a private ring of two cp.async stages (128-byte
+// swizzle, no block barrier), across row borders: the loads of the next rows are in
 // flight while a row is finished.  Ten warps with two stages reach 6.8 TB/s (96 sequences of
 // 16384 tokens, heads kept at 25 to 75 %: 363 us for 2.47 GB, 152 blocks); eight warps with
 // three stages take 377 us: more bytes in flight only lengthen every other load.  Short of
@@ -38,7 +38,9 @@ namespace {
 
 constexpr int kErrAttnDecode = 9;  // a length or page id out of range
 
-constexpr int kTile = 16;        // keys
+// Keys of a tile: 8 KB of K and V.  Half of that at d = 64 left the arithmetic's latency in
+// the way (96 x 16384 tokens: 72 % of the DRAM's rate).
+__host__ __device__ constexpr int tile_keys(int d) { return d == 128 ? 16 : 32; }
 constexpr int kMaxBlocks = 160;  // of the persistent grid; sizes the workspace
 constexpr int kMaxWarps = 16;    // of a block
 constexpr long long kL2Bytes = 129ll << 20;
@@ -48,9 +50,9 @@ constexpr int kMaxChunks = 256;  // of rows, in the scan of their tiles
 constexpr int kCachedRows = 512; // whose lengths a block keeps in shared memory
 constexpr float kSlack = 8.f;    // log2 of how far a weight may exceed the reference
 
-__host__ __device__ constexpr int stages(int d) { return d == 128 ? 2 : 4; }
-__host__ __device__ constexpr int stage_bytes(int d) { return 2 * kTile * d * 2; }
-constexpr int kRingBytes = stages(128) * stage_bytes(128);  // per warp, either d
+constexpr int kStages = 2;
+constexpr int kStageBytes = 2 * tile_keys(128) * 128 * 2;  // either d
+constexpr int kRingBytes = kStages * kStageBytes;          // per warp
 
 // A partial result of a row segment: O^T fragments [d / 16 * 4 * NG][32 lanes], then (in
 // the workspace) the reference and the sum of each of the 8 NG heads.
@@ -126,6 +128,7 @@ __device__ __forceinline__ int ring_pos(const AttnDecodeArgs& a, int row) {
 }
 
 // A place in the stream of tiles.  The lanes hold the lengths of the 32 rows from `base` on.
+template <int kTile>
 struct Cursor {
   int row, group, tile;   // group: which 8 NG of the row's query heads
   Keys keys;              // of the row
@@ -214,11 +217,12 @@ __device__ __forceinline__ void store_unit(const AttnDecodeArgs& a, int row, int
 }
 
 // The copies of a warp: finds where the keys of a tile lie, and brings their rows of K and V
-// into a stage of its ring.  Lane i (and i + 16) has key i of the tile.  The lanes keep 32
+// into a stage of its ring.  Lane i has key i (mod the tile) of the tile.  The lanes keep 32
 // entries of the row's block table from page tbase on; a load of more of them is used an
 // iteration later.
 template <int D>
 struct Copies {
+  static constexpr int kTile = tile_keys(D);
   const AttnDecodeArgs& a;
   const int ps_shift, lane;  // log2 of the page size, or -1
   const uint32_t ring_u;
@@ -227,7 +231,7 @@ struct Copies {
   int idx = 0, inside = 0;   // the key's page in the row, and its row in the page
 
   __device__ __forceinline__ void look_up(int row, int tile, const Keys& keys, bool new_row) {
-    const int first = tile * kTile, key = first + (lane & 15);
+    const int first = tile * kTile, key = first + lane % kTile;
     idx = ps_shift >= 0 ? key >> ps_shift : key / a.page_size;
     inside = key - idx * a.page_size;
     const int paged = min(kTile, keys.paged - first);  // keys of the tile in pages
@@ -243,7 +247,7 @@ struct Copies {
   }
 
   __device__ __forceinline__ void copy(int row, int tile, const Keys& keys, int stage) {
-    const int key0 = tile * kTile + (lane & 15);
+    const int key0 = tile * kTile + lane % kTile;
     const int page = __shfl_sync(0xffffffffu, entry, (idx - tbase) & 31);
     long long at_row = -1;  // row in the pool, or in the ring
     const bool in_ring = key0 >= keys.paged;
@@ -260,7 +264,7 @@ struct Copies {
     if (lane == 0) live[stage] = here;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a step
     const int c = lane % kLanes;
-    const uint32_t dst = ring_u + stage * stage_bytes(D);
+    const uint32_t dst = ring_u + stage * kStageBytes;
     const uint64_t policy = read_once_policy();
 #pragma unroll
     for (int i = 0; i < kTile / kRows; ++i) {
@@ -309,27 +313,35 @@ struct Heads {
 
   // One tile in shared memory (K at kb, V behind it) whose keys `here` are there.
   __device__ __forceinline__ void tile(uint32_t kb, uint32_t here, int lane) {
+    constexpr int kTile = tile_keys(D), M = kTile / 16;  // M rows of MMAs
     const float scale = rsqrtf((float)D) * kLog2e;
-    float x[NG][4] = {};
+    float x[M][NG][4] = {};
     {
       const int key = ((lane >> 3) & 1) * 8 + (lane & 7);
       const uint32_t row_u = kb + key * (D * 2);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        uint32_t k[4];
-        ldmatrix_x4(row_u + (((s * 2 + (lane >> 4)) ^ (key & 7)) << 4), k[0], k[1], k[2], k[3]);
 #pragma unroll
-        for (int j = 0; j < NG; ++j) mma_bf16_16816(x[j], k, q[j][s][0], q[j][s][1]);
+        for (int n = 0; n < M; ++n) {
+          uint32_t k[4];
+          ldmatrix_x4(row_u + n * (16 * D * 2) + (((s * 2 + (lane >> 4)) ^ (key & 7)) << 4), k[0],
+                      k[1], k[2], k[3]);
+#pragma unroll
+          for (int j = 0; j < NG; ++j) mma_bf16_16816(x[n][j], k, q[j][s][0], q[j][s][1]);
+        }
       }
     }
     bool raise = false;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
+    for (int n = 0; n < M; ++n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = (lane >> 2) + (i >> 1) * 8;
-        x[j][i] = (here >> key) & 1 ? x[j][i] * scale : -INFINITY;
-        raise |= x[j][i] > m[j][i & 1] + kSlack;
+      for (int j = 0; j < NG; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = n * 16 + (lane >> 2) + (i >> 1) * 8;
+          x[n][j][i] = (here >> key) & 1 ? x[n][j][i] * scale : -INFINITY;
+          raise |= x[n][j][i] > m[j][i & 1] + kSlack;
+        }
       }
     }
     if (__any_sync(0xffffffffu, raise)) {
@@ -337,11 +349,12 @@ struct Heads {
       for (int j = 0; j < NG; ++j) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float top = fmaxf(x[j][i], x[j][i + 2]);
+          float top = m[j][i];
+#pragma unroll
+          for (int n = 0; n < M; ++n) top = fmaxf(top, fmaxf(x[n][j][i], x[n][j][i + 2]));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          top = fmaxf(m[j][i], top);
           const float c = fast_exp2(m[j][i] - finite_ref(top));
           m[j][i] = top;
           l[j][i] *= c;
@@ -353,25 +366,32 @@ struct Heads {
         }
       }
     }
-    uint32_t pf[NG][2];
+    uint32_t pf[M][NG][2];
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      float p[4];
+    for (int n = 0; n < M; ++n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = fast_exp2(x[j][i] - finite_ref(m[j][i & 1]));
-      l[j][0] += p[0] + p[2];
-      l[j][1] += p[1] + p[3];
-      pf[j][0] = transpose8x8(pack2(p[0], p[1]));
-      pf[j][1] = transpose8x8(pack2(p[2], p[3]));
+      for (int j = 0; j < NG; ++j) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = fast_exp2(x[n][j][i] - finite_ref(m[j][i & 1]));
+        l[j][0] += p[0] + p[2];
+        l[j][1] += p[1] + p[3];
+        pf[n][j][0] = transpose8x8(pack2(p[0], p[1]));
+        pf[n][j][1] = transpose8x8(pack2(p[2], p[3]));
+      }
     }
     const int key = (lane >> 4) * 8 + (lane & 7);
     const uint32_t row_u = kb + (kTile + key) * (D * 2);
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      uint32_t v[4];
-      ldmatrix_x4_trans(row_u + (((s * 2 + ((lane >> 3) & 1)) ^ (key & 7)) << 4), v);
+    for (int n = 0; n < M; ++n) {
 #pragma unroll
-      for (int j = 0; j < NG; ++j) mma_bf16_16816(o[j][s], v, pf[j][0], pf[j][1]);
+      for (int s = 0; s < KS; ++s) {
+        uint32_t v[4];
+        ldmatrix_x4_trans(row_u + n * (16 * D * 2) +
+                              (((s * 2 + ((lane >> 3) & 1)) ^ (key & 7)) << 4), v);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) mma_bf16_16816(o[j][s], v, pf[n][j][0], pf[n][j][1]);
+      }
     }
   }
 
@@ -427,7 +447,8 @@ struct Heads {
 template <int D, int NG>
 __global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
     const __grid_constant__ AttnDecodeArgs a, int rows, int groups, int ps_shift) {
-  constexpr int S = stages(D), KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
+  constexpr int S = kStages, KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
+  constexpr int kTile = tile_keys(D);
   constexpr int kWarps = warps_of(D, NG);
   static_assert(NF * 32 * 4 <= kRingBytes && kWarps <= kMaxWarps, "a partial result fits the ring");
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -519,7 +540,7 @@ __global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
     const long long u0 = groups == 1 ? t0 : t0 / groups;  // in tiles of one group
     const int l0 = __ffs(__ballot_sync(0xffffffffu, lanes_incl > u0)) - 1;
     long long rel = u0 - __shfl_sync(0xffffffffu, lanes_incl - lane_tiles, l0);
-    Cursor ld;
+    Cursor<kTile> ld;
     ld.group = 0;
     if (few) {
       ld.base = 0;
@@ -560,7 +581,7 @@ __global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
       ld.group = (int)(off / nt);
       ld.tile = (int)(off - (long long)ld.group * nt);
     }
-    Cursor cur = ld;
+    Cursor<kTile> cur = ld;
     if (tid == 0) head_first = t0 - ld.tile;
 
     uint8_t* ring = smem + warp * warp_bytes(D, NG);
@@ -595,7 +616,7 @@ __global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
         stage = stage == S - 1 ? 0 : stage + 1;
         continue;
       }
-      heads.tile(ring_u + stage * stage_bytes(D), live[warp][stage], lane);
+      heads.tile(ring_u + stage * kStageBytes, live[warp][stage], lane);
       stage = stage == S - 1 ? 0 : stage + 1;
 
       const bool row_end = cur.at_row_end(), last = t + 1 == t1;
@@ -804,7 +825,7 @@ struct Sent { float x[8 * 32], ref[8], sum[8]; };
 template <int D, int NG, int W>
 __global__ void __launch_bounds__(W * 32, (NG == 1 ? 12 : 8) / W) attn_decode_row_kernel(
     const __grid_constant__ AttnDecodeArgs a, int groups, int ps_shift) {
-  constexpr int S = stages(D), KS = D / 16, NF = frags(D, NG), H = NG * 8;
+  constexpr int S = kStages, KS = D / 16, NF = frags(D, NG), H = NG * 8, kTile = tile_keys(D);
   static_assert(NF / 8 <= kMaxCluster && (NF & (NF - 1)) == 0, "units fit what is sent");
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t live[W][S];
@@ -838,7 +859,7 @@ __global__ void __launch_bounds__(W * 32, (NG == 1 ? 12 : 8) / W) attn_decode_ro
         copies.copy(row, next - 1, keys, stage == 0 ? S - 1 : stage - 1);
       cp_async_commit();
       if (next < t1) copies.look_up(row, next, keys, next == t0);
-      if (t >= t0) heads.tile(ring_u + stage * stage_bytes(D), live[warp][stage], lane);
+      if (t >= t0) heads.tile(ring_u + stage * kStageBytes, live[warp][stage], lane);
       stage = stage == S - 1 ? 0 : stage + 1;
     }
     cp_async_wait<0>();
@@ -954,7 +975,7 @@ cudaError_t launch_rows(const AttnDecodeArgs& a, long long vrows, int cluster, i
 
 template <int D, int NG>
 cudaError_t launch(AttnDecodeArgs a, int rows, int groups, cudaStream_t s) {
-  constexpr int kWarps = warps_of(D, NG);
+  constexpr int kWarps = warps_of(D, NG), kTile = tile_keys(D);
   constexpr int smem = kWarps * warp_bytes(D, NG) + kCachedRows * (int)sizeof(Keys);
   static int nsm[64] = {};
   int dev = 0;
@@ -970,7 +991,7 @@ cudaError_t launch(AttnDecodeArgs a, int rows, int groups, cudaStream_t s) {
     for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
   const long long vrows = (long long)rows * groups;
   const long long row_tiles = ((long long)a.max_pages * a.page_size + a.w + kTile - 1) / kTile;
-  a.read_once = groups == 1 && (long long)rows * row_tiles * stage_bytes(D) > kL2Bytes / 2;
+  a.read_once = groups == 1 && (long long)rows * row_tiles * kStageBytes > kL2Bytes / 2;
   const RowShape shape = row_shape(vrows, row_tiles);
   if (shape.warps == 4) return launch_rows<D, NG, 4>(a, vrows, shape.cluster, groups, shift, s);
   if (shape.warps == 2) return launch_rows<D, NG, 2>(a, vrows, shape.cluster, groups, shift, s);
