@@ -757,7 +757,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Ends end = static_cast<const Ends*>(a.ws)[blockIdx.x];
-  if (end.vrow < 0) return;
+  // the bounds hold even if another stream writes the workspace meanwhile
+  if ((uint32_t)end.vrow >= (uint32_t)(rows * groups) || (uint32_t)end.first >= blockIdx.x) return;
   const int n = blockIdx.x - end.first + 1;
   auto part = [&](int p) { return block_part(a.ws, end.first + p, p == 0 ? 1 : 0, PF); };
   const int f = blockIdx.y * kJoinThreads + threadIdx.x;

@@ -246,9 +246,10 @@ __device__ __forceinline__ Decision decide(const AppendArgs& a, const PlanView& 
 }
 
 // The plan has checked every page and table index; this holds also if another stream changes
-// the tables or token starts while the call runs, which nothing can make right.
-__device__ __forceinline__ bool inside(const AppendArgs& a, int idx, int page) {
-  if ((uint32_t)idx < (uint32_t)a.max_pages && (uint32_t)page < (uint32_t)a.capacity) return true;
+// tables, token starts or the workspace while the call runs, which nothing can make right.
+__device__ __forceinline__ bool inside(const AppendArgs& a, int slot, int idx, int page) {
+  if (slot >= 0 && (uint32_t)idx < (uint32_t)a.max_pages && (uint32_t)page < (uint32_t)a.capacity)
+    return true;
   atomicCAS(&g_append_error, 0, kErrAppend);
   return false;
 }
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 7) append_kernel(const __grid_consta
     const int used = (p.x + m) % a.page_size, last = (p.x + m) / a.page_size;
     if (used == 0 || last < have) return;
     const int pg = base[row >> plan_shift] + p.y + last - have;  // the unused rows of a new page
-    if (!inside(a, last, pg)) return;
+    if (!inside(a, min(p.x, p.x + m), last, pg)) return;
     const size_t at = ((size_t)pg * a.page_size + used) * D;
     const int chunks = (a.page_size - used) * (D / 8);
     for (int c = lane; c < chunks; c += 32) {
@@ -352,9 +353,9 @@ __global__ void __launch_bounds__(kThreads, 7) append_kernel(const __grid_consta
     const int cr = (at - n_q) * a.B + b;
     const int2 p = plan.rows[cr];
     const int slot = p.x + j, idx = slot / a.page_size, off = slot - idx * a.page_size;
-    if (!inside(a, idx, 0)) continue;
+    if (!inside(a, slot, idx, 0)) continue;
     const int pg = page_of(a, cr, p.x, base[cr >> plan_shift] + p.y, idx);
-    if (!inside(a, idx, pg)) continue;
+    if (!inside(a, slot, idx, pg)) continue;
     // a new page enters the table with the first of its rows that this call writes
     if (u == 0 && off == 0) a.block_table[(size_t)cr * a.max_pages + idx] = pg;
     const size_t to = ((size_t)pg * a.page_size + off) * D;
