@@ -128,15 +128,26 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   float c[8], s[8];
   if (ln.rotate) angles(r, u, r.pos[t], c, s);
   const int n_q = r.q ? r.L * r.Hq : 0, n_all = n_q + (r.k ? r.L * r.Hkv : 0);
-  for (int slab = blockIdx.y; slab < n_all; slab += gridDim.y) {
-    const bool is_q = slab < n_q;
-    const size_t row = ((size_t)(is_q ? slab : slab - n_q) * r.N + t) * D;
-    const uint4* in = reinterpret_cast<const uint4*>((is_q ? r.q : r.k) + row);
-    uint4* out = reinterpret_cast<uint4*>((is_q ? r.q_out : r.k_out) + row);
-    uint4 x0 = in[ln.c0], x1 = in[ln.c1];
-    if (ln.rotate) rotate(x0, x1, c, s, r.interleaved);
-    out[ln.c0] = x0;
-    out[ln.c1] = x1;
+  auto row_at = [&](int slab) {
+    return ((size_t)(slab < n_q ? slab : slab - n_q) * r.N + t) * D;
+  };
+  uint4 x0, x1;
+  auto load = [&](int slab) {
+    const uint4* in = reinterpret_cast<const uint4*>((slab < n_q ? r.q : r.k) + row_at(slab));
+    x0 = in[ln.c0];
+    x1 = in[ln.c1];
+  };
+  int slab = blockIdx.y;
+  if (slab < n_all) load(slab);
+  while (slab < n_all) {
+    const int at = slab;
+    uint4 y0 = x0, y1 = x1;
+    slab += gridDim.y;
+    if (slab < n_all) load(slab);
+    if (ln.rotate) rotate(y0, y1, c, s, r.interleaved);
+    uint4* out = reinterpret_cast<uint4*>((at < n_q ? r.q_out : r.k_out) + row_at(at));
+    out[ln.c0] = y0;
+    out[ln.c1] = y1;
   }
 }
 
@@ -368,12 +379,17 @@ __global__ void __launch_bounds__(kThreads, 7) append_kernel(const __grid_consta
   }
 }
 
-// Blocks per group of tokens: a thread walks several heads with one set of angles, in about
-// `waves` times the 16 blocks of an SM.  A 16384-token prompt of 2 layers turns in 102.2,
-// 100.4, 99.2 and 171 us with 2, 4, 8 and 32; a chunk of 8192 tokens in 4 layers is appended
-// in 126.7, 128.2 and 131.6 us with 2, 3 and 6.
+// Blocks per group of tokens: a thread walks at least four heads with one set of angles (one
+// would spend more time on those than on the rows) while that leaves a quarter of the SMs'
+// 16 blocks each, and otherwise in about `waves` times those 16.  One layer of 4096 tokens, 32
+// and 8 heads, takes 25.8 us with a head a thread and 16.8 with four; 2079 tokens of 14 heads
+// 6.2 and 4.9; a 16384-token prompt of 2 layers 102.2, 100.4, 99.2 and 171 us in 2, 4, 8 and
+// 32 waves, a chunk of 8192 tokens in 4 layers 126.7, 128.2 and 131.6 us in 2, 3 and 6.
 int slab_groups(int token_blocks, int slabs, int waves) {
+  const int fill = (152 * 4 + token_blocks - 1) / token_blocks;
   int groups = (152 * 16 * waves + token_blocks - 1) / token_blocks;
+  groups = groups < slabs / 4 ? groups : slabs / 4;
+  if (groups < fill) groups = fill;
   return groups < 1 ? 1 : groups > slabs ? slabs : groups > 65535 ? 65535 : groups;
 }
 
