@@ -443,9 +443,10 @@ kvs_status kvs_compact_paged_multi(const kvs_dims* dims, const kvs_bf16* k, cons
  * where (a, b) are dimensions (i, i + rot_dim / 2) with interleaved == 0 and
  * (2 i, 2 i + 1) otherwise; dimensions from rot_dim on are copied.  Whole turns are taken
  * off without loss at any position, so the angle is good to 2^-22 radians (the fp32
- * resolution of [-pi, pi]) for |pos * inv_freq| up to 2^27; the products are fp32, and each
- * result is rounded to bf16 once.  Negated frequencies undo a rotation; since a rotation is orthogonal, the
- * same call on the gradients of the outputs gives the gradients of the inputs.
+ * resolution of [-pi, pi]) for |pos * inv_freq| up to 2^27, its cosine and sine to 2^-21; the
+ * products are fp32, and each result is rounded to bf16 once.  Negated frequencies undo a
+ * rotation; since a rotation is orthogonal, the same call on the gradients of the outputs
+ * gives the gradients of the inputs.
  *
  *   pos        [N]             int32; any value
  *   inv_freq   [rot_dim / 2]   double in HOST memory, radians per position, finite; read

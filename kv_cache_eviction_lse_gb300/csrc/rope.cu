@@ -7,9 +7,9 @@
 // product that wraps where the angle does: the angle of any 32-bit position is exact to
 // p 2^-65 turns and needs no range reduction (a 32-bit product would be off by 0.01 rad at
 // position 131072).  In [-pi, pi] the hardware's sine and cosine are good to 2^-21, far
-// below the bf16 rounding of the result (2^-8 relative), and shorten small batches (2079
-// tokens of 14 heads 6.5 -> 5.9 us against sincospif).  The products are fp32, and each
-// result is rounded to bf16 once.
+// below the bf16 rounding of the result (2^-8 relative); sincospif took a tenth longer where
+// a thread has one head (2079 tokens of 14 heads 6.5 against 5.9 us).  The products are
+// fp32, and each result is rounded to bf16 once.
 //
 // Bound by HBM (or, for a few tokens, by latency): every row is read and written once, and
 // a thread that has the cosines and sines of its token's 8 pairs reuses them for the heads

@@ -3,8 +3,8 @@ fp64 oracle, at the sizes and states where they can go wrong, and their use toge
 
 Tolerances, from the arithmetic (u = 2^-24, an fp32 rounding; 2^-8, a bf16 rounding):
   rotation   |err| <= 2^-8 |y| + 2^-20 (|a| + |b|): the output's rounding; the angle is good
-             to 2^-22, cosine and sine to 2 ulp, and the two products and their sum add
-             three roundings (together below 2^-20 of the pair's size)
+             to 2^-22, the hardware's cosine and sine of it to 2^-21.2, and the two products
+             and their sum add three fp32 roundings (together below 2^-20 of the pair's size)
   attention  logits: |dx| <= delta = (d + 8) u max_i sum_e |q_e k_ie| / sqrt(d) + 2^-20 |x|max
              (fp32 sums in any order, the scale by log2 e, ex2 to 2^-22)
              lse: delta + 2^-20 (1 + |lse|) + (n / 8 + 16) u (sums of positive terms: at most
