@@ -1028,9 +1028,13 @@ size_t attn_decode_workspace_bytes(int rows, int group, int d) {
   return ends_bytes() + (size_t)kMaxBlocks * 2 * part_floats(d, ng) * sizeof(float);
 }
 
-cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t s) {
+cudaError_t launch_attn_decode(const AttnDecodeArgs& args, cudaStream_t s) {
+  AttnDecodeArgs a = args;
   const int rows = a.L * a.Hkv * a.B, g = a.Hq / a.Hkv;
   if (rows == 0) return cudaSuccess;
+  // a copy of no bytes still names an address: one that is there
+  if (!a.k_pages) a.k_pages = a.v_pages = a.q;
+  if (!a.ring_k) a.ring_k = a.ring_v = a.q;
   // groups of 8 heads fill an MMA's N; above 8 a pass takes 16, so that K and V are read
   // once for up to 16 heads
   if (g <= 8)

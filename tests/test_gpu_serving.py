@@ -557,6 +557,33 @@ def test_attend(C, name, room):
     assert np.array_equal(bits(o2), bits(o))
 
 
+@pytest.mark.parametrize("room", [1, 100000], ids=["tight", "wide"])
+def test_attend_with_an_empty_pool(C, room):
+    """No pool at all (NULL pages, capacity 0): the ring's keys alone, or none."""
+    c = attend_case(C, L=1, Hq=4, H=2, B=3, d=128, ps=16, n=0, w=7, pos=[0, 3, 9], seed=3, room=room)
+    g = {n: c[n].cuda() for n in ("q", "bt", "sl", "pos", "rk", "rv")}
+    o, z = torch.full_like(g["q"], 9.0), torch.full(c["q"].shape[:3], 9.0, device="cuda")
+    nb = C.kvs_attn_decode_workspace_size(c["dm"], c["B"])
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    C.kvs_attn_decode(c["dm"], c["B"], g["q"], c["ps"], None, None, 0, g["bt"], c["mp"], g["sl"], 7,
+                      g["pos"], g["rk"], g["rv"], o, z, ws, nb)
+    torch.cuda.synchronize()
+    assert C.kvs_device_error(clear=True) == 0
+    check_attend(c, o.cpu(), z.cpu())
+
+
+def test_binding_refuses_strided_tensors(C):
+    """The layouts are dense: a transposed or sliced tensor is refused by name."""
+    dm = C.dims(1, 2, 2, 64)
+    x = torch.zeros(1, 2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(8, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        C.kvs_rope(dm, 4, pos, 0, None, False, x[..., :64], y, None, None)
+    with pytest.raises(ValueError, match="contiguous"):
+        C.kvs_rope(dm, 4, pos[::2], 64, [1.0] * 32, False, y, y, None, None)
+
+
 @pytest.mark.parametrize("room", [0, 100000], ids=["tight", "wide"])
 def test_attend_minus_infinity_and_nan_stay_in_their_row(C, room):
     """Logits of -inf weigh nothing (a row of nothing else is an empty one); a NaN key gives
