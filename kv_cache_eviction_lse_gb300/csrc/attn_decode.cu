@@ -15,7 +15,7 @@
 // A warp streams its tiles through a private ring of two cp.async stages (128-byte
 // swizzle, no block barrier), across row borders: the loads of the next rows are in
 // flight while a row is finished.  Ten warps with two stages reach 6.8 TB/s (96 sequences of
-// 16384 tokens, heads kept at 25 to 75 %: 363 us for 2.47 GB, 152 blocks); eight warps with
+// 16384 tokens, heads kept at 25 to 75 %: 361 us for 2.47 GB, 152 blocks); eight warps with
 // three stages take 377 us: more bytes in flight only lengthen every other load.  Short of
 // that, about 9 us of a call is latency (scan of the lengths, table, first tile, joins).
 // Per tile (mma.m16n8k16, keys in M, heads in N, bf16 -> fp32):
@@ -464,6 +464,8 @@ __global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
   __shared__ long long head_first;  // the first tile of warp 0's first row
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.Hq / a.Hkv;
+  // started beside the end of the kernel before; the join must not start beside that one too
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
 
   if (tid == 0) heads_m = ends_m = tails_m = 0;
@@ -835,6 +837,7 @@ __global__ void __launch_bounds__(W * 32, (NG == 1 ? 12 : 8) / W) attn_decode_ro
   const int g = a.Hq / a.Hkv;
   const int blocks = cluster_size(), rank = blockIdx.x % blocks;
   const int vrow = blockIdx.x / blocks, row = vrow / groups, group = vrow - row * groups;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // started beside the kernel before
   const int len = a.seq_lens[row];
   const Keys keys = keys_of(a, len, ring_pos(a, row));
   if (tid == 0 && rank == 0 && keys.paged != len) atomicCAS(&g_attn_decode_error, 0, kErrAttnDecode);
@@ -964,12 +967,14 @@ cudaError_t launch_rows(const AttnDecodeArgs& a, long long vrows, int cluster, i
   cfg.blockDim = dim3(W * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   count_launches(1);
   return cudaLaunchKernelEx(&cfg, attn_decode_row_kernel<D, NG, W>, a, groups, shift);
 }
@@ -1004,19 +1009,22 @@ cudaError_t launch(AttnDecodeArgs a, int rows, int groups, cudaStream_t s) {
                            smem);
   if (e != cudaSuccess) return e;
   count_launches(2);
-  attn_decode_kernel<D, NG><<<blocks, kWarps * 32, smem, s>>>(a, rows, groups, shift);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the join's blocks come up while the first kernel runs and wait for its results
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, frags(D, NG) * 32 / kJoinThreads);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NG>, a, rows, groups, shift);
+  if (e != cudaSuccess) return e;
+  // the join's blocks come up while the first kernel runs and wait for its results
+  cfg.gridDim = dim3(blocks, frags(D, NG) * 32 / kJoinThreads);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, NG>, a, rows, groups);
 }
 

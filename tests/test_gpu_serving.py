@@ -687,6 +687,74 @@ def test_two_calls_at_once(C, room):
         assert torch.equal(run[2].cpu(), o)
 
 
+def test_calls_that_follow_other_streams(C):
+    """Rotations on two streams that a third joins by events, then the append and the attention
+    there, eager and captured, after a memset and a library kernel of torch's: every call
+    starts from what came before it, wherever that ran (the kernels may start early)."""
+    L, Hq, H, B, d, ps, n = 1, 8, 2, 3, 128, 16, 700
+    gen = torch.Generator().manual_seed(12)
+    dm, f = C.dims(L, Hq, H, d), freqs(d)
+    rnd = lambda *s: torch.randn(*s, generator=gen).to(torch.bfloat16).cuda()  # noqa: E731
+    c = attend_case(C, L=L, Hq=Hq, H=H, B=B, d=d, ps=ps, n=n, seed=12, room=5000)
+    src = {"kp": c["kp"].cuda(), "vp": c["vp"].cuda(), "bt": c["bt"].cuda(), "sl": c["sl"].cuda()}
+    src["kp"] = torch.cat([src["kp"], torch.zeros_like(src["kp"])])
+    src["vp"] = torch.cat([src["vp"], torch.zeros_like(src["vp"])])
+    cap, nxt0 = len(src["kp"]), int(c["nxt"])
+    q0, k0, v0 = rnd(L, Hq, B, d), rnd(L, H, B, d), rnd(L, H, B, d)
+    pos = torch.tensor([900, 5, 70000], dtype=torch.int32, device="cuda")
+    g = {k: v.clone() for k, v in src.items()}
+    nxt = torch.full((1,), nxt0, dtype=torch.int32, device="cuda")
+    q, k, o = torch.empty_like(q0), torch.empty_like(k0), torch.empty_like(q0)
+    na, nd = C.kvs_append_paged_workspace_size(dm, B), C.kvs_attn_decode_workspace_size(dm, B)
+    wa = torch.empty(na, dtype=torch.uint8, device="cuda")
+    wd = torch.empty(nd, dtype=torch.uint8, device="cuda")
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+
+    def work():
+        main = torch.cuda.current_stream()
+        for x in g:
+            g[x].copy_(src[x])
+        nxt.fill_(nxt0)
+        o.zero_()
+        for s, (x, y, which) in zip(sides, ((q0, q, 0), (k0, k, 1))):
+            s.wait_stream(main)
+            with torch.cuda.stream(s):
+                y.copy_(x * 2)                    # a kernel of torch's before the early starter
+                a = (y, y, None, None) if which == 0 else (None, None, y, y)
+                C.kvs_rope(dm, B, pos, d, f, False, *a)
+        for s in sides:
+            main.wait_stream(s)
+        C.kvs_append_paged(dm, B, B, None, None, 0, None, False, None, None, k, v0, ps, g["kp"],
+                           g["vp"], cap, nxt, nxt, g["bt"], c["mp"], g["sl"], g["sl"], wa, na)
+        C.kvs_attn_decode(dm, B, q, ps, g["kp"], g["vp"], cap, g["bt"], c["mp"], g["sl"], 0, None,
+                          None, None, o, None, wd, nd)
+        return o + 0                              # and one behind it
+
+    def check(out):
+        torch.cuda.synchronize()
+        assert C.kvs_device_error(clear=True) == 0
+        assert (g["sl"] == n + 1).all()
+        want, _, spread = O.attn_decode(f64(q), f64(g["kp"]), f64(g["vp"]), ps, g["bt"].cpu().numpy(),
+                                        g["sl"].cpu().numpy())
+        err = np.abs(f64(out) - want)
+        assert (err <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 1e-3) * spread).all()
+        check_rotated(q, (q0 * 2).cpu(), pos.cpu().numpy(), d, f, False, "q")
+
+    first = work()
+    check(first)
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = work()
+    for _ in range(3):
+        for x in (q, k, o, *g.values()):
+            x.zero_()
+        graph.replay()
+        check(out)
+        assert torch.equal(out, first)
+
+
 # ----------------------------------------------------------------------------- together
 
 def test_prompt_pruned_then_decoded(C):
