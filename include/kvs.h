@@ -529,7 +529,8 @@ kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const in
  *   pos    [B] int32;  ring_k, ring_v [L][H_kv][B][w][d] bf16   (NULL with w == 0)
  *   ws     scratch of kvs_attn_decode_workspace_size() bytes; calls that may overlap on
  *          the GPU need their own
- * With B = 1 the pages are those of kvs_compact_paged as they are.
+ * No output and no workspace overlaps another tensor.  With B = 1 the pages are those of
+ * kvs_compact_paged as they are.
  * ------------------------------------------------------------------------------- */
 size_t kvs_attn_decode_workspace_size(const kvs_dims* dims, int32_t B);
 kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, int32_t page_size,

@@ -958,9 +958,12 @@ RowShape row_shape(long long vrows, long long row_tiles) {
 template <int D, int NG, int W>
 cudaError_t launch_rows(const AttnDecodeArgs& a, long long vrows, int cluster, int groups, int shift,
                         cudaStream_t s) {
-  const int smem = W * kRingBytes + (cluster > 1 ? kMaxCluster * (int)sizeof(Sent) : 0);
+  constexpr int sent = kMaxCluster * (int)sizeof(Sent);
+  const int smem = W * kRingBytes + (cluster > 1 ? sent : 0);
+  // the same limit whatever this call needs: another thread may launch the other form
   cudaError_t e = cudaFuncSetAttribute(attn_decode_row_kernel<D, NG, W>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       W * kRingBytes + sent);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(vrows * cluster));

@@ -12,6 +12,8 @@ Tolerances, from the arithmetic (u = 2^-24, an fp32 rounding; 2^-8, a bf16 round
              o: 2^-8 |o| (output) + (2^-8 + 2.1 delta + (n + 32) u) sum a |v| (weights rounded
              to bf16, their error from the logits in numerator and denominator, the sums)
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -685,6 +687,87 @@ def test_two_calls_at_once(C, room):
     torch.cuda.synchronize()
     for (o, _), run in zip(alone, runs):
         assert torch.equal(run[2].cpu(), o)
+
+
+def test_calls_of_two_threads(C):
+    """Host threads that launch rows of one block and rows of clusters, each on a stream of its
+    own: neither changes the other's launch."""
+    cases = [attend_case(C, L=1, Hq=2, H=2, B=150, d=128, ps=16, n=9, seed=1, room=600),
+             attend_case(C, L=1, Hq=2, H=2, B=2, d=128, ps=16, n=100, seed=2, room=1500)]
+    alone = [call_attend(c)[0] for c in cases]
+    outs, failed = [], []
+
+    def calls(c, g, o, ws, nb, s):
+        try:
+            for _ in range(400):
+                C.kvs_attn_decode(c["dm"], c["B"], g["q"], c["ps"], g["kp"], g["vp"], c["cap"],
+                                  g["bt"], c["mp"], g["sl"], 0, None, None, None, o, None, ws, nb,
+                                  stream=s)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = []
+    for c in cases:
+        g = {n: c[n].cuda() for n in ("q", "kp", "vp", "bt", "sl")}
+        nb = C.kvs_attn_decode_workspace_size(c["dm"], c["B"])
+        outs.append(torch.empty_like(g["q"]))
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        threads.append(threading.Thread(target=calls, args=(c, g, outs[-1], ws, nb,
+                                                            torch.cuda.Stream())))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for o, want in zip(outs, alone):
+        assert torch.equal(o.cpu(), want)
+
+
+@pytest.mark.parametrize("room", [0, 100000], ids=["tight", "wide"])
+def test_chain_without_gaps_gives_what_separate_calls_give(C, room):
+    """Rotation in place, append and attention behind one another on the same few buffers, each
+    starting while the one before it ends: the same bits as with a synchronisation between."""
+    L, Hq, H, B, d, ps, steps = 2, 8, 2, 6, 128, 16, 40
+    gen = torch.Generator().manual_seed(21)
+    dm, f = C.dims(L, Hq, H, d), freqs(d)
+    rnd = lambda *s: torch.randn(*s, generator=gen).to(torch.bfloat16).cuda()  # noqa: E731
+    mp = max(8, -(-room // ps))
+    cap = L * H * B * (steps // ps + 1)
+    q0, k0, v = rnd(L, Hq, B, d), rnd(L, H, B, d), rnd(L, H, B, d)
+    pos = torch.arange(1, B + 1, dtype=torch.int32, device="cuda") * 37
+    na, nd = C.kvs_append_paged_workspace_size(dm, B), C.kvs_attn_decode_workspace_size(dm, B)
+    wa = torch.empty(na, dtype=torch.uint8, device="cuda")
+    wd = torch.empty(nd, dtype=torch.uint8, device="cuda")
+
+    def run(between):
+        q, k = q0.clone(), k0.clone()
+        kp = torch.zeros(cap, ps, d, dtype=torch.bfloat16, device="cuda")
+        vp = torch.zeros_like(kp)
+        bt = torch.full((L, H, B, mp), -1, dtype=torch.int32, device="cuda")
+        sl = torch.zeros(L, H, B, dtype=torch.int32, device="cuda")
+        nxt = torch.zeros(1, dtype=torch.int32, device="cuda")
+        o = torch.empty(steps, *q0.shape, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):  # queries and keys turn on from step to step
+            C.kvs_rope(dm, B, pos, d, f, False, q, q, k, k)
+            between()
+            C.kvs_append_paged(dm, B, B, None, None, 0, None, False, None, None, k, v, ps, kp, vp,
+                               cap, nxt, nxt, bt, mp, sl, sl, wa, na)
+            between()
+            C.kvs_attn_decode(dm, B, q, ps, kp, vp, cap, bt, mp, sl, 0, None, None, None, o[i], None,
+                              wd, nd)
+            between()
+        torch.cuda.synchronize()
+        return o, kp, vp, bt, sl, nxt, k, q
+
+    want = run(torch.cuda.synchronize)
+    assert (want[4] == steps).all() and C.kvs_device_error(clear=True) == 0
+    for _ in range(3):
+        for x, y in zip(run(lambda: None), want):
+            assert torch.equal(x, y)
+    assert C.kvs_device_error(clear=True) == 0
 
 
 def test_calls_that_follow_other_streams(C):
