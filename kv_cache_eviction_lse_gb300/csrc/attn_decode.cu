@@ -732,17 +732,10 @@ __global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
   }
 }
 
-// Rows that cross blocks: block x joins the row that ends in block x of the first kernel,
-// from the tail of its first block and the heads of those after.  Rows without keys, which
-// no block of the first kernel meets, are written here too.
-template <int D, int NG>
-__global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
-    const __grid_constant__ AttnDecodeArgs a, int rows, int groups) {
-  constexpr int KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
-  constexpr int kFirst = 24;  // parts whose loads start before the weights are known
-  __shared__ float ref_s[kMaxBlocks][NG * 8], sum_s[kMaxBlocks][NG * 8];
-  const int g = a.Hq / a.Hkv;
-  // while the first kernel runs: the outputs of rows without keys, and lengths out of range
+// While the first kernel runs: the outputs of rows without keys, which no block of it meets,
+// and lengths out of range.
+template <int D>
+__device__ __forceinline__ void rows_without_keys(const AttnDecodeArgs& a, int rows, int g) {
   const int every = gridDim.x * gridDim.y * kJoinThreads;
   for (int r = (blockIdx.y * gridDim.x + blockIdx.x) * kJoinThreads + threadIdx.x; r < rows;
        r += every) {
@@ -757,6 +750,20 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
       }
     }
   }
+}
+
+// Rows that cross blocks: block x joins the row that ends in block x of the first kernel,
+// from the tail of its first block and the heads of those after.  Registers for six blocks an
+// SM let one come up beside each block of the first kernel; six parts with their loads early
+// instead of 24, which spilled at d = 64: 36.2 -> 35.1 us for 384 rows of 131 tiles.
+template <int D, int NG>
+__global__ void __launch_bounds__(kJoinThreads, 6) attn_decode_join_kernel(
+    const __grid_constant__ AttnDecodeArgs a, int rows, int groups) {
+  constexpr int KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
+  constexpr int kFirst = 6;  // parts whose loads start before the weights are known
+  __shared__ float ref_s[kMaxBlocks][NG * 8], sum_s[kMaxBlocks][NG * 8];
+  const int g = a.Hq / a.Hkv;
+  rows_without_keys<D>(a, rows, g);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Ends end = static_cast<const Ends*>(a.ws)[blockIdx.x];
   // the bounds hold even if another stream writes the workspace meanwhile
@@ -795,6 +802,80 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(
   }
   const int row = end.vrow / groups;
   const int head = (end.vrow - row * groups) * NG * 8 + h;
+  if (head < g) store_out<D>(a, out_row(a, row, g, head), dim, acc, top, sum);
+}
+
+// The same for few rows, each over many blocks: a block per row and fragment, whose warps
+// take every eighth part and meet in shared memory, so that the parts' loads come in one or a
+// few rounds.  Against the kernel above (us): one row of 16384 tokens over 103 blocks 9.5 /
+// 14.6, of 262144 over 152 32.0 / 34.5; 4 rows over 38 12.3 / 13.6; 8 rows of a 131072-token
+// document over 19 29.7 / 30.9; 16 rows over 9 18.8 / 19.6; 32 rows over 5 66.5 / 66.1.
+template <int D, int NG>
+__global__ void __launch_bounds__(kJoinThreads) attn_decode_join_few_kernel(
+    const __grid_constant__ AttnDecodeArgs a, int rows, int groups, int blocks) {
+  constexpr int KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
+  constexpr int kWarps = kJoinThreads / 32, kAhead = 4;
+  __shared__ float acc_s[kWarps][32], top_s[kWarps][32], sum_s[kWarps][32];
+  __shared__ int last_s, first_s;
+  static_assert(kMaxBlocks <= kJoinThreads, "a thread per block of the first kernel");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = a.Hq / a.Hkv;
+  if (threadIdx.x == 0) last_s = first_s = 0;
+  rows_without_keys<D>(a, rows, g);
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int vrow = blockIdx.x;
+  if ((int)threadIdx.x < blocks) {
+    const Ends end = static_cast<const Ends*>(a.ws)[threadIdx.x];
+    if (end.vrow == vrow) { last_s = threadIdx.x; first_s = end.first; }
+  }
+  __syncthreads();
+  const int last = last_s, first = first_s;
+  // the bounds hold even if another stream writes the workspace meanwhile
+  if ((uint32_t)first >= (uint32_t)last) return;  // (also: the row crosses no blocks)
+  const int n = last - first + 1;
+  const int f = blockIdx.y, j = f / (KS * 4), s = f / 4 % KS, c = f % 4;
+  const int h = j * 8 + (lane & 3) * 2 + (c & 1), dim = s * 16 + (lane >> 2) + (c >> 1) * 8;
+  float top = -INFINITY, acc = 0.f, sum = 0.f;
+  for (int p0 = warp; p0 < n; p0 += kAhead * kWarps) {
+    float x[kAhead], ref[kAhead], part_sum[kAhead], high = top;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int p = p0 + i * kWarps;
+      const float* from = block_part(a.ws, first + min(p, n - 1), p == 0 ? 1 : 0, PF);
+      x[i] = from[f * 32 + lane];
+      ref[i] = p < n ? from[NF * 32 + h] : -INFINITY;
+      part_sum[i] = from[NF * 32 + NG * 8 + h];
+      if (p >= n) x[i] = part_sum[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) high = fmaxf(high, ref[i]);
+    const float base = finite_ref(high), w = fast_exp2(top - base);
+    acc *= w;
+    sum *= w;
+    top = high;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float v = fast_exp2(ref[i] - base);
+      acc += x[i] * v;
+      sum += part_sum[i] * v;
+    }
+  }
+  acc_s[warp][lane] = acc;
+  top_s[warp][lane] = top;
+  sum_s[warp][lane] = sum;
+  __syncthreads();
+  if (warp) return;
+  top = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < kWarps; ++v) top = fmaxf(top, top_s[v][lane]);
+  acc = sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < kWarps; ++v) {
+    const float w = fast_exp2(top_s[v][lane] - finite_ref(top));
+    acc += acc_s[v][lane] * w;
+    sum += sum_s[v][lane] * w;
+  }
+  const int row = vrow / groups, head = (vrow - row * groups) * NG * 8 + h;
   if (head < g) store_out<D>(a, out_row(a, row, g, head), dim, acc, top, sum);
 }
 
@@ -1025,9 +1106,13 @@ cudaError_t launch(AttnDecodeArgs a, int rows, int groups, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NG>, a, rows, groups, shift);
   if (e != cudaSuccess) return e;
   // the join's blocks come up while the first kernel runs and wait for its results
-  cfg.gridDim = dim3(blocks, frags(D, NG) * 32 / kJoinThreads);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
+  if (vrows * 8 <= blocks) {
+    cfg.gridDim = dim3((unsigned)vrows, frags(D, NG));
+    return cudaLaunchKernelEx(&cfg, attn_decode_join_few_kernel<D, NG>, a, rows, groups, blocks);
+  }
+  cfg.gridDim = dim3(blocks, frags(D, NG) * 32 / kJoinThreads);
   return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, NG>, a, rows, groups);
 }
 
