@@ -168,6 +168,25 @@ struct Cursor {
   }
 };
 
+// The equal contiguous shares of `warps` warps of a stream of tiles; the first `more` have one
+// more than `each`.
+struct Shares {
+  long long each = 1, more = 0;
+  __device__ __forceinline__ Shares(long long total, int warps) {
+    if (total > warps) {
+      each = total <= UINT32_MAX ? (uint32_t)total / (uint32_t)warps : total / warps;
+      more = total - each * warps;
+    }
+  }
+  __device__ __forceinline__ long long first(int warp) const {  // tile of a warp
+    return warp * each + min((long long)warp, more);
+  }
+  __device__ __forceinline__ long long of(long long tile) const {  // warp of a tile
+    const long long wide = more * (each + 1);
+    return tile < wide ? tile / (each + 1) : more + (tile - wide) / each;
+  }
+};
+
 // Output rows of the 8 NG heads of a group: element offset of head h's row.
 __device__ __forceinline__ size_t out_row(const AttnDecodeArgs& a, int row, int g, int head) {
   return ((size_t)(row / a.B) * g + head) * a.B + row % a.B;
@@ -522,13 +541,8 @@ __global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
     if (lane >= o) lanes_incl += y;
   }
   const long long total = __shfl_sync(0xffffffffu, lanes_incl, 31) * groups;
-  const int most = gridDim.x * kWarps;
-  long long share_base = 1, share_rem = 0;  // tiles a warp; the first `rem` take one more
-  if (total > most) {
-    share_base = total <= UINT32_MAX ? (uint32_t)total / (uint32_t)most : total / most;
-    share_rem = total - share_base * most;
-  }
-  const long long warps = min((long long)most, total);
+  const Shares shares(total, gridDim.x * kWarps);
+  const long long warps = min((long long)gridDim.x * kWarps, total);
   const int gw = blockIdx.x * kWarps + warp;
   Ends* ends = static_cast<Ends*>(a.ws);
   if (blockIdx.x * kWarps >= warps) {
@@ -537,8 +551,8 @@ __global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
   }
 
   if (gw < warps) {
-    const long long t0 = gw * share_base + min((long long)gw, share_rem);
-    long long t1 = t0 + share_base + (gw < share_rem);
+    const long long t0 = shares.first(gw);
+    long long t1 = shares.first(gw + 1);
     const long long u0 = groups == 1 ? t0 : t0 / groups;  // in tiles of one group
     const int l0 = __ffs(__ballot_sync(0xffffffffu, lanes_incl > u0)) - 1;
     long long rel = u0 - __shfl_sync(0xffffffffu, lanes_incl - lane_tiles, l0);
@@ -662,13 +676,8 @@ __global__ void __launch_bounds__(warps_of(D, NG) * 32, 1) attn_decode_kernel(
   const uint32_t starts = (heads & 1) | (tails_m << 1);
   if (tid == 0) {
     Ends e = {-1, 0};
-    if ((heads & 1) && (ends_m & (stop & -stop))) {
-      // the warp of the row's first tile
-      const long long wide = share_rem * (share_base + 1);
-      const long long fw = head_first < wide ? head_first / (share_base + 1)
-                                             : share_rem + (head_first - wide) / share_base;
-      e = {vrow_of[0], (int)(fw / kWarps)};
-    }
+    if ((heads & 1) && (ends_m & (stop & -stop)))
+      e = {vrow_of[0], (int)(shares.of(head_first) / kWarps)};
     ends[blockIdx.x] = e;
   }
   // a warp takes a chain, or with few chains a slice of one, eight fragments at a time with
@@ -825,32 +834,37 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attn_decode_join_kernel(
 
 // The same for few rows, each over many blocks: a block per row and fragment, whose warps
 // take every eighth part and meet in shared memory, so that the parts' loads come in one or a
-// few rounds.  Against the kernel above (us): one row of 16384 tokens over 103 blocks 9.5 /
-// 14.6, of 262144 over 152 32.0 / 34.5; 4 rows over 38 12.3 / 13.6; 8 rows of a 131072-token
-// document over 19 29.7 / 30.9; 16 rows over 9 18.8 / 19.6; 32 rows over 5 66.5 / 66.1.
+// few rounds; which parts they are it works out while the first kernel runs.  Against the
+// kernel above (us): one row of 16384 tokens over 103 blocks 9.1 / 14.6, of 262144 over 152
+// 30.7 / 34.5; 4 rows over 38 11.9 / 13.6; 8 rows of a 131072-token document over 19 29.6 /
+// 30.9; 16 rows over 9 19.1 / 19.6; with the parts read from the first kernel's word on each
+// border instead 9.5, 32.4, 12.4, 29.9 and 18.8.  32 rows over 5 take 66.5 / 66.1.
 template <int D, int NG>
 __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_few_kernel(
     const __grid_constant__ AttnDecodeArgs a, int rows, int groups, int blocks) {
   constexpr int KS = D / 16, PF = part_floats(D, NG), NF = frags(D, NG);
   constexpr int kWarps = kJoinThreads / 32, kAhead = 4;
   __shared__ float acc_s[kWarps][32], top_s[kWarps][32], sum_s[kWarps][32];
-  __shared__ int last_s, first_s;
-  static_assert(kMaxBlocks <= kJoinThreads, "a thread per block of the first kernel");
+  static_assert(kMaxBlocks / 8 <= 32, "a lane per row");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = a.Hq / a.Hkv;
-  if (threadIdx.x == 0) last_s = first_s = 0;
   rows_without_keys<D>(a, rows, g);
-  __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int vrow = blockIdx.x;
-  if ((int)threadIdx.x < blocks) {
-    const Ends end = static_cast<const Ends*>(a.ws)[threadIdx.x];
-    if (end.vrow == vrow) { last_s = threadIdx.x; first_s = end.first; }
+  // while the first kernel runs: its blocks that share this row, by the same arithmetic
+  const int vrow = blockIdx.x, row = vrow / groups;
+  const int tiles = lane < rows ? (keys_of(a, a.seq_lens[lane], ring_pos(a, lane)).all +
+                                   tile_keys(D) - 1) / tile_keys(D) : 0;
+  long long all = tiles, before = lane < row ? tiles : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
   }
-  __syncthreads();
-  const int last = last_s, first = first_s;
-  // the bounds hold even if another stream writes the workspace meanwhile
-  if ((uint32_t)first >= (uint32_t)last) return;  // (also: the row crosses no blocks)
-  const int n = last - first + 1;
+  const int mine = __shfl_sync(0xffffffffu, tiles, row);
+  const Shares shares(all * groups, blocks * warps_of(D, NG));
+  const long long tile0 = before * groups + (long long)(vrow - row * groups) * mine;
+  const int first = mine ? (int)(shares.of(tile0) / warps_of(D, NG)) : 0;
+  const int n = mine ? (int)(shares.of(tile0 + mine - 1) / warps_of(D, NG)) - first + 1 : 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n == 1) return;  // the first kernel has written it
   const int f = blockIdx.y, j = f / (KS * 4), s = f / 4 % KS, c = f % 4;
   const int h = j * 8 + (lane & 3) * 2 + (c & 1), dim = s * 16 + (lane >> 2) + (c >> 1) * 8;
   float top = -INFINITY, acc = 0.f, sum = 0.f;
@@ -893,7 +907,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_few_kernel(
     acc += acc_s[v][lane] * w;
     sum += sum_s[v][lane] * w;
   }
-  const int row = vrow / groups, head = (vrow - row * groups) * NG * 8 + h;
+  const int head = (vrow - row * groups) * NG * 8 + h;
   if (head < g) store_out<D>(a, out_row(a, row, g, head), dim, acc, top, sum);
 }
 
