@@ -1,7 +1,10 @@
-"""Build the kvs CUDA library in-tree: kv_cache_eviction_lse_gb300/_lib/libkvs.so.
+"""Build the kvs CUDA library in-tree: kv_cache_eviction_lse_gb300/_lib/libkvs.so, and beside
+it kvs_binding.so, the Python side of the calls made for every token.
 
-Every translation unit is compiled for sm_103a only (one -gencode), in parallel, then
-linked into one shared library with the CUDA runtime linked statically.
+Every CUDA translation unit is compiled for sm_103a only (one -gencode), in parallel, then
+linked into one shared library with the CUDA runtime linked statically.  The binding is plain
+C++ against the headers of the Python and torch that run the build; it is built anew for
+others.
 
     python -m kv_cache_eviction_lse_gb300.build          # build (incremental)
     python -m kv_cache_eviction_lse_gb300.build --force  # rebuild everything
@@ -13,11 +16,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT, "libkvs.so")
+BINDING = os.path.join(OUT, "kvs_binding.so")
+BUILT_FOR = os.path.join(OUT, "kvs_binding.txt")  # the Python and torch it was built for
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,10 +48,55 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _run(what, cmd, verbose=False):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout, r.stderr, file=sys.stderr)
+
+
+def _hosts() -> str:
+    import torch
+    return f"{sys.version} torch {torch.__version__} at {os.path.dirname(torch.__file__)}"
+
+
+def _fresh(*outputs) -> bool:
+    newest = _deps_mtime()
+    return all(os.path.exists(o) and os.path.getmtime(o) >= newest for o in outputs)
+
+
+def _binding_object():
+    import torch
+    t = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    obj = os.path.join(OUT, "binding.cpp.o")
+    _run("binding.cpp", ["g++", "-O2", "-std=c++17", "-fPIC", f"-I{t}",
+                         f"-I{t}/torch/csrc/api/include", f"-I{cuda}",
+                         f"-I{sysconfig.get_paths()['include']}",
+                         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                         "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj])
+    return obj
+
+
+def _link_binding(obj):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    _run("link of the binding", ["g++", "-shared", "-o", tmp, obj, f"-L{OUT}", "-lkvs", f"-L{libs}",
+                                 "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                                 "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BINDING)
+    with open(BUILT_FOR, "w") as f:
+        f.write(_hosts())
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if stale) and return the path of libkvs.so."""
     os.makedirs(OUT, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and _fresh(LIB, BINDING):
+        if not os.path.exists(BUILT_FOR) or open(BUILT_FOR).read() != _hosts():
+            _link_binding(_binding_object())
         return LIB
     nvcc = _nvcc()
     srcs = sources()
@@ -53,21 +104,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
     def compile_one(src):
         obj = os.path.join(OUT, os.path.basename(src) + ".o")
         cmd = [nvcc, *ARCH, *FLAGS, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout, r.stderr, file=sys.stderr)
+        _run(f"nvcc for {src}", cmd, verbose)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_binding_object)
         objs = list(ex.map(compile_one, srcs))
+        binding = binding.result()
     tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run("link", [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

@@ -47,6 +47,11 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"kvs CUDA library not built ({LIB_PATH} missing); run "
                       "`python -m kv_cache_eviction_lse_gb300.build` (needs nvcc)")
 _lib = ctypes.CDLL(LIB_PATH)
+from ._lib import kvs_binding as _binding  # noqa: E402
+
+if _binding.torch_version != torch.__version__.split("+")[0]:
+    raise ImportError(f"kvs binding built for torch {_binding.torch_version}, this is "
+                      f"{torch.__version__}; run `python -m kv_cache_eviction_lse_gb300.build`")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -275,58 +280,13 @@ def kvs_compact_paged(dm, k, v, T, mask, page_size, k_pages, v_pages, capacity_p
                                   ws_bytes, _stream(stream)))
 
 
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
-
-
-def _here(stream):
-    """The current device, where the library launches, and the raw stream of a call."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
-    if stream is None and dev is not None and _raw_stream is not None:
-        return dev, _raw_stream(dev)
-    return dev, _stream(stream)
-
-
-def _arg(t, dtype, n, name, dev):
-    """Device pointer of a tensor argument that must hold at least n elements of dtype and
-    lie on the current device."""
-    if t is None or t.__class__ is int:
-        return t
-    if t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype is not dtype or t.numel() < n:
-        raise ValueError(f"kvs: {name} must hold at least {n} elements of {dtype}, got "
-                         f"{t.numel()} of {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"kvs: tensor arguments must be CUDA tensors on the current device "
-                         f"({name} is on {t.device})")
-    raise ValueError(f"kvs: tensor arguments must be contiguous ({name} is not)")
-
-
-def _freqs(inv_freq, rot_dim):
-    """Host pointer of the rotation frequencies (a float64 CPU tensor, or any sequence of
-    floats) and the object that keeps them alive during the call."""
-    if inv_freq is None or rot_dim <= 0:
-        return None, None
-    f = inv_freq
-    if not (isinstance(f, torch.Tensor) and f.dtype is torch.float64 and not f.is_cuda
-            and f.is_contiguous()):
-        f = torch.tensor([float(x) for x in inv_freq], dtype=torch.float64)
-    if f.numel() < rot_dim // 2:
-        raise ValueError(f"kvs: inv_freq holds {f.numel()} frequencies, {rot_dim // 2} needed")
-    return f.data_ptr(), f
-
+# The calls of a decode loop go through the compiled binding, which checks each tensor for its
+# type, size, device and layout; the others above take what they get.
 
 def kvs_rope(dm, N, pos, rot_dim, inv_freq, interleaved, q, q_out, k, k_out, stream=None):
     """inv_freq: rot_dim / 2 radians per position in host memory (a float64 CPU tensor or a
     sequence of floats)."""
-    fp, _keep = _freqs(inv_freq, rot_dim)
-    dev, raw = _here(stream)
-    per = dm.L * dm.d * N
-    nq, nk = per * dm.H_q, per * dm.H_kv
-    _check(_lib.kvs_rope(_d(dm), N, _arg(pos, _I32, N, "pos", dev), rot_dim, fp,
-                         1 if interleaved else 0, _arg(q, _BF16, nq, "q", dev),
-                         _arg(q_out, _BF16, nq, "q_out", dev), _arg(k, _BF16, nk, "k", dev),
-                         _arg(k_out, _BF16, nk, "k_out", dev), raw))
+    _check(_binding.rope(dm, N, pos, rot_dim, inv_freq, interleaved, q, q_out, k, k_out, stream))
 
 
 def kvs_append_paged_workspace_size(dm, B) -> int:
@@ -337,23 +297,10 @@ def kvs_append_paged(dm, B, N, tok_start, pos, rot_dim, inv_freq, interleaved, q
                      page_size, k_pages, v_pages, capacity_pages, next_page, next_page_out,
                      block_table, max_pages, seq_lens, seq_lens_out, ws, ws_bytes, stream=None):
     """inv_freq as for kvs_rope; tok_start None: one token per sequence (N == B)."""
-    fp, _keep = _freqs(inv_freq, rot_dim)
-    dev, raw = _here(stream)
-    heads, d = dm.L * dm.H_kv, dm.d
-    rows, nk, nq = heads * B, heads * N * d, dm.L * dm.H_q * N * d
-    pool = capacity_pages * page_size * d
-    _check(_lib.kvs_append_paged(
-        _d(dm), B, N, _arg(tok_start, _I32, B + 1, "tok_start", dev), _arg(pos, _I32, N, "pos", dev),
-        rot_dim, fp, 1 if interleaved else 0, _arg(q, _BF16, nq, "q", dev),
-        _arg(q_out, _BF16, nq, "q_out", dev), _arg(k, _BF16, nk, "k", dev),
-        _arg(v, _BF16, nk, "v", dev), page_size,
-        _arg(k_pages, _BF16, pool, "k_pages", dev), _arg(v_pages, _BF16, pool, "v_pages", dev),
-        capacity_pages, _arg(next_page, _I32, 1, "next_page", dev),
-        _arg(next_page_out, _I32, 1, "next_page_out", dev),
-        _arg(block_table, _I32, rows * max_pages, "block_table", dev), max_pages,
-        _arg(seq_lens, _I32, rows, "seq_lens", dev),
-        _arg(seq_lens_out, _I32, rows, "seq_lens_out", dev),
-        _arg(ws, torch.uint8, ws_bytes, "ws", dev), ws_bytes, raw))
+    _check(_binding.append_paged(
+        dm, B, N, tok_start, pos, rot_dim, inv_freq, interleaved, q, q_out, k, v, page_size,
+        k_pages, v_pages, capacity_pages, next_page, next_page_out, block_table, max_pages,
+        seq_lens, seq_lens_out, ws, ws_bytes, stream))
 
 
 def kvs_attn_decode_workspace_size(dm, B) -> int:
@@ -362,16 +309,6 @@ def kvs_attn_decode_workspace_size(dm, B) -> int:
 
 def kvs_attn_decode(dm, B, q, page_size, k_pages, v_pages, capacity_pages, block_table, max_pages,
                     seq_lens, w, pos, ring_k, ring_v, o, lse, ws, ws_bytes, stream=None):
-    dev, raw = _here(stream)
-    rows, d = dm.L * dm.H_kv * B, dm.d
-    nq, pool = dm.L * dm.H_q * B, capacity_pages * page_size * d
-    _check(_lib.kvs_attn_decode(
-        _d(dm), B, _arg(q, _BF16, nq * d, "q", dev), page_size,
-        _arg(k_pages, _BF16, pool, "k_pages", dev), _arg(v_pages, _BF16, pool, "v_pages", dev),
-        capacity_pages,
-        _arg(block_table, _I32, rows * max_pages, "block_table", dev), max_pages,
-        _arg(seq_lens, _I32, rows, "seq_lens", dev), w, _arg(pos, _I32, B if w else 0, "pos", dev),
-        _arg(ring_k, _BF16, rows * w * d, "ring_k", dev),
-        _arg(ring_v, _BF16, rows * w * d, "ring_v", dev),
-        _arg(o, _BF16, nq * d, "o", dev), _arg(lse, _F32, nq, "lse", dev),
-        _arg(ws, torch.uint8, ws_bytes, "ws", dev), ws_bytes, raw))
+    _check(_binding.attn_decode(dm, B, q, page_size, k_pages, v_pages, capacity_pages, block_table,
+                                max_pages, seq_lens, w, pos, ring_k, ring_v, o, lse, ws, ws_bytes,
+                                stream))

@@ -17,7 +17,7 @@
 // flight while a row is finished.  Ten warps with two stages reach 6.8 TB/s (96 sequences of
 // 16384 tokens, heads kept at 25 to 75 %: 361 us for 2.47 GB, 152 blocks); eight warps with
 // three stages take 377 us: more bytes in flight only lengthen every other load.  Short of
-// that, about 9 us of a call is latency (scan of the lengths, table, first tile, joins).
+// that, about 8 us of a call is latency (scan of the lengths, table, first tile, joins).
 // Per tile (mma.m16n8k16, keys in M, heads in N, bf16 -> fp32):
 //   S^T = K Q^T       A = K rows by ldmatrix, B = Q in registers
 //   P^T = exp2(S^T)   in registers, turned into a B operand by movmatrix

@@ -147,3 +147,57 @@ def test_binding_checks_types_and_sizes(C):
     with pytest.raises(ValueError, match="tok_start"):
         C.kvs_append_paged(dm, 8, 9, i32, FAKE, 0, None, False, None, None, FAKE, FAKE, 16, FAKE,
                            FAKE, 4, FAKE, FAKE, FAKE, 4, FAKE, FAKE, FAKE, 1 << 20, stream=0)
+
+
+def test_binding_refuses_what_is_not_an_argument(C):
+    """Numbers that do not fit, things that are neither tensors nor addresses, other dims,
+    frequencies that are no numbers: Python errors that name the argument, no call."""
+    dm = C.dims(1, 2, 1, 64)
+    f = [1.0] * 32
+
+    def call(dm=dm, N=0, pos=FAKE, rot=64, f=f, q=None, stream=0):
+        C.kvs_rope(dm, N, pos, rot, f, False, q, q, None, None, stream=stream)
+
+    call()
+    for kw in (dict(N=1 << 31), dict(N=-(1 << 40)), dict(rot=1 << 32), dict(N=1 << 70)):
+        with pytest.raises(OverflowError, match="out of range"):
+            call(**kw)
+    for kw in (dict(N="4"), dict(N=1.5), dict(pos="x"), dict(q=[1.0]), dict(dm=b"abc"),
+               dict(f=["a"] * 32), dict(f=3.0)):
+        with pytest.raises((TypeError, ValueError)):
+            call(**kw)
+    with pytest.raises(AttributeError):
+        call(stream="s")
+    with pytest.raises(OverflowError):
+        C.kvs_attn_decode(dm, 0, FAKE, 16, FAKE, FAKE, 4, FAKE, 4, FAKE, 0, None, None, None, FAKE,
+                          None, FAKE, -1, stream=0)
+    with pytest.raises(C.KvsError) as e:   # the library's own refusals keep status and message
+        call(N=-1)
+    assert e.value.status == C.KVS_ERR_ARG and "N = -1" in str(e.value)
+
+
+def test_binding_takes_frequencies_of_any_kind(C):
+    """float64 CPU tensors, other tensors, arrays, lists and iterators; the library refuses a
+    value that is not finite, so that it shows which ones were read."""
+    import numpy as np
+    dm = C.dims(1, 2, 1, 64)
+    good = [10000.0 ** (-i / 32) for i in range(32)]
+    for bad in (False, True):
+        v = good[:31] + [float("nan")] if bad else good
+        kinds = [torch.tensor(v, dtype=torch.float64), torch.tensor(v), np.array(v), v, tuple(v),
+                 iter(v), torch.tensor(v + v, dtype=torch.float64)[:32],
+                 torch.tensor([v, v], dtype=torch.float64).t().contiguous().t()[0]]
+        for f in kinds:
+            if bad:
+                with pytest.raises(C.KvsError, match="not finite"):
+                    C.kvs_rope(dm, 0, None, 64, f, False, None, None, None, None, stream=0)
+            else:
+                C.kvs_rope(dm, 0, None, 64, f, False, None, None, None, None, stream=0)
+
+
+def test_binding_sizes_that_pass_64_bits(C):
+    """The sizes that tensors are checked against do not wrap."""
+    dm = C.dims(2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 128)
+    bf = torch.zeros(8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q must"):
+        C.kvs_rope(dm, 2 ** 31 - 1, FAKE, 0, None, False, bf, bf, None, None, stream=0)
