@@ -43,9 +43,10 @@ def dims(L, H_q, H_kv, d, D_h=0) -> Dims:
     return Dims(L, H_q, H_kv, d, D_h)
 
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"kvs CUDA library not built ({LIB_PATH} missing); run "
-                      "`python -m kv_cache_eviction_lse_gb300.build` (needs nvcc)")
+for _path in (LIB_PATH, os.path.join(_HERE, "_lib", "kvs_binding.so")):
+    if not os.path.exists(_path):
+        raise ImportError(f"kvs CUDA library not built ({_path} missing); run "
+                          "`python -m kv_cache_eviction_lse_gb300.build` (needs nvcc)")
 _lib = ctypes.CDLL(LIB_PATH)
 from ._lib import kvs_binding as _binding  # noqa: E402
 
