@@ -516,7 +516,7 @@ kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const in
  *   o[l][hq][b]   = sum_i exp(q[l][hq][b] . k_i / sqrt(d) - lse) v_i
  *
  * over the keys of KV head hq / g.  A row without keys gives o = 0 and lse = -inf.  The
- * softmax weights are rounded to bf16 before they multiply V on the tensor cores; sums
+ * softmax weights multiply V on the tensor cores as two bf16 parts (2^-15 relative); sums
  * and statistics are fp32 and o is stored as bf16.  Results do not depend on the order in
  * which blocks run; where a long row is split, and with it the rounding of the sums, goes by
  * the sizes of the call and the lengths of its rows.
