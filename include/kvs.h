@@ -524,9 +524,9 @@ kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const in
  * page id outside [0, capacity_pages) are left out; either sets the device error word (9).
  *
  *   q, o   [L][H_q][B][d] bf16;  lse [L][H_q][B] fp32 output, or NULL
- *   k_pages, v_pages [capacity_pages][page_size][d] bf16
+ *   k_pages, v_pages [capacity_pages][page_size][d] bf16 (not used with no pages)
  *   block_table [L][H_kv][B][max_pages] int32;  seq_lens [L][H_kv][B] int32
- *   pos    [B] int32;  ring_k, ring_v [L][H_kv][B][w][d] bf16   (NULL with w == 0)
+ *   pos    [B] int32;  ring_k, ring_v [L][H_kv][B][w][d] bf16   (not used with w == 0)
  *   ws     scratch of kvs_attn_decode_workspace_size() bytes; calls that may overlap on
  *          the GPU need their own
  * No output and no workspace overlaps another tensor.  With B = 1 the pages are those of

@@ -1179,9 +1179,10 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs& args, cudaStream_t s) {
   AttnDecodeArgs a = args;
   const int rows = a.L * a.Hkv * a.B, g = a.Hq / a.Hkv;
   if (rows == 0) return cudaSuccess;
-  // a copy of no bytes still names an address: one that is there
-  if (!a.k_pages) a.k_pages = a.v_pages = a.q;
-  if (!a.ring_k) a.ring_k = a.ring_v = a.q;
+  // a copy of no bytes still names an address: one that is there and aligned, whatever came
+  // for a pool of no pages or a ring of no slots (those are not checked)
+  if (a.capacity == 0) a.k_pages = a.v_pages = a.q;
+  if (a.w == 0) a.ring_k = a.ring_v = a.q;
   // groups of 8 heads fill an MMA's N; above 8 a pass takes 16, so that K and V are read
   // once for up to 16 heads
   if (g <= 8)

@@ -72,3 +72,29 @@ def test_attend_infinite_values_stay_infinite(C, g, d, room):  # noqa: F811
     inf[:, :, 2, 9] = float("nan")
     assert torch.equal(torch.isnan(o), torch.isnan(inf))
     assert torch.equal(torch.where(torch.isinf(o), o, 0.0), torch.where(torch.isinf(inf), inf, 0.0))
+
+
+@pytest.mark.parametrize("room", [0, 100000], ids=["tight", "wide"])
+def test_attend_does_not_touch_what_is_not_used(C, room):  # noqa: F811
+    """A ring of no slots and a pool of no pages may be anything: no tensor, one of the two, an
+    address that is not aligned."""
+    odd = 2 ** 20 + 2
+    c = attend_case(C, L=1, Hq=4, H=2, B=3, d=128, ps=16, n=[40, 0, 7], seed=1, room=room)
+    o, z = call_attend(c)
+    g = {n: c[n].cuda() for n in ("q", "kp", "vp", "bt", "sl")}
+    nb = C.kvs_attn_decode_workspace_size(c["dm"], c["B"])
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    for rk, rv in ((None, None), (g["q"], None), (None, g["q"]), (odd, odd + 4), (odd, None)):
+        o2 = torch.full_like(g["q"], 9.0)
+        C.kvs_attn_decode(c["dm"], c["B"], g["q"], c["ps"], g["kp"], g["vp"], c["cap"], g["bt"],
+                          c["mp"], g["sl"], 0, None, rk, rv, o2, None, ws, nb)
+        assert torch.equal(o2.cpu(), o)
+    c = attend_case(C, L=1, Hq=4, H=2, B=3, d=128, ps=16, n=0, w=7, pos=[0, 3, 9], seed=3, room=room)
+    o, z = call_attend(c)
+    g = {n: c[n].cuda() for n in ("q", "bt", "sl", "pos", "rk", "rv")}
+    for kp, vp in ((None, None), (g["q"], None), (None, g["q"]), (odd, odd + 4), (odd, None)):
+        o2 = torch.full_like(g["q"], 9.0)
+        C.kvs_attn_decode(c["dm"], c["B"], g["q"], c["ps"], kp, vp, 0, g["bt"], c["mp"], g["sl"], 7,
+                          g["pos"], g["rk"], g["rv"], o2, None, ws, nb)
+        assert torch.equal(o2.cpu(), o)
+    assert C.kvs_device_error(clear=True) == 0
