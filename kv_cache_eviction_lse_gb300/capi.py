@@ -285,8 +285,8 @@ def kvs_compact_paged(dm, k, v, T, mask, page_size, k_pages, v_pages, capacity_p
 # type, size, device and layout; the others above take what they get.
 
 def kvs_rope(dm, N, pos, rot_dim, inv_freq, interleaved, q, q_out, k, k_out, stream=None):
-    """inv_freq: rot_dim / 2 radians per position in host memory (a float64 CPU tensor or a
-    sequence of floats)."""
+    """inv_freq: rot_dim / 2 radians per position in host memory (a CPU tensor, of float64 to be
+    read in place, or a sequence of floats)."""
     _check(_binding.rope(dm, N, pos, rot_dim, inv_freq, interleaved, q, q_out, k, k_out, stream))
 
 

@@ -135,10 +135,13 @@ struct Place {
   }
 };
 
-// The rotation frequencies in host memory: a float64 CPU tensor's own, or a copy of any
-// sequence of numbers.
+// The rotation frequencies in host memory: a contiguous float64 CPU tensor's own, another CPU
+// tensor of real numbers converted whole (64 of float32: 0.1 us a call, number by number 59),
+// or a copy of any sequence of numbers.  A tensor elsewhere is refused: reading it would wait
+// for the device, and fail in a capture.
 struct Freqs {
   const double* p = nullptr;
+  at::Tensor as_double;
   std::vector<double> own;
 
   Freqs(PyObject* o, int32_t rot_dim) {
@@ -146,12 +149,28 @@ struct Freqs {
     int64_t n = 0;
     if (THPVariable_Check(o)) {
       const at::Tensor& t = THPVariable_Unpack(o);
-      if (t.scalar_type() == at::kDouble && t.is_cpu() && t.is_contiguous()) {
-        n = t.numel();
-        p = static_cast<const double*>(t.data_ptr());
+      if (!t.is_cpu()) {
+        PyObject* where = PyObject_GetAttrString(o, "device");
+        PyErr_Format(PyExc_ValueError, "kvs: inv_freq must be in host memory (it is on %S)", where);
+        Py_XDECREF(where);
+        throw PythonError();
       }
-    }
-    if (!p) {
+      if (!at::isFloatingType(t.scalar_type()) && !at::isIntegralType(t.scalar_type(), true)) {
+        PyErr_SetString(PyExc_TypeError, "kvs: inv_freq must hold real numbers");
+        throw PythonError();
+      }
+      n = t.numel();
+      if (t.scalar_type() == at::kFloat && t.is_contiguous()) {  // as models keep them
+        const float* x = static_cast<const float*>(t.data_ptr());
+        own.assign(x, x + n);
+        own.push_back(0);
+        p = own.data();
+      } else {
+        const bool as_it_is = t.scalar_type() == at::kDouble && t.is_contiguous();
+        as_double = as_it_is ? t : t.detach().to(at::kDouble).contiguous();
+        p = static_cast<const double*>(as_double.data_ptr());
+      }
+    } else {
       PyObject* all = PySequence_Fast(o, "kvs: inv_freq must be a sequence of numbers");
       if (!all) throw PythonError();
       n = PySequence_Fast_GET_SIZE(all);

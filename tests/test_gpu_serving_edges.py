@@ -98,3 +98,20 @@ def test_attend_does_not_touch_what_is_not_used(C, room):  # noqa: F811
                           g["pos"], g["rk"], g["rv"], o2, None, ws, nb)
         assert torch.equal(o2.cpu(), o)
     assert C.kvs_device_error(clear=True) == 0
+
+
+# ----------------------------------------------------------------------------- frequencies
+
+def test_frequencies_on_the_gpu_are_refused(C):  # noqa: F811
+    """... by name, and a model's float32 buffer on the host gives what its float64 copy does."""
+    dm, pos = C.dims(1, 2, 1, 64), torch.arange(5, dtype=torch.int32, device="cuda")
+    x = torch.randn(1, 2, 5, 64, device="cuda").to(torch.bfloat16)
+    f = torch.logspace(0, -3, 32)
+    outs = []
+    for g in (f.double(), f, f.tolist(), f.double().flip(0).flip(0)[::1]):
+        outs.append(torch.empty_like(x))
+        C.kvs_rope(dm, 5, pos, 64, g, False, x, outs[-1], None, None)
+        assert torch.equal(outs[-1], outs[0])
+    for g in (f.cuda(), f.double().cuda()):
+        with pytest.raises(ValueError, match="inv_freq must be in host memory"):
+            C.kvs_rope(dm, 5, pos, 64, g, False, x, outs[0], None, None)
