@@ -4,7 +4,8 @@ it kvs_binding.so, the Python side of the calls made for every token.
 Every CUDA translation unit is compiled for sm_103a only (one -gencode), in parallel, then
 linked into one shared library with the CUDA runtime linked statically.  The binding is plain
 C++ against the headers of the Python and torch that run the build; it is built anew for
-others.
+others.  Where it cannot be built (no g++, no headers) the library is built all the same, with
+a warning: only the serving calls need the binding, and they say so.
 
     python -m kv_cache_eviction_lse_gb300.build          # build (incremental)
     python -m kv_cache_eviction_lse_gb300.build --force  # rebuild everything
@@ -17,6 +18,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -56,9 +58,10 @@ def _run(what, cmd, verbose=False):
         print(r.stdout, r.stderr, file=sys.stderr)
 
 
-def _hosts() -> str:
+def hosts() -> str:
+    """The Python and torch that a binding belongs to."""
     import torch
-    return f"{sys.version} torch {torch.__version__} at {os.path.dirname(torch.__file__)}"
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch.__version__}"
 
 
 def _fresh(*outputs) -> bool:
@@ -88,18 +91,30 @@ def _link_binding(obj):
                                  "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, BINDING)
     with open(BUILT_FOR, "w") as f:
-        f.write(_hosts())
+        f.write(hosts())
+
+
+def _binding_fresh() -> bool:
+    if not _fresh(BINDING) or not os.path.exists(BUILT_FOR):
+        return False
+    with open(BUILT_FOR) as f:
+        return f.read() == hosts()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if stale) and return the path of libkvs.so."""
     os.makedirs(OUT, exist_ok=True)
-    if not force and _fresh(LIB, BINDING):
-        if not os.path.exists(BUILT_FOR) or open(BUILT_FOR).read() != _hosts():
-            _link_binding(_binding_object())
+    stale = force or not _fresh(LIB)
+    try:
+        binding_stale = stale or not _binding_fresh()
+    except ImportError:  # no torch
+        binding_stale = True
+    if not stale and not binding_stale:
         return LIB
-    nvcc = _nvcc()
-    srcs = sources()
+    if os.path.exists(BUILT_FOR):
+        os.remove(BUILT_FOR)  # no binding of another library or Python is loaded meanwhile
+    nvcc = _nvcc() if stale else None
+    srcs = sources() if stale else []
 
     def compile_one(src):
         obj = os.path.join(OUT, os.path.basename(src) + ".o")
@@ -110,11 +125,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         binding = ex.submit(_binding_object)
         objs = list(ex.map(compile_one, srcs))
-        binding = binding.result()
-    tmp = LIB + ".tmp"
-    _run("link", [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
-    os.replace(tmp, LIB)
-    _link_binding(binding)
+    if stale:
+        tmp = LIB + ".tmp"
+        _run("link", [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
+        os.replace(tmp, LIB)
+    try:
+        _link_binding(binding.result())
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"the binding of the serving calls was not built: {e}", stacklevel=2)
     return LIB
 
 

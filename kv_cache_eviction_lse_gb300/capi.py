@@ -5,14 +5,19 @@ arguments are CUDA tensors (or None for an optional/NULL pointer); they are pass
 raw device pointers.  ``stream`` defaults to torch's current CUDA stream.  A non-zero
 status raises :class:`KvsError` carrying the library's message.  Nothing is computed
 here: every step runs in the library's CUDA kernels.  The library must have been built
-(``kv_cache_eviction_lse_gb300.build``); importing this module without it raises.
+(``kv_cache_eviction_lse_gb300.build``); importing this module without it raises.  The calls
+made for every token (kvs_rope, kvs_append_paged, kvs_attn_decode) go through the compiled
+binding beside it, which their first call loads; without it that call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import torch
+
+from . import build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libkvs.so")
@@ -43,16 +48,38 @@ def dims(L, H_q, H_kv, d, D_h=0) -> Dims:
     return Dims(L, H_q, H_kv, d, D_h)
 
 
-for _path in (LIB_PATH, os.path.join(_HERE, "_lib", "kvs_binding.so")):
-    if not os.path.exists(_path):
-        raise ImportError(f"kvs CUDA library not built ({_path} missing); run "
-                          "`python -m kv_cache_eviction_lse_gb300.build` (needs nvcc)")
+if not os.path.exists(LIB_PATH):
+    raise ImportError(f"kvs CUDA library not built ({LIB_PATH} missing); run "
+                      "`python -m kv_cache_eviction_lse_gb300.build` (needs nvcc)")
 _lib = ctypes.CDLL(LIB_PATH)
-from ._lib import kvs_binding as _binding  # noqa: E402
 
-if _binding.torch_version != torch.__version__.split("+")[0]:
-    raise ImportError(f"kvs binding built for torch {_binding.torch_version}, this is "
-                      f"{torch.__version__}; run `python -m kv_cache_eviction_lse_gb300.build`")
+
+def load_binding():
+    """The compiled binding of the serving calls, or an ImportError that says what is missing.
+    It belongs to one Python and one torch, which is checked before it is loaded."""
+    if not (os.path.exists(build.BINDING) and os.path.exists(build.BUILT_FOR)):
+        raise ImportError(f"kvs binding not built ({build.BINDING} missing); run `python -m "
+                          "kv_cache_eviction_lse_gb300.build` (needs g++ and the headers of "
+                          "Python and torch)")
+    with open(build.BUILT_FOR) as f:
+        built_for = f.read()
+    if built_for != build.hosts():
+        raise ImportError(f"kvs binding built for {built_for}, this is {build.hosts()}; run "
+                          "`python -m kv_cache_eviction_lse_gb300.build`")
+    importlib.invalidate_caches()
+    return importlib.import_module("._lib.kvs_binding", __package__)
+
+
+class _Unloaded:
+    """Stands for the binding until the first call that needs it: the other calls need none."""
+
+    def __getattr__(self, name):
+        global _binding
+        _binding = load_binding()
+        return getattr(_binding, name)
+
+
+_binding = _Unloaded()
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32

@@ -9,7 +9,6 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/version.h>
 
 #include <vector>
 
@@ -305,10 +304,5 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "kvs_binding", nullptr, -1, methods
 }  // namespace
 
 PyMODINIT_FUNC PyInit_kvs_binding() {
-  PyObject* m = PyModule_Create(&module);
-  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION)) {
-    Py_DECREF(m);
-    return nullptr;
-  }
-  return m;
+  return PyModule_Create(&module);
 }
