@@ -4,9 +4,10 @@
 // A pair (a, b) of dimensions of a token at position p turns by the angle p f:
 //   (a cos - b sin, b cos + a sin).
 // f is kept as turns per position in a 64-bit binary fraction, so p f mod 1 is one integer
-// product that wraps where the angle does: the angle of any 32-bit position is exact to
-// p 2^-65 turns and needs no range reduction (a 32-bit product would be off by 0.01 rad at
-// position 131072).  In [-pi, pi] the hardware's sine and cosine are good to 2^-21, far
+// product that wraps where the angle does and needs no range reduction (a 32-bit product would
+// be off by 0.01 rad at position 131072).  The fraction comes from one product of doubles, with
+// 1 / (2 pi) rounded to one: the turns are off by 2^-52 of themselves at most, the angle of a frequency
+// up to 1 by p 2^-55 turns.  In [-pi, pi] the hardware's sine and cosine are good to 2^-21, far
 // below the bf16 rounding of the result (2^-8 relative); sincospif took a tenth longer where
 // a thread has one head (2079 tokens of 14 heads 6.5 against 5.9 us).  The products are
 // fp32, and each result is rounded to bf16 once.
