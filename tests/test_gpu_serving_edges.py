@@ -52,6 +52,94 @@ def test_attend_weights_keep_their_bits(C, name, room):  # noqa: F811
     check_attend_closely(c, o, z)
 
 
+def plan(c):
+    """Which kernels take a case, by the rules of their launch: ("row", warps, cluster), or
+    ("stream", "few" or "general", the most blocks that share a row and group of heads)."""
+    d, g, rows = c["d"], c["q"].shape[1] // c["H"], c["n"].size
+    groups, tile = 1 if g <= 8 else -(-g // 16), 16 if d == 128 else 32
+    vrows, room = rows * groups, -(-(c["mp"] * c["ps"] + c["w"]) // tile)
+    if vrows > 456 and room <= 32:
+        return "row", 2, 1
+    cluster = 1
+    while cluster < 8 and vrows * cluster * 2 <= 456:
+        cluster *= 2
+    if room <= cluster * 4 * (16 if vrows * cluster >= 152 else 6):
+        return "row", 4, cluster
+    warps = {(64, 1): 12, (64, 2): 10, (128, 1): 10, (128, 2): 8}[d, 1 if g <= 8 else 2]
+    sms = min(160, torch.cuda.get_device_properties(0).multi_processor_count)
+    blocks = min(sms, -(-vrows * room // warps))
+    held = np.minimum(c["pos"].numpy(), c["w"]) if c["w"] else np.zeros(c["B"], int)
+    tiles = np.repeat(-(-(c["n"] + held) // tile), groups)       # row by row, its groups in turn
+    each, more = divmod(int(tiles.sum()), blocks * warps)
+    if not each:
+        each, more = 1, 0
+    first = np.concatenate([[0], np.cumsum(tiles)])
+    warp = lambda t: t // (each + 1) if t < more * (each + 1) else more + (t - more * (each + 1)) // each  # noqa: E731
+    spans = [warp(b - 1) // warps - warp(a) // warps + 1 for a, b in zip(first[:-1], first[1:]) if b > a]
+    return "stream", "few" if vrows * 8 <= blocks else "general", max(spans)
+
+
+SPANS = [  # lengths of 40 rows, and how many blocks the longest one takes at least
+    ([6000, 2500, 900, 400, 0, 200] + [3, 0, 40, 17] * 8 + [1300, 64], 16),
+    ([700, 5, 1100, 0] * 10, 4),
+    ([2900 + 7 * i for i in range(40)], 3),
+    ([25000] + [100] * 38 + [9000], 34),
+]
+
+
+@pytest.mark.parametrize("lengths,span", SPANS, ids=["one long", "some", "even", "two long"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [3, 12, 24])
+def test_attend_rows_over_many_blocks(C, g, d, lengths, span):  # noqa: F811
+    """More rows than the join of few rows takes, the longest over three and more blocks."""
+    c = attend_case(C, L=1, Hq=g, H=1, B=40, d=d, ps=16, n=lengths, seed=g + d, room=100000)
+    kind, join, most = plan(c)
+    assert (kind, join) == ("stream", "general") and most >= span
+    o, z = call_attend(c)
+    assert C.kvs_device_error(clear=True) == 0
+    check_attend_closely(c, o, z)
+    o2, z2 = call_attend(c)                                # the same bits again
+    assert torch.equal(o2, o) and torch.equal(z2, z)
+
+
+SHAPES = {  # B sequences of H KV heads: the four warps' clusters of 1, 2, 4 and 8, and two warps
+    ("row", 4, 1): dict(B=150, H=2), ("row", 4, 2): dict(B=75, H=2), ("row", 4, 4): dict(B=39, H=2),
+    ("row", 4, 8): dict(B=9, H=2), ("row", 2, 1): dict(B=231, H=2),
+}
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [2, 9, 17])
+def test_attend_shapes_of_a_row(C, g, d, shape):  # noqa: F811
+    """Every shape of the kernel that takes a block or cluster per row."""
+    B, H = SHAPES[shape]["B"], SHAPES[shape]["H"]
+    if g == 17:                                            # two groups of heads a row
+        H = 1
+    n = (np.arange(B) * 37) % 301
+    n[[1, B // 2]] = 0
+    c = attend_case(C, L=1, Hq=g * H, H=H, B=B, d=d, ps=16, n=n, w=11, pos=np.arange(B) % 14,
+                    seed=g + d, room=320)
+    assert plan(c) == shape
+    o, z = call_attend(c)
+    assert C.kvs_device_error(clear=True) == 0
+    check_attend_closely(c, o, z)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_more_rows_than_a_scan_step(C, d):  # noqa: F811
+    """Over 8192 rows in one stream: chunks of several steps, with a number of sequences that
+    divides none of them, ring positions among them."""
+    L, H, B, w = 3, 16, 173, 5
+    n = (np.arange(B)[None, None] * 5 + np.arange(H)[None, :, None] + np.arange(L)[:, None, None]) % 23
+    c = attend_case(C, L=L, Hq=H, H=H, B=B, d=d, ps=16, n=n, w=w, pos=np.arange(B) * 7 % 9, seed=d,
+                    room=3000)
+    assert plan(c)[:2] == ("stream", "general")
+    o, z = call_attend(c)
+    assert C.kvs_device_error(clear=True) == 0
+    check_attend_closely(c, o, z)
+
+
 @pytest.mark.parametrize("room", [0, 100000], ids=["tight", "wide"])
 @pytest.mark.parametrize("g,d", [(4, 128), (12, 128), (4, 64), (12, 64)])
 def test_attend_infinite_values_stay_infinite(C, g, d, room):  # noqa: F811
