@@ -391,7 +391,10 @@ class DecodePipeline:
     attention: the step a model takes, with the arriving tokens' queries x["q"]
     [L][H_q][B][d]: queries and keys are rotated at their positions (kvs_rope; rope_base is
     the base of the frequencies, by default that of Llama-3), the rotated key is decided and
-    stored, and the new token attends over its rows' pages and ring (kvs_attn_decode)."""
+    stored, and the new token attends over its rows' pages and ring (kvs_attn_decode).  The
+    cache starts empty, so that the number of tokens that entered the ring is also the next
+    token's position.  Behind a prompt that is already in the pages it is not: there a caller
+    makes these calls with a position tensor of its own for kvs_rope."""
 
     def __init__(self, wl: Workload, x: dict, max_steps=4096, attention=False, rope_base=5e5):
         self.wl, self.x = wl, x
