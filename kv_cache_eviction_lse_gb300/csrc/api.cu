@@ -772,8 +772,7 @@ size_t kvs_attn_decode_workspace_size(const kvs_dims* dims, int32_t B) {
   if (!dims || dims->L <= 0 || dims->H_kv <= 0 || dims->H_q <= 0 || dims->H_q % dims->H_kv ||
       B <= 0 || (int64_t)dims->L * dims->H_q >= INT32_MAX / 32 / B + 1)
     return 0;
-  return kvs::attn_decode_workspace_bytes(dims->L * dims->H_kv * B, dims->H_q / dims->H_kv,
-                                          dims->d);
+  return kvs::attn_decode_workspace_bytes(dims->H_q / dims->H_kv, dims->d);
 }
 
 kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, int32_t page_size,

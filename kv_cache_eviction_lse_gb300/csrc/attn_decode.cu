@@ -110,12 +110,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // A weight in two bf16 parts: its first eight bits, and what they leave.  The second part is
 // taken of p (1 + 2^-20), so that it is never 0 beside a weight: an infinite value then gives
 // infinity with both parts, and not NaN with one.
@@ -1169,8 +1163,7 @@ cudaError_t launch(AttnDecodeArgs a, int rows, int groups, cudaStream_t s) {
 
 }  // namespace
 
-size_t attn_decode_workspace_bytes(int rows, int group, int d) {
-  (void)rows;
+size_t attn_decode_workspace_bytes(int group, int d) {
   const int ng = group <= 8 ? 1 : 2;
   return ends_bytes() + (size_t)kMaxBlocks * 2 * part_floats(d, ng) * sizeof(float);
 }

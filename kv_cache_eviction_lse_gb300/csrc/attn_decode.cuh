@@ -25,7 +25,7 @@ struct AttnDecodeArgs {
   bool read_once = false;           // set at launch: keys and values leave L2 first
 };
 
-size_t attn_decode_workspace_bytes(int rows, int group, int d);
+size_t attn_decode_workspace_bytes(int group, int d);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t s);
 cudaError_t attn_decode_device_error(int* code, bool clear, cudaStream_t s);
 

@@ -58,12 +58,6 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* x) {
   x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
