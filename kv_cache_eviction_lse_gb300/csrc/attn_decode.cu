@@ -111,8 +111,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 // A weight in two bf16 parts: its first eight bits, and what they leave.  The second part is
-// taken of p (1 + 2^-20), so that it is never 0 beside a weight: an infinite value then gives
-// infinity with both parts, and not NaN with one.
+// taken of p (1 + 2^-20), so that it is not 0 beside a weight (above 2^-112): an infinite value
+// then gives infinity with both parts, and not NaN with one.
 __device__ __forceinline__ uint32_t high2(float a, float b) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
