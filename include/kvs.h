@@ -77,7 +77,8 @@ uint64_t kvs_launch_count(void);
  * (0 = none; 1 = a bounded wait of a tensor-core kernel ran out, 3 = shared-memory
  * window misaligned, 4/5 = kvs_decode_step or kvs_append_paged out of pages, 6 =
  * kvs_value_refit met a non-positive pivot, 8 = kvs_append_paged met a token start, length
- * or page id out of range, 9 = kvs_attn_decode did).  Reading synchronises
+ * or page id out of range, 9 = kvs_attn_decode did, 11 = kvs_accept_paged, kvs_fork_paged or
+ * kvs_reclaim_paged did; 4 also for kvs_fork_paged out of pages).  Reading synchronises
  * `stream`; `clear` != 0 resets it to 0. */
 kvs_status kvs_device_error(int32_t* code_out, int32_t clear, void* stream);
 
@@ -492,7 +493,8 @@ kvs_status kvs_rope(const kvs_dims* dims, int32_t N, const int32_t* pos, int32_t
  *   seq_lens, seq_lens_out [L][H_kv][B] int32; may be the same
  *   ws        scratch of kvs_append_paged_workspace_size() bytes; calls that may overlap
  *             on the GPU need their own
- * No two rows may own the same page, and no tensors overlap but where said.
+ * Rows may share full pages (kvs_fork_paged); the page that a row goes on in is its own.  No
+ * tensors overlap but where said.
  * ------------------------------------------------------------------------------- */
 size_t kvs_append_paged_workspace_size(const kvs_dims* dims, int32_t B);
 kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const int32_t* tok_start,
@@ -539,6 +541,102 @@ kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, i
                            const int32_t* seq_lens, int32_t w, const int32_t* pos,
                            const kvs_bf16* ring_k, const kvs_bf16* ring_v, kvs_bf16* o,
                            float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * kvs_accept_paged -- the accepted path of a draft moved together.  The last
+ * m = tok_start[b + 1] - tok_start[b] tokens of every row of sequence b are drafted ones, as
+ * kvs_append_paged leaves them; of these the n_accept[b] with the indices
+ * accept[tok_start[b]] < accept[tok_start[b] + 1] < ... (from 0, within the sequence's own)
+ * stay.  With base = seq_lens[r] - m, for every row r = (l * H_kv + hk) * B + b:
+ *
+ *   slot base + j  <-  slot base + accept[tok_start[b] + j],   j < n_accept[b]
+ *   seq_lens_out[r] = base + n_accept[b]
+ *
+ * Keys keep their rotation: a drafted token's position is its depth, which does not change.
+ * Slots and pages behind the row's new end keep what they hold and are the row's no more
+ * (kvs_append_paged takes new pages for them, kvs_reclaim_paged frees the old ones).
+ * A row whose token starts, count, indices, length or page ids are out of range, or whose
+ * indices do not grow, stays as it is, with its length, and the device error word is set
+ * (kvs_device_error: 11).
+ *
+ *   tok_start [B + 1] int32, 0 <= tok_start[b] <= tok_start[b + 1] <= N
+ *   n_accept  [B] int32;  accept [N] int32 (may be NULL when N == 0)
+ *   k_pages, v_pages [capacity_pages][page_size][d] bf16 state
+ *   block_table [L][H_kv][B][max_pages] int32
+ *   seq_lens, seq_lens_out [L][H_kv][B] int32; may be the same
+ * Pages that rows share (kvs_fork_paged) hold no drafted tokens.  No tensors overlap but where
+ * said.
+ * ------------------------------------------------------------------------------- */
+kvs_status kvs_accept_paged(const kvs_dims* dims, int32_t B, int32_t N, const int32_t* tok_start,
+                            const int32_t* n_accept, const int32_t* accept, int32_t page_size,
+                            kvs_bf16* k_pages, kvs_bf16* v_pages, int32_t capacity_pages,
+                            const int32_t* block_table, int32_t max_pages,
+                            const int32_t* seq_lens, int32_t* seq_lens_out, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * kvs_fork_paged -- sequences that go on as several (samples of one prompt, beams): for every
+ * i < n_forks the rows of sequence dst[i] become copies of those of sequence src[i].  They share
+ * the source's full pages, which nothing writes any more, and get their own copy of the page
+ * that they go on in, from next_page on, in the order (layer, KV head, fork); its unused rows are
+ * zero.  Table entries behind a row's pages become -1.  With w > 0 the ring of kvs_decode_step
+ * and pos are copied too.  What dst[i] held before is dropped; its pages come free with
+ * kvs_reclaim_paged.  A source's rows may not be cut back (a draft taken back) below the length
+ * at which they were forked, since what follows would be written into shared pages.
+ * All or nothing: if the pool is too small (error word 4), or a sequence number, length or the
+ * counter is out of range, a target is named twice or is a source (11), nothing is written but
+ * next_page_out, which equals next_page.  A bad id of the page to be copied counts as a page of
+ * zeros and sets the error word (11); other ids are copied as they are.
+ *
+ *   src, dst  [n_forks] int32, n_forks <= B <= 131072
+ *   k_pages, v_pages [capacity_pages][page_size][d] bf16 state
+ *   next_page, next_page_out [1] int32; may be the same
+ *   block_table [L][H_kv][B][max_pages] int32 state;  seq_lens [L][H_kv][B] int32 state
+ *   pos [B] int32 state;  ring_score [L][H_kv][B][w] fp32 state;  ring_k, ring_v
+ *             [L][H_kv][B][w][d] bf16 state (not used with w == 0)
+ *   ws        scratch of kvs_fork_paged_workspace_size() bytes; calls that may overlap on the
+ *             GPU need their own
+ * ------------------------------------------------------------------------------- */
+size_t kvs_fork_paged_workspace_size(const kvs_dims* dims, int32_t B, int32_t n_forks);
+kvs_status kvs_fork_paged(const kvs_dims* dims, int32_t B, int32_t n_forks, const int32_t* src,
+                          const int32_t* dst, int32_t page_size, kvs_bf16* k_pages,
+                          kvs_bf16* v_pages, int32_t capacity_pages, const int32_t* next_page,
+                          int32_t* next_page_out, int32_t* block_table, int32_t max_pages,
+                          int32_t* seq_lens, int32_t w, int32_t* pos, float* ring_score,
+                          kvs_bf16* ring_k, kvs_bf16* ring_v, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * kvs_reclaim_paged -- pages that no row names any more come free, and those in use come
+ * together at the front of the pool, so that the counter next_page can go on from their number.
+ * In use are the first ceil(seq_lens[r] / page_size) entries of every row (a finished sequence
+ * is freed by setting its lengths to 0); a page that several rows share counts once.  With n of
+ * them in use, those with ids from n on move, in order of their ids, to the ids below n that
+ * are not in use, in order: as few pages move as can.
+ *
+ *   block_table_out[r][i] = the new id of page i of row r, -1 behind the row's pages
+ *   next_page_out[0]      = n
+ *
+ * Pages that do not move and the old places of those that do keep what they hold, so with
+ * block_table_out and next_page_out apart from their inputs the state before the call stays
+ * good until pages are next taken.  All or nothing: if the counter, a length or the id of a page
+ * in use is out of range (ids of pages in use lie below next_page), nothing moves,
+ * block_table_out and next_page_out equal their inputs, and the device error word is set (11).
+ * All rows that use the pool are in one call.
+ *
+ *   k_pages, v_pages [capacity_pages][page_size][d] bf16 state
+ *   next_page, next_page_out [1] int32; may be the same
+ *   block_table, block_table_out [L][H_kv][B][max_pages] int32; may be the same
+ *   seq_lens  [L][H_kv][B] int32
+ *   ws        scratch of kvs_reclaim_paged_workspace_size() bytes; calls that may overlap on
+ *             the GPU need their own
+ * ------------------------------------------------------------------------------- */
+size_t kvs_reclaim_paged_workspace_size(const kvs_dims* dims, int32_t B, int32_t capacity_pages);
+kvs_status kvs_reclaim_paged(const kvs_dims* dims, int32_t B, int32_t page_size,
+                             kvs_bf16* k_pages, kvs_bf16* v_pages, int32_t capacity_pages,
+                             const int32_t* next_page, int32_t* next_page_out,
+                             const int32_t* block_table, int32_t* block_table_out,
+                             int32_t max_pages, const int32_t* seq_lens, void* ws, size_t ws_bytes,
+                             void* stream);
 
 #ifdef __cplusplus
 }

@@ -6,8 +6,9 @@ raw device pointers.  ``stream`` defaults to torch's current CUDA stream.  A non
 status raises :class:`KvsError` carrying the library's message.  Nothing is computed
 here: every step runs in the library's CUDA kernels.  The library must have been built
 (``kv_cache_eviction_lse_gb300.build``); importing this module without it raises.  The calls
-made for every token (kvs_rope, kvs_append_paged, kvs_attn_decode) go through the compiled
-binding beside it, which their first call loads; without it that call raises.
+made for every token (kvs_rope, kvs_append_paged, kvs_attn_decode, kvs_accept_paged,
+kvs_fork_paged, kvs_reclaim_paged) go through the compiled binding beside it, which their first
+call loads; without it that call raises.
 """
 from __future__ import annotations
 
@@ -124,6 +125,13 @@ _SIGS = {
     "kvs_attn_decode_workspace_size": ([_D, _I], _S),
     "kvs_attn_decode": ([_D, _I, _P, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _S,
                          _P], ctypes.c_int),
+    "kvs_accept_paged": ([_D, _I, _I, _P, _P, _P, _I, _P, _P, _I, _P, _I, _P, _P, _P], ctypes.c_int),
+    "kvs_fork_paged_workspace_size": ([_D, _I, _I], _S),
+    "kvs_fork_paged": ([_D, _I, _I, _P, _P, _I, _P, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P,
+                        _P, _S, _P], ctypes.c_int),
+    "kvs_reclaim_paged_workspace_size": ([_D, _I, _I], _S),
+    "kvs_reclaim_paged": ([_D, _I, _I, _P, _P, _I, _P, _P, _P, _P, _I, _P, _P, _S, _P],
+                          ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -340,3 +348,33 @@ def kvs_attn_decode(dm, B, q, page_size, k_pages, v_pages, capacity_pages, block
     _check(_binding.attn_decode(dm, B, q, page_size, k_pages, v_pages, capacity_pages, block_table,
                                 max_pages, seq_lens, w, pos, ring_k, ring_v, o, lse, ws, ws_bytes,
                                 stream))
+
+
+def kvs_accept_paged(dm, B, N, tok_start, n_accept, accept, page_size, k_pages, v_pages,
+                     capacity_pages, block_table, max_pages, seq_lens, seq_lens_out, stream=None):
+    _check(_binding.accept_paged(dm, B, N, tok_start, n_accept, accept, page_size, k_pages, v_pages,
+                                 capacity_pages, block_table, max_pages, seq_lens, seq_lens_out,
+                                 stream))
+
+
+def kvs_fork_paged_workspace_size(dm, B, n_forks) -> int:
+    return _lib.kvs_fork_paged_workspace_size(_d(dm), B, n_forks)
+
+
+def kvs_fork_paged(dm, B, n_forks, src, dst, page_size, k_pages, v_pages, capacity_pages, next_page,
+                   next_page_out, block_table, max_pages, seq_lens, w, pos, ring_score, ring_k,
+                   ring_v, ws, ws_bytes, stream=None):
+    _check(_binding.fork_paged(dm, B, n_forks, src, dst, page_size, k_pages, v_pages, capacity_pages,
+                               next_page, next_page_out, block_table, max_pages, seq_lens, w, pos,
+                               ring_score, ring_k, ring_v, ws, ws_bytes, stream))
+
+
+def kvs_reclaim_paged_workspace_size(dm, B, capacity_pages) -> int:
+    return _lib.kvs_reclaim_paged_workspace_size(_d(dm), B, capacity_pages)
+
+
+def kvs_reclaim_paged(dm, B, page_size, k_pages, v_pages, capacity_pages, next_page, next_page_out,
+                      block_table, block_table_out, max_pages, seq_lens, ws, ws_bytes, stream=None):
+    _check(_binding.reclaim_paged(dm, B, page_size, k_pages, v_pages, capacity_pages, next_page,
+                                  next_page_out, block_table, block_table_out, max_pages, seq_lens,
+                                  ws, ws_bytes, stream))

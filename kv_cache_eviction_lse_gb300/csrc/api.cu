@@ -14,6 +14,7 @@
 #include "decode.cuh"
 #include "gram.cuh"
 #include "mlp.cuh"
+#include "pages.cuh"
 #include "prune.cuh"
 #include "rope.cuh"
 #include "surrogate.cuh"
@@ -97,7 +98,7 @@ uint64_t kvs_launch_count(void) { return kvs::g_launches.load(std::memory_order_
 
 kvs_status kvs_device_error(int32_t* code_out, int32_t clear, void* stream) {
   REQUIRE(code_out, KVS_ERR_ARG, "kvs_device_error: code_out is NULL");
-  int codes[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  int codes[9] = {};
   cudaError_t e = kvs::attn_device_error(&codes[0], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::mlp_device_error(&codes[1], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::fwd_device_error(&codes[2], clear != 0, as_stream(stream));
@@ -107,6 +108,7 @@ kvs_status kvs_device_error(int32_t* code_out, int32_t clear, void* stream) {
   if (e == cudaSuccess) e = kvs::rope_device_error(&codes[6], clear != 0, as_stream(stream));
   if (e == cudaSuccess)
     e = kvs::attn_decode_device_error(&codes[7], clear != 0, as_stream(stream));
+  if (e == cudaSuccess) e = kvs::pages_device_error(&codes[8], clear != 0, as_stream(stream));
   if (e != cudaSuccess) return cuda_status(e, "kvs_device_error");
   *code_out = 0;
   for (int c : codes)
@@ -817,6 +819,143 @@ kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, i
   a.k_pages = k_pages; a.v_pages = v_pages; a.block_table = block_table; a.seq_lens = seq_lens;
   a.pos = pos; a.ring_k = ring_k; a.ring_v = ring_v; a.o = o; a.lse = lse; a.ws = ws;
   return cuda_status(kvs::launch_attn_decode(a, as_stream(stream)), "kvs_attn_decode");
+}
+
+namespace {
+// What the calls that move pages share: sizes, tables and lengths.  B == 0 is left to the caller.
+kvs_status check_paged(const char* fn, const kvs_dims* dm, int32_t B, int32_t page_size,
+                       kvs_bf16* k_pages, kvs_bf16* v_pages, int32_t capacity_pages,
+                       const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                       kvs::PagedArgs* p) {
+  REQUIRE(B >= 0 && capacity_pages >= 0, KVS_ERR_ARG, "%s: negative size", fn);
+  REQUIRE(page_size >= 1 && page_size <= 4096, KVS_ERR_UNSUPPORTED, "%s: page_size = %d (1..4096)",
+          fn, page_size);
+  REQUIRE(max_pages >= 1, KVS_ERR_SHAPE, "%s: max_pages = %d must be >= 1", fn, max_pages);
+  REQUIRE((int64_t)dm->L * dm->H_kv < INT32_MAX / 32 / (B > 0 ? B : 1), KVS_ERR_UNSUPPORTED,
+          "%s: too many rows", fn);
+  if (B == 0) return KVS_OK;
+  if (capacity_pages > 0) {
+    REQUIRE(k_pages && v_pages, KVS_ERR_ARG, "%s: k_pages or v_pages is NULL", fn);
+    REQUIRE(aligned16(k_pages) && aligned16(v_pages), KVS_ERR_ALIGN,
+            "%s: k_pages or v_pages is not 16-byte aligned", fn);
+  }
+  REQUIRE(block_table && seq_lens, KVS_ERR_ARG, "%s: block_table or seq_lens is NULL", fn);
+  REQUIRE(aligned16(block_table) && aligned16(seq_lens), KVS_ERR_ALIGN,
+          "%s: block_table or seq_lens is not 16-byte aligned", fn);
+  p->L = dm->L; p->Hkv = dm->H_kv; p->B = B; p->d = dm->d; p->page_size = page_size;
+  p->capacity = capacity_pages; p->max_pages = max_pages; p->k_pages = k_pages;
+  p->v_pages = v_pages; p->block_table = block_table; p->seq_lens = seq_lens;
+  return KVS_OK;
+}
+}  // namespace
+
+kvs_status kvs_accept_paged(const kvs_dims* dims, int32_t B, int32_t N, const int32_t* tok_start,
+                            const int32_t* n_accept, const int32_t* accept, int32_t page_size,
+                            kvs_bf16* k_pages, kvs_bf16* v_pages, int32_t capacity_pages,
+                            const int32_t* block_table, int32_t max_pages,
+                            const int32_t* seq_lens, int32_t* seq_lens_out, void* stream) {
+  kvs_status st = check_dims(dims, __func__);
+  if (st) return st;
+  REQUIRE(N >= 0, KVS_ERR_ARG, "kvs_accept_paged: N = %d is negative", N);
+  kvs::PagedArgs p;
+  st = check_paged(__func__, dims, B, page_size, k_pages, v_pages, capacity_pages, block_table,
+                   max_pages, seq_lens, &p);
+  if (st) return st;
+  if (B == 0) return ok();
+  REQUIRE_PTR(tok_start);
+  REQUIRE_PTR(n_accept);
+  if (N > 0) REQUIRE_PTR(accept);
+  REQUIRE_PTR(seq_lens_out);
+  const size_t rows = (size_t)dims->L * dims->H_kv * B;
+  REQUIRE(seq_lens == seq_lens_out || !overlap(seq_lens, seq_lens_out, rows * 4, rows * 4),
+          KVS_ERR_ARG, "kvs_accept_paged: seq_lens_out overlaps seq_lens without being it");
+  kvs::AcceptArgs a;
+  a.N = N; a.tok_start = tok_start; a.n_accept = n_accept; a.accept = accept;
+  a.seq_lens_out = seq_lens_out;
+  return cuda_status(kvs::launch_accept(p, a, as_stream(stream)), "kvs_accept_paged");
+}
+
+size_t kvs_fork_paged_workspace_size(const kvs_dims* dims, int32_t B, int32_t n_forks) {
+  if (!dims || dims->L <= 0 || dims->H_kv <= 0 || B <= 0 || n_forks <= 0 || n_forks > B ||
+      (int64_t)dims->L * dims->H_kv >= INT32_MAX / 32 / B + 1)
+    return 0;
+  return kvs::fork_workspace_bytes(dims->L * dims->H_kv * n_forks);
+}
+
+kvs_status kvs_fork_paged(const kvs_dims* dims, int32_t B, int32_t n_forks, const int32_t* src,
+                          const int32_t* dst, int32_t page_size, kvs_bf16* k_pages,
+                          kvs_bf16* v_pages, int32_t capacity_pages, const int32_t* next_page,
+                          int32_t* next_page_out, int32_t* block_table, int32_t max_pages,
+                          int32_t* seq_lens, int32_t w, int32_t* pos, float* ring_score,
+                          kvs_bf16* ring_k, kvs_bf16* ring_v, void* ws, size_t ws_bytes,
+                          void* stream) {
+  kvs_status st = check_dims(dims, __func__);
+  if (st) return st;
+  REQUIRE(n_forks >= 0 && w >= 0, KVS_ERR_ARG, "kvs_fork_paged: negative n_forks or w");
+  kvs::PagedArgs p;
+  st = check_paged(__func__, dims, B, page_size, k_pages, v_pages, capacity_pages, block_table,
+                   max_pages, seq_lens, &p);
+  if (st) return st;
+  REQUIRE(B <= kvs::kMaxForkBatch, KVS_ERR_UNSUPPORTED, "kvs_fork_paged: B = %d (at most %d)", B,
+          kvs::kMaxForkBatch);
+  REQUIRE(n_forks <= B, KVS_ERR_SHAPE, "kvs_fork_paged: n_forks = %d above B = %d", n_forks, B);
+  if (n_forks == 0) return ok();
+  REQUIRE_PTR(src);
+  REQUIRE_PTR(dst);
+  REQUIRE_PTR(next_page);
+  REQUIRE_PTR(next_page_out);
+  if (w > 0) {
+    REQUIRE_PTR(pos);
+    REQUIRE_PTR(ring_score);
+    REQUIRE_PTR(ring_k);
+    REQUIRE_PTR(ring_v);
+  }
+  REQUIRE((int64_t)dims->L * dims->H_kv * n_forks * (w / 16 + 2) < INT32_MAX &&
+              (int64_t)w * dims->d < INT32_MAX,
+          KVS_ERR_UNSUPPORTED, "kvs_fork_paged: w = %d is too large for the rows", w);
+  REQUIRE_PTR(ws);
+  const size_t need = kvs_fork_paged_workspace_size(dims, B, n_forks);
+  REQUIRE(ws_bytes >= need, KVS_ERR_CAPACITY, "kvs_fork_paged: workspace of %zu bytes, %zu needed",
+          ws_bytes, need);
+  kvs::ForkArgs a;
+  a.forks = n_forks; a.w = w; a.src = src; a.dst = dst; a.next_page = next_page;
+  a.next_page_out = next_page_out; a.block_table = block_table; a.seq_lens = seq_lens; a.pos = pos;
+  a.ring_score = ring_score; a.ring_k = ring_k; a.ring_v = ring_v; a.plan = ws;
+  return cuda_status(kvs::launch_fork(p, a, as_stream(stream)), "kvs_fork_paged");
+}
+
+size_t kvs_reclaim_paged_workspace_size(const kvs_dims* dims, int32_t B, int32_t capacity_pages) {
+  if (!dims || dims->L <= 0 || dims->H_kv <= 0 || B <= 0 || capacity_pages < 0) return 0;
+  return kvs::reclaim_workspace_bytes(capacity_pages);
+}
+
+kvs_status kvs_reclaim_paged(const kvs_dims* dims, int32_t B, int32_t page_size,
+                             kvs_bf16* k_pages, kvs_bf16* v_pages, int32_t capacity_pages,
+                             const int32_t* next_page, int32_t* next_page_out,
+                             const int32_t* block_table, int32_t* block_table_out,
+                             int32_t max_pages, const int32_t* seq_lens, void* ws, size_t ws_bytes,
+                             void* stream) {
+  kvs_status st = check_dims(dims, __func__);
+  if (st) return st;
+  kvs::PagedArgs p;
+  st = check_paged(__func__, dims, B, page_size, k_pages, v_pages, capacity_pages, block_table,
+                   max_pages, seq_lens, &p);
+  if (st) return st;
+  if (B == 0) return ok();
+  REQUIRE_PTR(next_page);
+  REQUIRE_PTR(next_page_out);
+  REQUIRE_PTR(block_table_out);
+  const size_t table = (size_t)dims->L * dims->H_kv * B * max_pages * 4;
+  REQUIRE(block_table == block_table_out || !overlap(block_table, block_table_out, table, table),
+          KVS_ERR_ARG, "kvs_reclaim_paged: block_table_out overlaps block_table without being it");
+  REQUIRE_PTR(ws);
+  const size_t need = kvs_reclaim_paged_workspace_size(dims, B, capacity_pages);
+  REQUIRE(ws_bytes >= need, KVS_ERR_CAPACITY,
+          "kvs_reclaim_paged: workspace of %zu bytes, %zu needed", ws_bytes, need);
+  kvs::ReclaimArgs a;
+  a.next_page = next_page; a.next_page_out = next_page_out; a.block_table_out = block_table_out;
+  a.ws = ws;
+  return cuda_status(kvs::launch_reclaim(p, a, as_stream(stream)), "kvs_reclaim_paged");
 }
 
 }  // extern "C"

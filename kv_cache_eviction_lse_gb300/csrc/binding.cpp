@@ -1,5 +1,6 @@
 // The Python side of the calls that a decode loop makes for every token: kvs_rope,
-// kvs_append_paged and kvs_attn_decode.  Their kernels take 2 to 10 us for a token of a batch,
+// kvs_append_paged and kvs_attn_decode, and around drafted tokens kvs_accept_paged,
+// kvs_fork_paged and kvs_reclaim_paged.  Their kernels take 2 to 10 us for a token of a batch,
 // and up to 25 arguments checked and converted in Python took longer: calls back to back are
 // one per 6.8 us (rotation of 64 tokens), 13.2 (their append) and 8.7 (attention of a short
 // sequence) that way, and 2.9, 5.0 and 5.9 through this file, launches included.  Arguments
@@ -293,10 +294,92 @@ PyObject* attn_decode(PyObject*, PyObject* const* x, Py_ssize_t nx) {
   });
 }
 
+PyObject* accept_paged(PyObject*, PyObject* const* x, Py_ssize_t nx) {
+  return guarded([&] {
+    expect(nx, 15);
+    kvs_dims dm;
+    dims(x[0], &dm);
+    const int32_t B = int32(x[1], "B"), N = int32(x[2], "N"), ps = int32(x[6], "page_size");
+    const int32_t cap = int32(x[9], "capacity_pages"), mp = int32(x[11], "max_pages");
+    const Place at(x[14]);
+    const int64_t rows = times(dm.L, dm.H_kv, B), pool = times(cap, ps, dm.d);
+    const int32_t *tok = at.i32(x[3], (int64_t)B + 1, "tok_start"), *n = at.i32(x[4], B, "n_accept");
+    const int32_t* path = at.i32(x[5], N, "accept");
+    kvs_bf16 *kp = at.bf16(x[7], pool, "k_pages"), *vp = at.bf16(x[8], pool, "v_pages");
+    const int32_t* bt = at.i32(x[10], times(rows, mp), "block_table");
+    const int32_t* sl = at.i32(x[12], rows, "seq_lens");
+    int32_t* sl_out = at.i32(x[13], rows, "seq_lens_out");
+    kvs_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = kvs_accept_paged(&dm, B, N, tok, n, path, ps, kp, vp, cap, bt, mp, sl, sl_out, at.stream);
+    Py_END_ALLOW_THREADS
+    return st;
+  });
+}
+
+PyObject* fork_paged(PyObject*, PyObject* const* x, Py_ssize_t nx) {
+  return guarded([&] {
+    expect(nx, 22);
+    kvs_dims dm;
+    dims(x[0], &dm);
+    const int32_t B = int32(x[1], "B"), forks = int32(x[2], "n_forks"), ps = int32(x[5], "page_size");
+    const int32_t cap = int32(x[8], "capacity_pages"), mp = int32(x[12], "max_pages");
+    const int32_t w = int32(x[14], "w");
+    const int64_t ws_bytes = integer(x[20], "ws_bytes", 0, INT64_MAX);
+    const Place at(x[21]);
+    const int64_t rows = times(dm.L, dm.H_kv, B), pool = times(cap, ps, dm.d), ring = times(rows, w);
+    const int32_t *src = at.i32(x[3], forks, "src"), *dst = at.i32(x[4], forks, "dst");
+    kvs_bf16 *kp = at.bf16(x[6], pool, "k_pages"), *vp = at.bf16(x[7], pool, "v_pages");
+    const int32_t* next = at.i32(x[9], 1, "next_page");
+    int32_t* next_out = at.i32(x[10], 1, "next_page_out");
+    int32_t* bt = at.i32(x[11], times(rows, mp), "block_table");
+    int32_t *sl = at.i32(x[13], rows, "seq_lens"), *pos = at.i32(x[15], w ? B : 0, "pos");
+    float* score = at.arg<float>(x[16], at::kFloat, ring, "ring_score");
+    kvs_bf16* rk = at.bf16(x[17], times(ring, dm.d), "ring_k");
+    kvs_bf16* rv = at.bf16(x[18], times(ring, dm.d), "ring_v");
+    void* ws = at.arg<void>(x[19], at::kByte, ws_bytes, "ws");
+    kvs_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = kvs_fork_paged(&dm, B, forks, src, dst, ps, kp, vp, cap, next, next_out, bt, mp, sl, w, pos,
+                        score, rk, rv, ws, (size_t)ws_bytes, at.stream);
+    Py_END_ALLOW_THREADS
+    return st;
+  });
+}
+
+PyObject* reclaim_paged(PyObject*, PyObject* const* x, Py_ssize_t nx) {
+  return guarded([&] {
+    expect(nx, 15);
+    kvs_dims dm;
+    dims(x[0], &dm);
+    const int32_t B = int32(x[1], "B"), ps = int32(x[2], "page_size");
+    const int32_t cap = int32(x[5], "capacity_pages"), mp = int32(x[10], "max_pages");
+    const int64_t ws_bytes = integer(x[13], "ws_bytes", 0, INT64_MAX);
+    const Place at(x[14]);
+    const int64_t rows = times(dm.L, dm.H_kv, B), pool = times(cap, ps, dm.d);
+    kvs_bf16 *kp = at.bf16(x[3], pool, "k_pages"), *vp = at.bf16(x[4], pool, "v_pages");
+    const int32_t* next = at.i32(x[6], 1, "next_page");
+    int32_t* next_out = at.i32(x[7], 1, "next_page_out");
+    const int32_t* bt = at.i32(x[8], times(rows, mp), "block_table");
+    int32_t* bt_out = at.i32(x[9], times(rows, mp), "block_table_out");
+    const int32_t* sl = at.i32(x[11], rows, "seq_lens");
+    void* ws = at.arg<void>(x[12], at::kByte, ws_bytes, "ws");
+    kvs_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = kvs_reclaim_paged(&dm, B, ps, kp, vp, cap, next, next_out, bt, bt_out, mp, sl, ws,
+                           (size_t)ws_bytes, at.stream);
+    Py_END_ALLOW_THREADS
+    return st;
+  });
+}
+
 PyMethodDef methods[] = {
     {"rope", (PyCFunction)(void (*)())rope, METH_FASTCALL, nullptr},
     {"append_paged", (PyCFunction)(void (*)())append_paged, METH_FASTCALL, nullptr},
     {"attn_decode", (PyCFunction)(void (*)())attn_decode, METH_FASTCALL, nullptr},
+    {"accept_paged", (PyCFunction)(void (*)())accept_paged, METH_FASTCALL, nullptr},
+    {"fork_paged", (PyCFunction)(void (*)())fork_paged, METH_FASTCALL, nullptr},
+    {"reclaim_paged", (PyCFunction)(void (*)())reclaim_paged, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "kvs_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

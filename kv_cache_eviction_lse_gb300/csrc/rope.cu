@@ -17,6 +17,7 @@
 // and layers it walks through.  A 16384-token prompt of 2 layers takes 98 us (671 MB, 6.8
 // TB/s, the rate of a copy).
 #include "common.cuh"
+#include "launch.cuh"
 #include "rope.cuh"
 
 namespace kvs {
@@ -390,24 +391,6 @@ int slab_groups(int token_blocks, int slabs, int waves) {
   if (groups < fill) groups = fill;
   return groups < 1 ? 1 : groups > slabs ? slabs : groups > 65535 ? 65535 : groups;
 }
-
-// A launch that may start before the kernel before it in the stream has ended; every kernel
-// here waits for that (griddepcontrol.wait) before it touches memory, or reads only what
-// kernels further back have written.  A rotation of 64 tokens takes 2.1 us in a graph (2.5
-// launched after the end), the append of 64 tokens 4.8 (5.1).
-struct Launch {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  Launch(dim3 grid, int threads, cudaStream_t s) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-};
 
 }  // namespace
 
