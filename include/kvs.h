@@ -77,8 +77,9 @@ uint64_t kvs_launch_count(void);
  * (0 = none; 1 = a bounded wait of a tensor-core kernel ran out, 3 = shared-memory
  * window misaligned, 4/5 = kvs_decode_step or kvs_append_paged out of pages, 6 =
  * kvs_value_refit met a non-positive pivot, 8 = kvs_append_paged met a token start, length
- * or page id out of range, 9 = kvs_attn_decode did, 11 = kvs_accept_paged, kvs_fork_paged or
- * kvs_reclaim_paged did; 4 also for kvs_fork_paged out of pages).  Reading synchronises
+ * or page id out of range, 9 = kvs_attn_decode did, 10 = kvs_attn_tree met one or a parent out
+ * of range, 11 = kvs_accept_paged, kvs_fork_paged or kvs_reclaim_paged did; 4 also for
+ * kvs_fork_paged out of pages).  Reading synchronises
  * `stream`; `clear` != 0 resets it to 0. */
 kvs_status kvs_device_error(int32_t* code_out, int32_t clear, void* stream);
 
@@ -541,6 +542,53 @@ kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, i
                            const int32_t* seq_lens, int32_t w, const int32_t* pos,
                            const kvs_bf16* ring_k, const kvs_bf16* ring_v, kvs_bf16* o,
                            float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * kvs_attn_tree -- attention of drafted tokens over the pruned cache, a tree of them per
+ * sequence, to verify them in one pass [KVzap limitation 3: head lengths differ; KVzap 3.2,
+ * Eq. 2].  Tokens tok_start[b] .. tok_start[b + 1] - 1 of the batch's N are drafted ones of
+ * sequence b and, as kvs_append_paged leaves them, the last m = tok_start[b + 1] - tok_start[b]
+ * paged tokens of each of its rows r = (l * H_kv + hk) * B + b.  parent gives for each the index
+ * (from 0, within the sequence's own) of the token that it follows, or -1 for one that follows
+ * the cache; parents come before their children.  Token i sees
+ *
+ *   - the paged tokens before the drafted ones (slots below seq_lens[r] - m) and, with w > 0,
+ *     the min(pos[b], w) tokens in the ring of kvs_decode_step,
+ *   - of the drafted ones itself, its parent, that one's parent, and so on:
+ *
+ *   lse[l][hq][t] = ln sum_k exp(q[l][hq][t] . k / sqrt(d))      over the keys that t sees
+ *   o[l][hq][t]   = sum_k exp(q[l][hq][t] . k / sqrt(d) - lse) v
+ *
+ * A drafted token that t does not see has no part in its result, whatever it holds (infinities
+ * and NaN included).  Tokens from tok_start[B] on are padding: nothing is read or written for
+ * them.  A token that sees no key gives o = 0 and lse = -inf.  The softmax weights are rounded
+ * to bf16 before they multiply V; sums and statistics are fp32 and o is stored as bf16.  Results
+ * do not depend on the order in which blocks run; where a long row is split goes by the sizes of
+ * the call and the lengths of its rows.
+ * A length outside [0, max_pages * page_size] is taken as the nearest bound, keys of a page id
+ * outside [0, capacity_pages) are left out, drafted tokens before slot 0 too, a parent that does
+ * not come before its child counts as -1, and a sequence whose token starts do not lie in order
+ * in [0, N] or that has more than max_draft tokens gets no results; each sets the device error
+ * word (10).
+ *
+ *   max_draft 1 .. 256: no sequence has more drafted tokens
+ *   tok_start [B + 1] int32;  parent [N] int32, or NULL: token i follows token i - 1
+ *   q, o   [L][H_q][N][d] bf16;  lse [L][H_q][N] fp32 output, or NULL
+ *   k_pages, v_pages [capacity_pages][page_size][d] bf16 (not used with no pages)
+ *   block_table [L][H_kv][B][max_pages] int32;  seq_lens [L][H_kv][B] int32
+ *   pos    [B] int32;  ring_k, ring_v [L][H_kv][B][w][d] bf16   (not used with w == 0)
+ *   ws     scratch of kvs_attn_tree_workspace_size() bytes; calls that may overlap on the
+ *          GPU need their own
+ * No output and no workspace overlaps another tensor.
+ * ------------------------------------------------------------------------------- */
+size_t kvs_attn_tree_workspace_size(const kvs_dims* dims, int32_t B, int32_t N);
+kvs_status kvs_attn_tree(const kvs_dims* dims, int32_t B, int32_t N, int32_t max_draft,
+                         const int32_t* tok_start, const int32_t* parent, const kvs_bf16* q,
+                         int32_t page_size, const kvs_bf16* k_pages, const kvs_bf16* v_pages,
+                         int32_t capacity_pages, const int32_t* block_table, int32_t max_pages,
+                         const int32_t* seq_lens, int32_t w, const int32_t* pos,
+                         const kvs_bf16* ring_k, const kvs_bf16* ring_v, kvs_bf16* o, float* lse,
+                         void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------
  * kvs_accept_paged -- the accepted path of a draft moved together.  The last

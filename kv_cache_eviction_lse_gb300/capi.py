@@ -6,9 +6,9 @@ raw device pointers.  ``stream`` defaults to torch's current CUDA stream.  A non
 status raises :class:`KvsError` carrying the library's message.  Nothing is computed
 here: every step runs in the library's CUDA kernels.  The library must have been built
 (``kv_cache_eviction_lse_gb300.build``); importing this module without it raises.  The calls
-made for every token (kvs_rope, kvs_append_paged, kvs_attn_decode, kvs_accept_paged,
-kvs_fork_paged, kvs_reclaim_paged) go through the compiled binding beside it, which their first
-call loads; without it that call raises.
+made for every token (kvs_rope, kvs_append_paged, kvs_attn_decode, kvs_attn_tree,
+kvs_accept_paged, kvs_fork_paged, kvs_reclaim_paged) go through the compiled binding beside it,
+which their first call loads; without it that call raises.
 """
 from __future__ import annotations
 
@@ -125,6 +125,9 @@ _SIGS = {
     "kvs_attn_decode_workspace_size": ([_D, _I], _S),
     "kvs_attn_decode": ([_D, _I, _P, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _S,
                          _P], ctypes.c_int),
+    "kvs_attn_tree_workspace_size": ([_D, _I, _I], _S),
+    "kvs_attn_tree": ([_D, _I, _I, _I, _P, _P, _P, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P,
+                       _P, _S, _P], ctypes.c_int),
     "kvs_accept_paged": ([_D, _I, _I, _P, _P, _P, _I, _P, _P, _I, _P, _I, _P, _P, _P], ctypes.c_int),
     "kvs_fork_paged_workspace_size": ([_D, _I, _I], _S),
     "kvs_fork_paged": ([_D, _I, _I, _P, _P, _I, _P, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P,
@@ -348,6 +351,19 @@ def kvs_attn_decode(dm, B, q, page_size, k_pages, v_pages, capacity_pages, block
     _check(_binding.attn_decode(dm, B, q, page_size, k_pages, v_pages, capacity_pages, block_table,
                                 max_pages, seq_lens, w, pos, ring_k, ring_v, o, lse, ws, ws_bytes,
                                 stream))
+
+
+def kvs_attn_tree_workspace_size(dm, B, N) -> int:
+    return _lib.kvs_attn_tree_workspace_size(_d(dm), B, N)
+
+
+def kvs_attn_tree(dm, B, N, max_draft, tok_start, parent, q, page_size, k_pages, v_pages,
+                  capacity_pages, block_table, max_pages, seq_lens, w, pos, ring_k, ring_v, o, lse, ws,
+                  ws_bytes, stream=None):
+    """parent None: every sequence's tokens follow one another."""
+    _check(_binding.attn_tree(dm, B, N, max_draft, tok_start, parent, q, page_size, k_pages, v_pages,
+                              capacity_pages, block_table, max_pages, seq_lens, w, pos, ring_k, ring_v,
+                              o, lse, ws, ws_bytes, stream))
 
 
 def kvs_accept_paged(dm, B, N, tok_start, n_accept, accept, page_size, k_pages, v_pages,

@@ -10,6 +10,7 @@
 #include "../../include/kvs.h"
 #include "attn.cuh"
 #include "attn_decode.cuh"
+#include "attn_tree.cuh"
 #include "compact.cuh"
 #include "decode.cuh"
 #include "gram.cuh"
@@ -98,7 +99,7 @@ uint64_t kvs_launch_count(void) { return kvs::g_launches.load(std::memory_order_
 
 kvs_status kvs_device_error(int32_t* code_out, int32_t clear, void* stream) {
   REQUIRE(code_out, KVS_ERR_ARG, "kvs_device_error: code_out is NULL");
-  int codes[9] = {};
+  int codes[10] = {};
   cudaError_t e = kvs::attn_device_error(&codes[0], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::mlp_device_error(&codes[1], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::fwd_device_error(&codes[2], clear != 0, as_stream(stream));
@@ -109,6 +110,7 @@ kvs_status kvs_device_error(int32_t* code_out, int32_t clear, void* stream) {
   if (e == cudaSuccess)
     e = kvs::attn_decode_device_error(&codes[7], clear != 0, as_stream(stream));
   if (e == cudaSuccess) e = kvs::pages_device_error(&codes[8], clear != 0, as_stream(stream));
+  if (e == cudaSuccess) e = kvs::attn_tree_device_error(&codes[9], clear != 0, as_stream(stream));
   if (e != cudaSuccess) return cuda_status(e, "kvs_device_error");
   *code_out = 0;
   for (int c : codes)
@@ -819,6 +821,63 @@ kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, i
   a.k_pages = k_pages; a.v_pages = v_pages; a.block_table = block_table; a.seq_lens = seq_lens;
   a.pos = pos; a.ring_k = ring_k; a.ring_v = ring_v; a.o = o; a.lse = lse; a.ws = ws;
   return cuda_status(kvs::launch_attn_decode(a, as_stream(stream)), "kvs_attn_decode");
+}
+
+size_t kvs_attn_tree_workspace_size(const kvs_dims* dims, int32_t B, int32_t N) {
+  if (!dims || dims->L <= 0 || dims->H_kv <= 0 || dims->H_q <= 0 || dims->H_q % dims->H_kv ||
+      B <= 0 || N <= 0 || (int64_t)dims->L * dims->H_q >= INT32_MAX / 32 / B + 1)
+    return 0;
+  return kvs::attn_tree_workspace_bytes(dims->d);
+}
+
+kvs_status kvs_attn_tree(const kvs_dims* dims, int32_t B, int32_t N, int32_t max_draft,
+                         const int32_t* tok_start, const int32_t* parent, const kvs_bf16* q,
+                         int32_t page_size, const kvs_bf16* k_pages, const kvs_bf16* v_pages,
+                         int32_t capacity_pages, const int32_t* block_table, int32_t max_pages,
+                         const int32_t* seq_lens, int32_t w, const int32_t* pos,
+                         const kvs_bf16* ring_k, const kvs_bf16* ring_v, kvs_bf16* o, float* lse,
+                         void* ws, size_t ws_bytes, void* stream) {
+  kvs_status st = check_dims(dims, __func__);
+  if (st) return st;
+  REQUIRE(B >= 0 && N >= 0 && w >= 0 && capacity_pages >= 0, KVS_ERR_ARG,
+          "kvs_attn_tree: negative size");
+  REQUIRE(max_draft >= 1 && max_draft <= kvs::kMaxDraft, KVS_ERR_UNSUPPORTED,
+          "kvs_attn_tree: max_draft = %d (1..%d)", max_draft, kvs::kMaxDraft);
+  REQUIRE(page_size >= 1 && page_size <= 4096, KVS_ERR_UNSUPPORTED,
+          "kvs_attn_tree: page_size = %d (1..4096)", page_size);
+  REQUIRE(max_pages >= 1, KVS_ERR_SHAPE, "kvs_attn_tree: max_pages = %d must be >= 1", max_pages);
+  REQUIRE((int64_t)dims->L * dims->H_q < INT32_MAX / 32 / (B > 0 ? B : 1), KVS_ERR_UNSUPPORTED,
+          "kvs_attn_tree: too many rows");
+  REQUIRE((int64_t)max_pages * page_size + w < INT32_MAX - 65536, KVS_ERR_UNSUPPORTED,
+          "kvs_attn_tree: max_pages * page_size + w of a row above 2^31");
+  if (B == 0 || N == 0) return ok();
+  REQUIRE_PTR(tok_start);
+  REQUIRE_OPT_PTR(parent);
+  REQUIRE_PTR(q);
+  REQUIRE_PTR(block_table);
+  REQUIRE_PTR(seq_lens);
+  if (capacity_pages > 0) {
+    REQUIRE_PTR(k_pages);
+    REQUIRE_PTR(v_pages);
+  }
+  if (w > 0) {
+    REQUIRE_PTR(pos);
+    REQUIRE_PTR(ring_k);
+    REQUIRE_PTR(ring_v);
+  }
+  REQUIRE_PTR(o);
+  REQUIRE_OPT_PTR(lse);
+  REQUIRE_PTR(ws);
+  const size_t need = kvs_attn_tree_workspace_size(dims, B, N);
+  REQUIRE(ws_bytes >= need, KVS_ERR_CAPACITY, "kvs_attn_tree: workspace of %zu bytes, %zu needed",
+          ws_bytes, need);
+  kvs::AttnTreeArgs a;
+  a.q = q; a.L = dims->L; a.Hq = dims->H_q; a.Hkv = dims->H_kv; a.B = B; a.N = N; a.d = dims->d;
+  a.max_draft = max_draft; a.page_size = page_size; a.capacity = capacity_pages;
+  a.max_pages = max_pages; a.w = w; a.tok_start = tok_start; a.parent = parent;
+  a.k_pages = k_pages; a.v_pages = v_pages; a.block_table = block_table; a.seq_lens = seq_lens;
+  a.pos = pos; a.ring_k = ring_k; a.ring_v = ring_v; a.o = o; a.lse = lse; a.ws = ws;
+  return cuda_status(kvs::launch_attn_tree(a, as_stream(stream)), "kvs_attn_tree");
 }
 
 namespace {

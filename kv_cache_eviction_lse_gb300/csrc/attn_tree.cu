@@ -1,0 +1,991 @@
+// Attention of a tree of drafted tokens per sequence over its rows' paged cache and window ring.
+// The m drafted tokens of a sequence are the last m paged tokens of its rows; token i sees all
+// keys before them, the ring's, and of the drafted ones itself and those above it in the tree:
+//   o_i = sum_k a_ik v_k,  a_ik = exp(q_i . k / sqrt(d) - lse_i) over what it sees.
+//
+// The g query heads of a KV head and the m tokens make m g query rows that read the same keys:
+// 4 d bytes and 4 d m g flops a key.  Up to 128 rows, one M = 128 tile of tcgen05, HBM bounds it
+// (64 rows: 64 flop/B where the chip has 286); more rows take more tiles, which read the keys
+// again from L2.
+//
+// Rows differ in length by the pruning, so the work is cut by tiles of 128 keys, not by rows: the
+// tiles of all (row, query tile) pairs form one stream, every block of a persistent grid takes an
+// equal contiguous share, and a pair that crosses a share's border is joined from partial sums
+// (running maximum, sum and weighted values) by a second kernel.  Shares depend on the lengths
+// alone, so results do too.  In a block:
+//   warps 0-3   copy K and V tiles by 16-byte cp.async into two 3-stage rings, in the 128-byte
+//               swizzled layout that the tensor core reads; pages may be of any size and end
+//               anywhere in a tile, which a TMA box could not
+//   warps 4-11  softmax, two threads per query row: S from TMEM, p = 2^(x - m), P as bf16 to TMEM
+//   warp 12     issues S = Q K^T (Q in TMEM) and O += P V (P in TMEM), M = 128 each
+// The registers of a block go to the softmax (setmaxnreg: 200 a thread, 56 for the others).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax of the
+// one before.  O is rescaled only when a row's maximum grows by more than 2^8.
+//
+// Which drafted tokens a token sees is a row of 256 bits, closed over the parents in log2(depth)
+// rounds at the start of a (row, query tile) whose share reaches the drafted keys.  A masked key
+// must not reach a row through 0 x inf: the V rows of drafted tokens are searched for infinities
+// and NaN, these multiply as zeros, and rows that do see them get them added at the end.
+#include <algorithm>
+
+#include <math_constants.h>
+
+#include "attn_tree.cuh"
+#include "launch.cuh"
+#include "tc.cuh"
+
+namespace kvs {
+
+__device__ int g_attn_tree_error = 0;
+
+namespace {
+
+constexpr int kErrWaitTimeout = 1;
+constexpr int kErrAttnTree = 10;  // a token start, parent, length or page id out of range
+
+constexpr int BM = 128;        // query rows of a tile = TMEM lanes
+constexpr int BN = 128;        // keys of a tile
+constexpr int kStages = 3;     // of the K ring and of the V ring
+constexpr int kCopyWarps = 4;  // 32 keys of a tile each
+constexpr int kSoftWarp = 4, kMmaWarp = 12;
+constexpr int kSoftThreads = 256;
+constexpr int kThreads = 16 * 32;  // three warps of the last four only share its registers
+constexpr int kWarps = kThreads / 32;
+constexpr int KC = BN / 2;     // keys of a softmax thread and tile
+constexpr int kLag = 3;        // copies (of half a stage) issued before one is waited for
+constexpr uint32_t kBox = 128 * 128;  // 128 rows x 64 bf16 (one 128-byte swizzle span)
+constexpr uint32_t kTmemCols = 512;
+constexpr int kCopyRegs = 56, kSoftRegs = 200, kMmaRegs = 56;
+static_assert(kCopyRegs + 2 * kSoftRegs + kMmaRegs <= 65536 / 128, "what the launch has");
+constexpr float kRescale = 8.f;  // log2 growth of the row max that forces a rescale of O
+constexpr int kMaxBlocks = 160;  // of the persistent grid; sizes the workspace
+constexpr int kWords = kMaxDraft / 32;
+constexpr long long kL2Bytes = 129ll << 20;
+constexpr int kJoinThreads = 256;
+constexpr int kDirty = 8;        // units whose mark for non-finite drafts is kept
+// Tiles whose bits of keys that are there are kept: a copy of tile i + 6 waits for the S product
+// of i + 3, and that for the softmax of i + 1.
+constexpr int kLive = 8;
+constexpr uint32_t kMaxSmem = 232448;
+
+template <int D>
+struct Cfg {
+  static constexpr uint32_t TILE = D / 64 * kBox;  // one K or V tile
+  static constexpr uint32_t OFF_K = 0;
+  static constexpr uint32_t OFF_V = OFF_K + kStages * TILE;
+  static constexpr uint32_t OFF_XM = OFF_V + kStages * TILE;     // row max exchange [2][2][BM]
+  static constexpr uint32_t OFF_XL = OFF_XM + 4 * BM * 4;        // row sum exchange [2][BM]
+  static constexpr uint32_t OFF_SEES = OFF_XL + 2 * BM * 4;      // [kMaxDraft][kWords]
+  static constexpr uint32_t OFF_UP = OFF_SEES + kMaxDraft * kWords * 4;  // [kMaxDraft]
+  static constexpr uint32_t OFF_BAR = OFF_UP + kMaxDraft * 4;
+  // q, k_full[3], k_empty[3], v_full[3], v_empty[3], s_full[2], s_empty[2], p[2], o[2], done
+  static constexpr uint32_t NBAR = 22;
+  static constexpr uint32_t USED = OFF_BAR + NBAR * 8;
+  static constexpr uint32_t SMEM = USED + 1024;
+  // TMEM columns: S buffers, then P (bf16 pairs of one tile), Q (bf16 pairs), O
+  static constexpr uint32_t COL_P = 2 * BN, COL_Q = COL_P + BN / 2, COL_O = COL_Q + D / 2;
+  static_assert(COL_O + D <= kTmemCols, "TMEM plan");
+  static_assert(SMEM + 2048 <= kMaxSmem, "shared-memory plan");
+};
+
+// A partial result: O transposed in chunks of four columns [D / 4][BM], then the reference and
+// the sum of each row.
+__host__ __device__ constexpr int part_floats(int d) { return BM * d + 2 * BM; }
+
+// Workspace: per block the (row, query tile) that ends there having begun in another block (row
+// -1: none) and that other block; per block the parts of the pairs that cross its borders (0:
+// began before, 1: goes on after).
+struct Ends { int row, mt, first, pad; };
+__host__ __device__ constexpr size_t ends_bytes() { return kMaxBlocks * sizeof(Ends); }
+__device__ __forceinline__ float* block_part(void* ws, int block, int side, int pf) {
+  return reinterpret_cast<float*>(static_cast<char*>(ws) + ends_bytes()) +
+         (size_t)(2 * block + side) * pf;
+}
+
+__device__ __forceinline__ void fault() { atomicCAS(&g_attn_tree_error, 0, kErrAttnTree); }
+
+// What a row holds: paged keys, all keys with the ring's, its sequence's first token and their
+// number (0 where the token starts are bad).
+struct Row {
+  int paged, all, t0, m;
+  __device__ __forceinline__ int tiles() const { return (all + BN - 1) / BN; }
+  __device__ __forceinline__ int first() const { return paged - m; }  // slot of drafted token 0
+};
+
+__device__ __forceinline__ Row row_of(const AttnTreeArgs& a, int r) {
+  const int b = r % a.B, t0 = a.tok_start[b], t1 = a.tok_start[b + 1];
+  const int paged = max(0, min(a.seq_lens[r], a.max_pages * a.page_size));
+  const bool good = t0 >= 0 && t1 >= t0 && t1 <= a.N && t1 - t0 <= a.max_draft;
+  return {paged, paged + (a.w > 0 ? max(0, min(a.pos[b], a.w)) : 0), t0, good ? t1 - t0 : 0};
+}
+
+__device__ __forceinline__ int query_tiles(int m, int g) { return (m * g + BM - 1) / BM; }
+
+// Segment of a (row, query tile) in a block's share.
+struct Unit {
+  int row, mt, ta, tb;  // key tiles ta .. tb - 1
+  Row is;
+  __device__ __forceinline__ bool whole() const { return ta == 0 && tb == is.tiles(); }
+};
+
+// Walks through the units of a share, every warp for itself: the lanes hold 32 rows.
+struct Walk {
+  const AttnTreeArgs& a;
+  int rows, g, lane, base, left;
+  Row mine;
+  Unit u;
+
+  __device__ __forceinline__ void fetch() {
+    mine = {0, 0, 0, 0};
+    if (base + lane < rows) mine = row_of(a, base + lane);
+  }
+  __device__ __forceinline__ void enter(int r) {
+    u.row = r;
+    u.is.paged = __shfl_sync(0xffffffffu, mine.paged, r - base);
+    u.is.all = __shfl_sync(0xffffffffu, mine.all, r - base);
+    u.is.t0 = __shfl_sync(0xffffffffu, mine.t0, r - base);
+    u.is.m = __shfl_sync(0xffffffffu, mine.m, r - base);
+  }
+  __device__ __forceinline__ void cut() {
+    u.tb = min(u.is.tiles(), u.ta + left);
+    left -= u.tb - u.ta;
+  }
+  __device__ __forceinline__ Walk(const AttnTreeArgs& args, int rows_, int g_, int row, int mt,
+                                  int ta, int tiles)
+      : a(args), rows(rows_), g(g_), lane(threadIdx.x & 31), base(row & ~31), left(tiles) {
+    fetch();
+    enter(row);
+    u.mt = mt;
+    u.ta = ta;
+    cut();
+  }
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    u.ta = 0;
+    if (u.mt + 1 < query_tiles(u.is.m, g)) {
+      ++u.mt;
+      cut();
+      return true;
+    }
+    u.mt = 0;
+    int from = u.row - base + 1;
+    for (;;) {
+      const uint32_t some = __ballot_sync(0xffffffffu, mine.all > 0 && mine.m > 0) &
+                            (from < 32 ? 0xffffffffu << from : 0u);
+      if (some) {
+        enter(base + __ffs(some) - 1);
+        cut();
+        return true;
+      }
+      base += 32;
+      from = 0;
+      if (base >= rows) return false;  // only if lengths change under the call
+      fetch();
+    }
+  }
+};
+
+// Equal contiguous shares of `blocks` blocks of a stream of tiles; the first `more` have one more
+// than `each`.
+struct Shares {
+  long long each = 1, more = 0;
+  __device__ __forceinline__ Shares(long long total, int blocks) {
+    if (total > blocks) {
+      each = total / blocks;
+      more = total - each * blocks;
+    }
+  }
+  __device__ __forceinline__ long long first(int block) const {
+    return block * each + min((long long)block, more);
+  }
+  __device__ __forceinline__ int of(long long tile) const {  // block of a tile
+    const long long wide = more * (each + 1);
+    return (int)(tile < wide ? tile / (each + 1) : more + (tile - wide) / each);
+  }
+};
+
+// 64 of the bits of a token's row from bit `off` on (which may be negative); bits outside are 0.
+__device__ __forceinline__ uint64_t bits_from(const uint32_t* row, int off) {
+  uint32_t w[3];
+  const int w0 = off >> 5, s = off & 31;  // rounds down
+#pragma unroll
+  for (int i = 0; i < 3; ++i) w[i] = (uint32_t)(w0 + i) < (uint32_t)kWords ? row[w0 + i] : 0u;
+  return (uint64_t)__funnelshift_r(w[1], w[2], s) << 32 | __funnelshift_r(w[0], w[1], s);
+}
+// The lowest n of 64 bits.
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
+
+__device__ __forceinline__ void named_sync(int id, int nthreads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// Registers a thread from here on; all warps of four call it.
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void cp_async16_once(uint32_t dst, const void* src, int src_bytes,
+                                                uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n" ::"r"(dst),
+               "l"(src), "r"(src_bytes), "l"(policy));
+}
+
+__device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float lse_of(float ref, float sum) {
+  return sum == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
+}
+
+// A warp's copies of its 32 keys of a tile.  Lane i finds where key i lies.
+template <int D>
+struct Copies {
+  const AttnTreeArgs& a;
+  const int warp, lane, ps_shift;
+  const uint64_t policy;
+  int page = -1, inside = 0, key = 0;      // of the tile looked up
+  const bf16_t *k = nullptr, *v = nullptr; // of the tile being copied; null: zeros
+
+  __device__ __forceinline__ void look_up(const Unit& u, int t) {
+    key = t * BN + warp * 32 + lane;
+    page = -1;
+    if (key < u.is.paged) {
+      const int idx = ps_shift >= 0 ? key >> ps_shift : key / a.page_size;
+      inside = key - idx * a.page_size;
+      page = a.block_table[(size_t)u.row * a.max_pages + idx];
+    }
+  }
+  __device__ __forceinline__ void resolve(const Unit& u) {
+    k = v = nullptr;
+    if (key < u.is.paged) {
+      if ((uint32_t)page < (uint32_t)a.capacity) {
+        const size_t at = ((size_t)page * a.page_size + inside) * D;
+        k = a.k_pages + at;
+        v = a.v_pages + at;
+      } else {
+        fault();
+      }
+    } else if (key < u.is.all) {
+      const size_t at = ((size_t)u.row * a.w + (key - u.is.paged)) * D;
+      k = a.ring_k + at;
+      v = a.ring_v + at;
+    }
+  }
+  static constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a step
+  // where this lane's chunk of a step goes in a tile
+  __device__ __forceinline__ uint32_t place(int step) const {
+    const int c = lane % kLanes, row = warp * 32 + step * kRows + lane / kLanes;
+    return (uint32_t)(c >> 3) * kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+  }
+  __device__ __forceinline__ void copy(const bf16_t* from, uint32_t tile) const {
+    const int c = lane % kLanes;
+#pragma unroll
+    for (int i = 0; i < 32 / kRows; ++i) {
+      const bf16_t* src = reinterpret_cast<const bf16_t*>(__shfl_sync(
+          0xffffffffu, reinterpret_cast<unsigned long long>(from), i * kRows + lane / kLanes));
+      const int bytes = src ? 16 : 0;
+      src = src ? src + c * 8 : a.q;
+      if (a.read_once) cp_async16_once(tile + place(i), src, bytes, policy);
+      else cp_async16(tile + place(i), src, bytes);
+    }
+  }
+  // Drafted rows lo .. hi - 1 of this warp's 32 of a V tile that has landed: what is not finite
+  // becomes 0; true if there was any.  A lane looks at the chunks that it copied.
+  __device__ __forceinline__ bool clean(uint8_t* tile, int lo, int hi) const {
+    bool any = false;
+    for (int i = 0; i < 32 / kRows; ++i) {
+      const int row = i * kRows + lane / kLanes;
+      if (row < lo || row >= hi) continue;
+      uint32_t* x = reinterpret_cast<uint32_t*>(tile + place(i));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t y = x[e];
+        if (not_finite(y)) y &= 0xffff0000u;
+        if (not_finite(y >> 16)) y &= 0xffffu;
+        if (y != x[e]) {
+          x[e] = y;
+          any = true;
+        }
+      }
+    }
+    return any;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
+    const __grid_constant__ AttnTreeArgs a, int rows, int ps_shift) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long warp_tiles[kWarps];
+  __shared__ int start_s[3];                 // row, query tile and key tile of the share's first
+  __shared__ uint32_t misc[2];               // TMEM address, abort flag
+  __shared__ int clean_s[kCopyWarps][kStages][2];  // rows of a stage's V that are drafted
+  __shared__ volatile uint32_t live_s[kLive][kCopyWarps];  // keys of a tile that are there
+  __shared__ volatile int dirty_s[kDirty];   // n + 1: unit n has drafted values that are not finite
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sb = raw + pad;
+  const uint32_t sK = sb + C::OFF_K, sV = sb + C::OFF_V;
+  float* xm = reinterpret_cast<float*>(smem + C::OFF_XM);
+  float* xl = reinterpret_cast<float*>(smem + C::OFF_XL);
+  uint32_t* sees = reinterpret_cast<uint32_t*>(smem + C::OFF_SEES);
+  int* up = reinterpret_cast<int*>(smem + C::OFF_UP);
+  const uint32_t bar0 = sb + C::OFF_BAR;
+  const uint32_t bar_q = bar0;  // the query rows are in TMEM (softmax threads arrive)
+  auto bar_kfull = [&](int s) { return bar0 + 8u * (1 + s); };
+  auto bar_kempty = [&](int s) { return bar0 + 8u * (4 + s); };
+  auto bar_vfull = [&](int s) { return bar0 + 8u * (7 + s); };
+  auto bar_vempty = [&](int s) { return bar0 + 8u * (10 + s); };
+  auto bar_sfull = [&](int s) { return bar0 + 8u * (13 + s); };   // S buffer s = tile & 1
+  auto bar_sempty = [&](int s) { return bar0 + 8u * (15 + s); };  // the softmax read it
+  // P(i) is ready on p[i & 1] and O += P(i) V(i) completes on o[i & 1]: the softmax waits for
+  // P V(i - 1) before it writes P(i), so neither barrier runs two phases ahead of a waiter
+  auto bar_p = [&](int i) { return bar0 + 8u * (17 + (i & 1)); };
+  auto bar_o = [&](int i) { return bar0 + 8u * (19 + (i & 1)); };
+  const uint32_t bar_done = bar0 + 8u * 21;
+  volatile uint32_t* abort_flag = misc + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.Hq / a.Hkv;
+
+  if (tid == 0) {
+    tc::mbar_init(bar_q, kSoftThreads);
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(bar_kfull(s), kCopyWarps);
+      tc::mbar_init(bar_kempty(s), 1);
+      tc::mbar_init(bar_vfull(s), kCopyWarps);
+      tc::mbar_init(bar_vempty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(bar_sfull(s), 1);
+      tc::mbar_init(bar_sempty(s), kSoftThreads);
+      tc::mbar_init(bar_p(s), kSoftThreads);
+      tc::mbar_init(bar_o(s), 1);
+    }
+    tc::mbar_init(bar_done, 1);
+    misc[1] = 0u;
+    tc::fence_mbar_init();
+  }
+  if (tid < kDirty) dirty_s[tid] = 0;
+  if (tid < 3) start_s[tid] = 0;  // stays only if lengths change under the call
+  // started beside the end of the kernel before; the join must not start beside that one too
+  wait_for_previous();
+  let_next_start();
+
+  // --- tiles of all rows: every thread a contiguous range of them
+  const int per = (rows + kThreads - 1) / kThreads;
+  const int r0 = min(tid * per, rows), r1 = min(r0 + per, rows);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Row x = row_of(a, r);
+    mine += x.m > 0 ? (long long)x.tiles() * query_tiles(x.m, g) : 0;
+    if (blockIdx.x == 0) {
+      const int b = r % a.B, m = a.tok_start[b + 1] - a.tok_start[b];
+      if (a.seq_lens[r] != x.paged || m != x.m || x.paged < x.m) fault();
+    }
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_tiles[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_tiles[w];
+    total += warp_tiles[w];
+  }
+  const Shares shares(total, gridDim.x);
+  Ends* ends = static_cast<Ends*>(a.ws);
+  if (blockIdx.x >= total) {
+    if (tid == 0) ends[blockIdx.x] = {-1, 0, 0, 0};
+    return;
+  }
+  const long long s0 = shares.first(blockIdx.x);
+  const int tiles = (int)(min(shares.first(blockIdx.x + 1), total) - s0);
+  if (before <= s0 && s0 < before + mine) {
+    long long at = s0 - before;
+    for (int r = r0; r < r1; ++r) {
+      const Row x = row_of(a, r);
+      const long long n = x.m > 0 ? (long long)x.tiles() * query_tiles(x.m, g) : 0;
+      if (at < n) {
+        start_s[0] = r;
+        start_s[1] = (int)(at / x.tiles());
+        start_s[2] = (int)(at - (long long)start_s[1] * x.tiles());
+        break;
+      }
+      at -= n;
+    }
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(smem_u32(misc), kTmemCols);
+    tc::tmem_relinquish();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = misc[0];
+  const uint32_t t_p = tmem + C::COL_P, t_q = tmem + C::COL_Q, t_o = tmem + C::COL_O;
+  if (tid == 0) {
+    Ends e = {-1, 0, 0, 0};
+    const int nt = row_of(a, start_s[0]).tiles();
+    if (start_s[2] > 0 && start_s[2] + tiles >= nt)
+      e = {start_s[0], start_s[1], shares.of(s0 - start_s[2]), 0};
+    ends[blockIdx.x] = e;
+  }
+  // A wait that has run out, here or elsewhere in the block: from then on a warp only goes
+  // through the motions (arrivals and named barriers, no waits, no TMEM), so that none is left
+  // waiting for it.  The same in all lanes.
+  bool dead = false;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (dead) return;
+    bool ok = tc::mbar_wait(bar, parity);
+    if (!ok) {
+      *abort_flag = 1u;
+      atomicCAS(&g_attn_tree_error, 0, kErrWaitTimeout);
+    }
+    ok = ok && !*abort_flag;
+    dead = !__all_sync(0xffffffffu, ok);
+  };
+
+  if (warp < kCopyWarps) {
+    // ============================================================ copies of K and V
+    give_registers<kCopyRegs>();
+    Walk walk(a, rows, g, start_s[0], start_s[1], start_s[2], tiles);
+    Copies<D> copies{a, warp, lane, ps_shift, read_once_policy()};
+    int unit = 0, t = walk.u.ta;
+    // copy 2 i is K of tile i of the share, copy 2 i + 1 its V; one is announced when it has
+    // landed, kLag copies later
+    auto announce = [&](int c) {
+      const int i = c >> 1, s = i % kStages;
+      if (c & 1) {
+        const int lo = clean_s[warp][s][0], hi = clean_s[warp][s][1];
+        // the unit's number is kept beside the first row
+        if ((lo & 63) < hi && copies.clean(smem + C::OFF_V + s * C::TILE, lo & 63, hi))
+          dirty_s[(lo >> 6) % kDirty] = (lo >> 6) + 1;
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive((c & 1) ? bar_vfull(s) : bar_kfull(s));
+    };
+    copies.look_up(walk.u, t);
+    int i = 0;
+    for (; i < tiles && !dead; ++i) {
+      copies.resolve(walk.u);
+      const int s = i % kStages;
+      const uint32_t empty = (uint32_t)(i / kStages & 1) ^ 1u;
+      // the tile's drafted rows among this warp's
+      const int k0 = t * BN + warp * 32;
+      const int lo = max(0, min(32, walk.u.is.first() - k0)), hi = max(0, min(32, walk.u.is.paged - k0));
+      const int mark = unit << 6 | lo, end = walk.u.is.m > 1 && lo < hi ? hi : -1;
+      // where the next tile's keys lie, a tile early
+      if (i + 1 < tiles) {
+        if (++t == walk.u.tb) {
+          walk.next();
+          t = walk.u.ta;
+          ++unit;
+        }
+        copies.look_up(walk.u, t);
+      }
+      const uint32_t there = __ballot_sync(0xffffffffu, copies.k != nullptr);
+      wait(bar_kempty(s), empty);
+      if (dead) break;
+      if (lane == 0) live_s[i % kLive][warp] = there;
+      copies.copy(copies.k, sK + s * C::TILE);
+      cp_async_commit();
+      cp_async_wait<kLag>();
+      if (2 * i >= kLag) announce(2 * i - kLag);
+      wait(bar_vempty(s), empty);
+      if (dead) break;
+      if (lane == 0) {
+        clean_s[warp][s][0] = mark;
+        clean_s[warp][s][1] = end < 0 ? 0 : end;
+      }
+      copies.copy(copies.v, sV + s * C::TILE);
+      cp_async_commit();
+      cp_async_wait<kLag>();
+      if (2 * i + 1 >= kLag) announce(2 * i + 1 - kLag);
+    }
+    cp_async_wait<0>();
+    if (!dead)
+      for (int c = max(0, 2 * tiles - kLag); c < 2 * tiles; ++c) announce(c);
+  } else if (warp >= kMmaWarp) {
+    // ============================================================ MMA issuer
+    give_registers<kMmaRegs>();
+    if (warp == kMmaWarp) {
+      Walk walk(a, rows, g, start_s[0], start_s[1], start_s[2], tiles);
+      constexpr uint32_t idesc_s = tc::idesc_bf16(BM, BN);
+      constexpr uint32_t idesc_o = tc::idesc_bf16_bmn(BM, D);
+      int gs = 0, gp = 0;  // S and P V products issued (all units)
+      int n = 0;
+      do {
+        const int count = walk.u.tb - walk.u.ta;
+        // the unit's query rows are in TMEM, and the softmax threads have read the previous
+        // unit's O (they arrive after both), so P V(0) may overwrite it
+        wait(bar_q, (uint32_t)n & 1u);
+        ++n;
+        for (int j = 0; j <= count && !dead; ++j) {
+          if (j < count) {  // S = Q K^T into S buffer gs & 1
+            const int s = gs % kStages, sbuf = gs & 1;
+            wait(bar_kfull(s), (uint32_t)(gs / kStages) & 1u);
+            wait(bar_sempty(sbuf), ((uint32_t)(gs >> 1) & 1u) ^ 1u);
+            if (dead) break;
+            tc::fence_after_sync();
+            if (lane == 0) {
+              const uint32_t k_s = sK + s * C::TILE;
+  #pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t o = (uint32_t)(k >> 2) * kBox + (uint32_t)(k & 3) * 32u;
+                tc::mma_bf16_ts(tmem + (uint32_t)(sbuf * BN), t_q + 8u * k, tc::sdesc_sw128(k_s + o),
+                                idesc_s, k > 0 ? 1u : 0u);
+              }
+              tc::commit(bar_sfull(sbuf));
+              tc::commit(bar_kempty(s));
+            }
+            __syncwarp();
+            ++gs;
+          }
+          if (j >= 1) {  // O += P V of the unit's tile j - 1
+            const int s = gp % kStages;
+            wait(bar_p(gp), (uint32_t)(gp >> 1) & 1u);
+            wait(bar_vfull(s), (uint32_t)(gp / kStages) & 1u);
+            if (dead) break;
+            tc::fence_after_sync();
+            if (lane == 0) {
+              const uint32_t v_s = sV + s * C::TILE;
+  #pragma unroll
+              for (int k = 0; k < BN / 16; ++k)
+                tc::mma_bf16_ts(t_o, t_p + 8u * k, tc::sdesc_sw128_mn(v_s + 2048u * k, kBox), idesc_o,
+                                (j > 1 || k > 0) ? 1u : 0u);
+              tc::commit(bar_vempty(s));
+              tc::commit(bar_o(gp));
+            }
+            __syncwarp();
+            ++gp;
+          }
+        }
+      } while (!dead && walk.next());
+      // drain: every MMA issued so far has completed once this commit lands
+      if (lane == 0) {
+        tc::commit(bar_done);
+        tc::mbar_wait(bar_done, 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ============================================================ softmax + epilogue
+    take_registers<kSoftRegs>();
+    Walk walk(a, rows, g, start_s[0], start_s[1], start_s[2], tiles);
+    constexpr int OC = D / 2;   // O columns of this thread in the rescale / epilogue
+    constexpr int QW = D / 4;   // 32-bit words (bf16 pairs) of the query row per thread
+    const int st = tid - kSoftWarp * 32;     // softmax thread
+    const int h = (warp - kSoftWarp) >> 2;   // key half of each tile (and of O's columns)
+    const int eq = warp & 3;                 // TMEM lane quarter
+    const int row = eq * 32 + lane;          // query row within the tile
+    const uint32_t lane_off = (uint32_t)(eq * 32) << 16;
+    const float sc2 = rsqrtf((float)D) * kLog2e;
+    uint32_t qv[QW];
+    int my_up = -1;       // parent of drafted token st
+    // this thread's part of a unit's query row (zeros past the last), and its token's parent
+    auto load_q = [&](const Unit& u) {
+      const int x = u.mt * BM + row;
+      if (x < u.is.m * g) {
+        const int i = x / g, hd = x - i * g, l_hk = u.row / a.B;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + (((size_t)l_hk * g + hd) * a.N + u.is.t0 + i) * D + h * OC);
+#pragma unroll
+        for (int c = 0; c < QW / 4; ++c) {
+          const uint4 y = src[c];
+          qv[4 * c] = y.x;
+          qv[4 * c + 1] = y.y;
+          qv[4 * c + 2] = y.z;
+          qv[4 * c + 3] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < QW; ++c) qv[c] = 0u;
+      }
+      if (a.parent && st < u.is.m) my_up = a.parent[u.is.t0 + st];
+    };
+    auto store_q = [&] {
+      if (dead) return;
+      if constexpr (QW == 32) tc::tmem_st32(t_q + lane_off + (uint32_t)(h * QW), qv);
+      else tc::tmem_st16(t_q + lane_off + (uint32_t)(h * QW), qv);
+      tc::tmem_st_wait();
+    };
+    load_q(walk.u);
+    store_q();
+    int gs = 0;  // tiles processed (all units): S buffer, exchange buffer, P and O barriers
+    int sees_of = -1;  // sequence whose tree is in `sees`
+    for (int n = 0;; ++n) {
+      const Unit u = walk.u;
+      const int x = u.mt * BM + row, live = u.is.m * g - u.mt * BM;  // query rows of the unit
+      const int i = x / g, hd = x - i * g, first = u.is.first();
+      const bool mine_live = row < live, warp_live = eq * 32 < live;
+      tc::fence_before_sync();
+      tc::mbar_arrive(bar_q);  // the unit's query rows are in TMEM, the previous unit's O is read
+      // --- which drafted tokens each one sees, if the segment has drafted keys
+      const int b = u.row % a.B;
+      if (a.parent && u.is.m > 1 && u.tb * BN > first && sees_of != b) {
+        sees_of = b;
+        uint32_t bits[kWords];
+        int p = -1;
+        if (st < u.is.m) {
+          p = my_up;
+          if (p < -1 || p >= st) {
+            fault();
+            p = -1;
+          }
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) bits[w] = w == st >> 5 ? 1u << (st & 31) : 0u;
+        }
+        // after `round` rounds a token has the 2^round next ones on its way up, and `up` the one
+        // above those
+        bool more = true;
+        for (int round = 0; more && round < 9; ++round) {
+          named_sync(1, kSoftThreads);  // all have read the row of the round (or unit) before
+          if (st < u.is.m) {
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) sees[st * kWords + w] = bits[w];
+            up[st] = p;
+          }
+          more = tc::bar_or(2, kSoftThreads, p >= 0);
+          if (p >= 0) {
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) bits[w] |= sees[p * kWords + w];
+            p = up[p];
+          }
+        }
+      }
+      float m_used = -CUDART_INF_F, lsum = 0.f;
+      for (int j = u.ta; j < u.tb; ++j, ++gs) {
+        const int s = gs & 1;  // max-exchange buffer and S buffer
+        wait(bar_sfull(s), (uint32_t)(gs >> 1) & 1u);
+        tc::fence_after_sync();
+        if (!warp_live) {
+          tc::mbar_arrive(bar_sempty(s));
+          tc::mbar_arrive(bar_p(gs));
+          continue;
+        }
+        uint32_t v[KC];
+        if (!dead) {
+#pragma unroll
+          for (int c = 0; c < KC; c += 32)
+            tc::tmem_ld32(tmem + lane_off + (uint32_t)(s * BN + h * KC + c), v + c);
+          tc::tmem_ld_wait();
+        }
+        // of the thread's 64 keys: those there are, without drafted ones that are not seen
+        uint64_t vis = (uint64_t)live_s[gs % kLive][2 * h + 1] << 32 | live_s[gs % kLive][2 * h];
+        tc::fence_before_sync();
+        tc::mbar_arrive(bar_sempty(s));  // the next S into this buffer may start now
+        const int kb = j * BN + h * KC;
+        if (kb + KC > first && kb < u.is.paged) {
+          const uint64_t drafts = low_bits(u.is.paged - kb) & ~low_bits(first - kb);
+          const uint64_t seen = !a.parent || u.is.m == 1 ? low_bits(first + i + 1 - kb)
+                                : mine_live ? bits_from(sees + i * kWords, kb - first) : 0ull;
+          vis &= ~drafts | seen;
+        }
+        if (~vis) {
+          const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
+#pragma unroll
+          for (int c = 0; c < KC; ++c)
+            if (!((c < 32 ? lo : hi) >> (c & 31) & 1u)) v[c] = __float_as_uint(-CUDART_INF_F);
+        }
+        float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F, mx2 = -CUDART_INF_F, mx3 = -CUDART_INF_F;
+#pragma unroll
+        for (int c = 0; c < KC; c += 8) {
+          mx0 = tc::max3(mx0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+          mx1 = tc::max3(mx1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+          mx2 = tc::max3(mx2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
+          mx3 = tc::max3(mx3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
+        }
+        float top = tc::max3(mx0, mx1, fmaxf(mx2, mx3)) * sc2;
+        // the two threads of a row are warps eq + 4 and eq + 8: a named barrier per lane quarter
+        float* xmj = xm + s * 2 * BM;
+        xmj[h * BM + row] = top;
+        named_sync(3 + eq, 64);
+        top = fmaxf(top, xmj[(h ^ 1) * BM + row]);
+        const bool need = top > m_used + kRescale;
+        float factor = 1.f;
+        if (need) {
+          factor = fast_exp2(m_used - top);  // 0 for the first keys
+          m_used = top;
+          lsum *= factor;
+        }
+        // p = 2^(x sc2 - m) with packed fp32 pairs; each weight is rounded to bf16 once for P V, as
+        // the output is, and enters the sum as it was
+        uint32_t pk[KC / 2];
+        const float2 k2 = make_float2(sc2, sc2), nm = make_float2(-finite_ref(m_used), -finite_ref(m_used));
+        float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+        for (int c = 0; c < KC; c += 4) {
+          const float2 y0 = __ffma2_rn(tc::f2(v[c], v[c + 1]), k2, nm);
+          const float2 y1 = __ffma2_rn(tc::f2(v[c + 2], v[c + 3]), k2, nm);
+          const float p0 = fast_exp2(y0.x), p1 = fast_exp2(y0.y);
+          const float p2 = fast_exp2(y1.x), p3 = fast_exp2(y1.y);
+          a0 = __fadd2_rn(a0, make_float2(p0, p1));
+          a1 = __fadd2_rn(a1, make_float2(p2, p3));
+          pk[c / 2] = pack2(p0, p1);
+          pk[c / 2 + 1] = pack2(p2, p3);
+        }
+        a0 = __fadd2_rn(a0, a1);
+        lsum += a0.x + a0.y;
+
+        // P V of the previous tile has read its P (and finished O) before P is written; O is
+        // rescaled only when a row's max grew past the threshold.  The unit's first tile needs
+        // no wait: the previous unit's last P V was waited for below.
+        const bool any_need = __any_sync(0xffffffffu, need);
+        if (j > u.ta) {
+          wait(bar_o(gs - 1), (uint32_t)((gs - 1) >> 1) & 1u);
+          tc::fence_after_sync();
+          if (!dead && any_need) {
+            const uint32_t to = t_o + lane_off + (uint32_t)(h * OC);
+#pragma unroll
+            for (int cb = 0; cb < OC; cb += 32) {
+              tc::tmem_ld32(to + cb, v);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * factor);
+              tc::tmem_st32(to + cb, v);
+            }
+            tc::tmem_st_wait();
+          }
+        }
+        if (!dead) {
+          tc::tmem_st32(t_p + lane_off + (uint32_t)(h * (KC / 2)), pk);
+          tc::tmem_st_wait();
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(bar_p(gs));
+      }
+      const bool go_on = walk.next();
+      // the next unit's query rows load while this unit's O is finished, and take the place of this
+      // unit's, whose S products are complete
+      if (go_on) load_q(walk.u);
+      // the last two P V products of the unit (on o[0] and o[1]) complete O
+      if (u.tb - u.ta > 1) wait(bar_o(gs - 2), (uint32_t)((gs - 2) >> 1) & 1u);
+      wait(bar_o(gs - 1), (uint32_t)((gs - 1) >> 1) & 1u);
+      tc::fence_after_sync();
+      if (go_on) store_q();
+      if (warp_live) {
+        xl[h * BM + row] = lsum;
+        named_sync(3 + eq, 64);
+        lsum += xl[(h ^ 1) * BM + row];
+        const bool dirty = dirty_s[n % kDirty] == n + 1;
+        const float inv = inverse(lsum);
+        const size_t out = ((size_t)(u.row / a.B) * g + hd) * a.N + u.is.t0 + i;
+        float* part = block_part(a.ws, blockIdx.x, u.ta > 0 ? 0 : 1, part_floats(D));
+#pragma unroll 1
+        for (int cb = 0; cb < OC && !dead; cb += 32) {
+          uint32_t v[32];
+          tc::tmem_ld32(t_o + lane_off + (uint32_t)(h * OC + cb), v);
+          tc::tmem_ld_wait();
+          if (dirty && mine_live) {
+            // drafted values that are not finite were zeros above: rows that see them get them
+            const int k0 = max(0, u.ta * BN - first), k1 = min(u.is.m, u.tb * BN - first);
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k) {
+              const int slot = first + k;
+              const bool seen = !a.parent ? k <= i : sees[i * kWords + (k >> 5)] >> (k & 31) & 1;
+              if (!seen || slot < 0) continue;
+              const int idx = slot / a.page_size;
+              const int page = a.block_table[(size_t)u.row * a.max_pages + idx];
+              if ((uint32_t)page >= (uint32_t)a.capacity) continue;
+              const bf16_t* src =
+                  a.v_pages + ((size_t)page * a.page_size + slot - idx * a.page_size) * D + h * OC + cb;
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const uint32_t y = *reinterpret_cast<const uint32_t*>(src + c);
+                if (not_finite(y)) v[c] = __float_as_uint(__uint_as_float(v[c]) + bf16_lo(y));
+                if (not_finite(y >> 16))
+                  v[c + 1] = __float_as_uint(__uint_as_float(v[c + 1]) + bf16_hi(y));
+              }
+            }
+          }
+          if (!mine_live) continue;
+          if (u.whole()) {
+            uint4* dst = reinterpret_cast<uint4*>(a.o + out * D + h * OC + cb);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                y[e] = pack2(__uint_as_float(v[8 * c + 2 * e]) * inv,
+                             __uint_as_float(v[8 * c + 2 * e + 1]) * inv);
+              dst[c] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(part) + (h * OC + cb) / 4 * BM + row;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              dst[c * BM] = make_float4(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
+                                        __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]));
+          }
+        }
+        if (mine_live && h == 0 && !dead) {
+          if (!u.whole()) {
+            part[BM * D + row] = m_used;
+            part[BM * D + BM + row] = lsum;
+          } else if (a.lse) {
+            a.lse[out] = lse_of(m_used, lsum);
+          }
+        }
+      }
+      if (!go_on) break;
+    }
+  }
+
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Pairs that cross blocks: block x joins the pair that ends in block x of the first kernel, from
+// the part of its first block and those after.  A thread takes eight columns of a query row.
+// While the first kernel runs: zeros for tokens that no key is there for.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(
+    const __grid_constant__ AttnTreeArgs a, int rows) {
+  const int g = a.Hq / a.Hkv;
+  const int every = gridDim.x * gridDim.y * (kJoinThreads / 32), lane = threadIdx.x & 31;
+  for (int r = (blockIdx.y * gridDim.x + blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+       r < rows; r += every) {
+    const Row x = row_of(a, r);
+    if (x.all > 0) continue;
+    for (int i = lane; i < x.m * g; i += 32) {
+      const size_t out = ((size_t)(r / a.B) * g + i % g) * a.N + x.t0 + i / g;
+      for (int e = 0; e < D / 8; ++e)
+        reinterpret_cast<uint4*>(a.o + out * D)[e] = make_uint4(0, 0, 0, 0);
+      if (a.lse) a.lse[out] = -INFINITY;
+    }
+  }
+  wait_for_previous();
+  const Ends end = static_cast<const Ends*>(a.ws)[blockIdx.x];
+  // the bounds hold even if another stream writes the workspace meanwhile
+  if ((uint32_t)end.row >= (uint32_t)rows || (uint32_t)end.first >= blockIdx.x || end.mt < 0) return;
+  const Row is = row_of(a, end.row);
+  const int item = blockIdx.y * kJoinThreads + threadIdx.x, row = item % BM, c8 = item / BM;
+  const long long x = (long long)end.mt * BM + row;
+  if (x >= (long long)is.m * g) return;
+  const int n = blockIdx.x - end.first + 1;
+  constexpr int kAhead = 4;
+  float top = -INFINITY, sum = 0.f, acc[8] = {};
+  for (int p0 = 0; p0 < n; p0 += kAhead) {
+    float ref[kAhead], l[kAhead];
+    float4 y[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int p = min(p0 + i, n - 1);
+      const float* part = block_part(a.ws, end.first + p, p == 0 ? 1 : 0, part_floats(D));
+      y[i][0] = reinterpret_cast<const float4*>(part)[2 * c8 * BM + row];
+      y[i][1] = reinterpret_cast<const float4*>(part)[(2 * c8 + 1) * BM + row];
+      ref[i] = part[BM * D + row];
+      l[i] = part[BM * D + BM + row];
+    }
+    float high = top;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) high = fmaxf(high, ref[i]);
+    const float base = finite_ref(high), w = fast_exp2(top - base);
+    sum *= w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= w;
+    top = high;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (p0 + i >= n) break;
+      const float v = fast_exp2(ref[i] - base);
+      sum += l[i] * v;
+      acc[0] += y[i][0].x * v;
+      acc[1] += y[i][0].y * v;
+      acc[2] += y[i][0].z * v;
+      acc[3] += y[i][0].w * v;
+      acc[4] += y[i][1].x * v;
+      acc[5] += y[i][1].y * v;
+      acc[6] += y[i][1].z * v;
+      acc[7] += y[i][1].w * v;
+    }
+  }
+  const int i = (int)x / g, hd = (int)x - i * g;
+  const size_t out = ((size_t)(end.row / a.B) * g + hd) * a.N + is.t0 + i;
+  const float inv = inverse(sum);
+  reinterpret_cast<uint4*>(a.o + out * D)[c8] =
+      make_uint4(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv),
+                 pack2(acc[4] * inv, acc[5] * inv), pack2(acc[6] * inv, acc[7] * inv));
+  if (a.lse && c8 == 0) a.lse[out] = lse_of(top, sum);
+}
+
+template <int D>
+cudaError_t launch(AttnTreeArgs a, int rows, cudaStream_t s) {
+  using C = Cfg<D>;
+  static int nsm[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!nsm[dev]) {
+    e = cudaDeviceGetAttribute(&nsm[dev], cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+  }
+  int shift = -1;
+  if ((a.page_size & (a.page_size - 1)) == 0)
+    for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
+  const long long row_tiles = ((long long)a.max_pages * a.page_size + a.w + BN - 1) / BN;
+  const long long query = ((long long)a.max_draft * (a.Hq / a.Hkv) + BM - 1) / BM;
+  a.read_once = query == 1 && (long long)rows * row_tiles * 2 * C::TILE > kL2Bytes / 2;
+  const int sms = std::min(nsm[dev], kMaxBlocks);
+  // no more blocks than tiles could need
+  const int blocks = (int)std::min<long long>(sms, (long long)rows * query * row_tiles);
+  e = cudaFuncSetAttribute(attn_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  count_launches(2);
+  Launch first(dim3(blocks), kThreads, s);
+  first.cfg.dynamicSmemBytes = C::SMEM;
+  e = cudaLaunchKernelEx(&first.cfg, attn_tree_kernel<D>, a, rows, shift);
+  if (e != cudaSuccess) return e;
+  Launch join(dim3(blocks, BM * (D / 8) / kJoinThreads), kJoinThreads, s);
+  return cudaLaunchKernelEx(&join.cfg, attn_tree_join_kernel<D>, a, rows);
+}
+
+}  // namespace
+
+size_t attn_tree_workspace_bytes(int d) {
+  return ends_bytes() + (size_t)kMaxBlocks * 2 * part_floats(d) * sizeof(float);
+}
+
+cudaError_t launch_attn_tree(const AttnTreeArgs& args, cudaStream_t s) {
+  AttnTreeArgs a = args;
+  const int rows = a.L * a.Hkv * a.B;
+  if (rows == 0 || a.N == 0) return cudaSuccess;
+  return a.d == 128 ? launch<128>(a, rows, s) : launch<64>(a, rows, s);
+}
+
+cudaError_t attn_tree_device_error(int* code, bool clear, cudaStream_t s) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(code, g_attn_tree_error, sizeof(int), 0,
+                                            cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && clear && *code) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_attn_tree_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
+  return e;
+}
+
+}  // namespace kvs

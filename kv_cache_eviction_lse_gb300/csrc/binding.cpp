@@ -1,6 +1,6 @@
 // The Python side of the calls that a decode loop makes for every token: kvs_rope,
-// kvs_append_paged and kvs_attn_decode, and around drafted tokens kvs_accept_paged,
-// kvs_fork_paged and kvs_reclaim_paged.  Their kernels take 2 to 10 us for a token of a batch,
+// kvs_append_paged and kvs_attn_decode, and around drafted tokens kvs_attn_tree,
+// kvs_accept_paged, kvs_fork_paged and kvs_reclaim_paged.  Their kernels take 2 to 10 us for a token of a batch,
 // and up to 25 arguments checked and converted in Python took longer: calls back to back are
 // one per 6.8 us (rotation of 64 tokens), 13.2 (their append) and 8.7 (attention of a short
 // sequence) that way, and 2.9, 5.0 and 5.9 through this file, launches included.  Arguments
@@ -294,6 +294,36 @@ PyObject* attn_decode(PyObject*, PyObject* const* x, Py_ssize_t nx) {
   });
 }
 
+PyObject* attn_tree(PyObject*, PyObject* const* x, Py_ssize_t nx) {
+  return guarded([&] {
+    expect(nx, 23);
+    kvs_dims dm;
+    dims(x[0], &dm);
+    const int32_t B = int32(x[1], "B"), N = int32(x[2], "N"), md = int32(x[3], "max_draft");
+    const int32_t ps = int32(x[7], "page_size"), cap = int32(x[10], "capacity_pages");
+    const int32_t mp = int32(x[12], "max_pages"), w = int32(x[14], "w");
+    const int64_t ws_bytes = integer(x[21], "ws_bytes", 0, INT64_MAX);
+    const Place at(x[22]);
+    const int64_t rows = times(dm.L, dm.H_kv, B), heads = times(dm.L, dm.H_q, N);
+    const int64_t nq = times(heads, dm.d), pool = times(cap, ps, dm.d), ring = times(rows, w, dm.d);
+    const int32_t *tok = at.i32(x[4], (int64_t)B + 1, "tok_start"), *up = at.i32(x[5], N, "parent");
+    const kvs_bf16* q = at.bf16(x[6], nq, "q");
+    const kvs_bf16 *kp = at.bf16(x[8], pool, "k_pages"), *vp = at.bf16(x[9], pool, "v_pages");
+    const int32_t* bt = at.i32(x[11], times(rows, mp), "block_table");
+    const int32_t *sl = at.i32(x[13], rows, "seq_lens"), *pos = at.i32(x[15], w ? B : 0, "pos");
+    const kvs_bf16 *rk = at.bf16(x[16], ring, "ring_k"), *rv = at.bf16(x[17], ring, "ring_v");
+    kvs_bf16* o = at.bf16(x[18], nq, "o");
+    float* lse = at.arg<float>(x[19], at::kFloat, heads, "lse");
+    void* ws = at.arg<void>(x[20], at::kByte, ws_bytes, "ws");
+    kvs_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = kvs_attn_tree(&dm, B, N, md, tok, up, q, ps, kp, vp, cap, bt, mp, sl, w, pos, rk, rv, o, lse,
+                       ws, (size_t)ws_bytes, at.stream);
+    Py_END_ALLOW_THREADS
+    return st;
+  });
+}
+
 PyObject* accept_paged(PyObject*, PyObject* const* x, Py_ssize_t nx) {
   return guarded([&] {
     expect(nx, 15);
@@ -377,6 +407,7 @@ PyMethodDef methods[] = {
     {"rope", (PyCFunction)(void (*)())rope, METH_FASTCALL, nullptr},
     {"append_paged", (PyCFunction)(void (*)())append_paged, METH_FASTCALL, nullptr},
     {"attn_decode", (PyCFunction)(void (*)())attn_decode, METH_FASTCALL, nullptr},
+    {"attn_tree", (PyCFunction)(void (*)())attn_tree, METH_FASTCALL, nullptr},
     {"accept_paged", (PyCFunction)(void (*)())accept_paged, METH_FASTCALL, nullptr},
     {"fork_paged", (PyCFunction)(void (*)())fork_paged, METH_FASTCALL, nullptr},
     {"reclaim_paged", (PyCFunction)(void (*)())reclaim_paged, METH_FASTCALL, nullptr},

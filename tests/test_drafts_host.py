@@ -1,4 +1,4 @@
-"""Host-side checks of kvs_accept_paged, kvs_fork_paged and kvs_reclaim_paged: refusals with
+"""Host-side checks of kvs_attn_tree, kvs_accept_paged, kvs_fork_paged and kvs_reclaim_paged: refusals with
 their status codes, empty calls, workspace sizes, and what the binding refuses.  No GPU: every
 call fails validation, or is an empty call, before anything is enqueued."""
 import ctypes
@@ -15,6 +15,13 @@ def C():
     build.build()
     from kv_cache_eviction_lse_gb300 import capi
     return capi
+
+
+def tree(C, dm=None, B=2, N=6, md=8, tok=FAKE, up=FAKE, q=FAKE, ps=16, kp=FAKE, vp=FAKE, cap=8, bt=FAKE, mp=4,
+         sl=FAKE, w=3, pos=FAKE, rk=FAKE, rv=FAKE, o=FAKE, lse=FAKE, ws=FAKE, wsb=1 << 30):
+    dm = dm or C.dims(1, 4, 2, 128)
+    return C._lib.kvs_attn_tree(ctypes.byref(dm), B, N, md, tok, up, q, ps, kp, vp, cap, bt, mp, sl, w, pos,
+                                rk, rv, o, lse, ws, wsb, None)
 
 
 def accept(C, dm=None, B=2, N=6, tok=FAKE, n=FAKE, path=FAKE, ps=16, kp=FAKE, vp=FAKE, cap=8, bt=FAKE,
@@ -38,7 +45,7 @@ def reclaim(C, dm=None, B=4, ps=16, kp=FAKE, vp=FAKE, cap=8, nxt=FAKE, nxo=FAKE,
                                     wsb, None)
 
 
-@pytest.mark.parametrize("call", [accept, fork, reclaim], ids=lambda f: f.__name__)
+@pytest.mark.parametrize("call", [tree, accept, fork, reclaim], ids=lambda f: f.__name__)
 def test_what_they_share(C, call):
     assert call(C, C.dims(0, 4, 2, 128)) == C.KVS_ERR_SHAPE
     assert call(C, C.dims(1, 3, 2, 128)) == C.KVS_ERR_SHAPE
@@ -47,12 +54,28 @@ def test_what_they_share(C, call):
     assert call(C, B=-1) == C.KVS_ERR_ARG and call(C, cap=-1) == C.KVS_ERR_ARG
     assert call(C, ps=0) == C.KVS_ERR_UNSUPPORTED and call(C, ps=4097) == C.KVS_ERR_UNSUPPORTED
     assert call(C, mp=0) == C.KVS_ERR_SHAPE
-    names = dict(accept=("tok", "n", "path", "kp", "vp", "bt", "sl", "slo"),
+    names = dict(tree=("tok", "q", "kp", "vp", "bt", "sl", "pos", "rk", "rv", "o", "ws"),
+                 accept=("tok", "n", "path", "kp", "vp", "bt", "sl", "slo"),
                  fork=("src", "dst", "kp", "vp", "nxt", "nxo", "bt", "sl", "pos", "rs", "rk", "rv", "ws"),
                  reclaim=("kp", "vp", "nxt", "nxo", "bt", "bto", "sl", "ws"))[call.__name__]
     for name in names:
         assert call(C, **{name: None}) == C.KVS_ERR_ARG, name
         assert call(C, **{name: FAKE + 4}) == C.KVS_ERR_ALIGN, name
+
+
+def test_tree_refusals(C):
+    dm = C.dims(1, 4, 2, 128)
+    assert tree(C, N=-1) == C.KVS_ERR_ARG and tree(C, w=-1) == C.KVS_ERR_ARG
+    for md in (0, -1, 257):
+        assert tree(C, md=md) == C.KVS_ERR_UNSUPPORTED
+    assert tree(C, up=FAKE + 4) == C.KVS_ERR_ALIGN and tree(C, lse=FAKE + 8) == C.KVS_ERR_ALIGN
+    assert tree(C, mp=1 << 27) == C.KVS_ERR_UNSUPPORTED
+    for d in (64, 128):
+        need = C.kvs_attn_tree_workspace_size(C.dims(1, 4, 2, d), 2, 6)
+        assert need > 0 and tree(C, C.dims(1, 4, 2, d), wsb=need - 1) == C.KVS_ERR_CAPACITY
+    assert C.kvs_attn_tree_workspace_size(dm, 0, 6) == C.kvs_attn_tree_workspace_size(dm, 2, 0) == 0
+    assert tree(C, B=0, tok=None, q=None, bt=None, sl=None, o=None, ws=None) == C.KVS_OK
+    assert tree(C, N=0, tok=None, q=None, bt=None, sl=None, o=None, ws=None) == C.KVS_OK
 
 
 def test_accept_refusals(C):
@@ -90,6 +113,12 @@ def test_binding_checks_types_and_sizes(C):
     """What the compiled binding refuses before the library sees it."""
     dm = C.dims(1, 2, 1, 64)
     meta = lambda *s, dtype=torch.int32: torch.zeros(*s, dtype=dtype, device="meta")  # noqa: E731
+    with pytest.raises(ValueError, match="parent must hold at least 6 elements of torch.int32, got 6 of torch.int64"):
+        C.kvs_attn_tree(dm, 2, 6, 8, FAKE, meta(6, dtype=torch.int64), FAKE, 16, FAKE, FAKE, 8, FAKE, 4, FAKE, 0,
+                        None, None, None, FAKE, None, FAKE, 1 << 30, stream=0)
+    with pytest.raises(ValueError, match="o must hold at least 768 elements of torch.bfloat16"):
+        C.kvs_attn_tree(dm, 2, 6, 8, FAKE, None, FAKE, 16, FAKE, FAKE, 8, FAKE, 4, FAKE, 0, None, None, None,
+                        meta(767, dtype=torch.bfloat16), None, FAKE, 1 << 30, stream=0)
     with pytest.raises(ValueError, match="accept must hold at least 6 elements of torch.int32"):
         C.kvs_accept_paged(dm, 2, 6, FAKE, FAKE, meta(5), 16, FAKE, FAKE, 8, FAKE, 4, FAKE, FAKE, stream=0)
     with pytest.raises(ValueError, match="n_accept must hold .* torch.int64"):
