@@ -17,8 +17,11 @@
 //               swizzled layout that the tensor core reads; pages may be of any size and end
 //               anywhere in a tile, which a TMA box could not
 //   warps 4-11  softmax, two threads per query row: S from TMEM, p = 2^(x - m), P as bf16 to TMEM
-//   warp 12     issues S = Q K^T (Q in TMEM) and O += P V (P in TMEM), M = 128 each
-// The registers of a block go to the softmax (setmaxnreg: 200 a thread, 56 for the others).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax of the
+//   warps 12, 14  issue S = Q K^T (Q in TMEM) and O += P V (P in TMEM), M = 128 each; one warp for
+//               both spent its time issuing (1.2 us a tile)
+//   warp 13     brings the page ids of the tiles to come, six tiles ahead (under a saturated HBM a
+//               load takes longer than a tile)
+// The registers of a block go to the softmax (setmaxnreg: 192 a thread, 80 for the copies, 48 for the rest).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax of the
 // one before.  O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // Which drafted tokens a token sees is a row of 256 bits, closed over the parents in log2(depth)
@@ -46,22 +49,23 @@ constexpr int BM = 128;        // query rows of a tile = TMEM lanes
 constexpr int BN = 128;        // keys of a tile
 constexpr int kStages = 3;     // of the K ring and of the V ring
 constexpr int kCopyWarps = 4;  // 32 keys of a tile each
-constexpr int kSoftWarp = 4, kMmaWarp = 12;
+constexpr int kSoftWarp = 4, kScoreWarp = 12, kFindWarp = 13, kValueWarp = 14;
 constexpr int kSoftThreads = 256;
-constexpr int kThreads = 16 * 32;  // three warps of the last four only share its registers
+constexpr int kThreads = 16 * 32;  // the last warp only makes up the four
 constexpr int kWarps = kThreads / 32;
 constexpr int KC = BN / 2;     // keys of a softmax thread and tile
-constexpr int kLag = 3;        // copies (of half a stage) issued before one is waited for
+constexpr int kAhead = 8;      // tiles whose page ids are on their way or not yet used
 constexpr uint32_t kBox = 128 * 128;  // 128 rows x 64 bf16 (one 128-byte swizzle span)
 constexpr uint32_t kTmemCols = 512;
-constexpr int kCopyRegs = 56, kSoftRegs = 200, kMmaRegs = 56;
+constexpr int kCopyRegs = 80, kSoftRegs = 192, kMmaRegs = 48;
 static_assert(kCopyRegs + 2 * kSoftRegs + kMmaRegs <= 65536 / 128, "what the launch has");
 constexpr float kRescale = 8.f;  // log2 growth of the row max that forces a rescale of O
 constexpr int kMaxBlocks = 160;  // of the persistent grid; sizes the workspace
 constexpr int kWords = kMaxDraft / 32;
 constexpr long long kL2Bytes = 129ll << 20;
 constexpr int kJoinThreads = 256;
-constexpr int kDirty = 8;        // units whose mark for non-finite drafts is kept
+constexpr int kUnits = 8;        // units that are known ahead
+constexpr int kDirty = 2 * kUnits;  // units whose mark for non-finite drafts is kept
 // Tiles whose bits of keys that are there are kept: a copy of tile i + 6 waits for the S product
 // of i + 3, and that for the softmax of i + 1.
 constexpr int kLive = 8;
@@ -77,14 +81,15 @@ struct Cfg {
   static constexpr uint32_t OFF_SEES = OFF_XL + 2 * BM * 4;      // [kMaxDraft][kWords]
   static constexpr uint32_t OFF_UP = OFF_SEES + kMaxDraft * kWords * 4;  // [kMaxDraft]
   static constexpr uint32_t OFF_BAR = OFF_UP + kMaxDraft * 4;
-  // q, k_full[3], k_empty[3], v_full[3], v_empty[3], s_full[2], s_empty[2], p[2], o[2], done
-  static constexpr uint32_t NBAR = 22;
+  // q, k_full[3], k_empty[3], v_full[3], v_empty[3], s_full[2], s_empty[2], p[2], o[2], done,
+  // ids_full[8], ids_empty[8], unit_full[8], unit_empty[8]
+  static constexpr uint32_t NBAR = 22 + 2 * kAhead + 2 * kUnits;
   static constexpr uint32_t USED = OFF_BAR + NBAR * 8;
   static constexpr uint32_t SMEM = USED + 1024;
   // TMEM columns: S buffers, then P (bf16 pairs of one tile), Q (bf16 pairs), O
   static constexpr uint32_t COL_P = 2 * BN, COL_Q = COL_P + BN / 2, COL_O = COL_Q + D / 2;
   static_assert(COL_O + D <= kTmemCols, "TMEM plan");
-  static_assert(SMEM + 2048 <= kMaxSmem, "shared-memory plan");
+  static_assert(SMEM + 6144 <= kMaxSmem, "shared-memory plan");
 };
 
 // A partial result: O transposed in chunks of four columns [D / 4][BM], then the reference and
@@ -104,7 +109,7 @@ __device__ __forceinline__ float* block_part(void* ws, int block, int side, int 
 __device__ __forceinline__ void fault() { atomicCAS(&g_attn_tree_error, 0, kErrAttnTree); }
 
 // What a row holds: paged keys, all keys with the ring's, its sequence's first token and their
-// number (0 where the token starts are bad).
+// number (negative where the token starts are bad).
 struct Row {
   int paged, all, t0, m;
   __device__ __forceinline__ int tiles() const { return (all + BN - 1) / BN; }
@@ -115,91 +120,78 @@ __device__ __forceinline__ Row row_of(const AttnTreeArgs& a, int r) {
   const int b = r % a.B, t0 = a.tok_start[b], t1 = a.tok_start[b + 1];
   const int paged = max(0, min(a.seq_lens[r], a.max_pages * a.page_size));
   const bool good = t0 >= 0 && t1 >= t0 && t1 <= a.N && t1 - t0 <= a.max_draft;
-  return {paged, paged + (a.w > 0 ? max(0, min(a.pos[b], a.w)) : 0), t0, good ? t1 - t0 : 0};
+  return {paged, paged + (a.w > 0 ? max(0, min(a.pos[b], a.w)) : 0), t0, good ? t1 - t0 : -1};
 }
 
-__device__ __forceinline__ int query_tiles(int m, int g) { return (m * g + BM - 1) / BM; }
+__device__ __forceinline__ int query_tiles(int m, int g) { return (max(m, 0) * g + BM - 1) / BM; }
 
-// Segment of a (row, query tile) in a block's share.
+// Segment of a (row, query tile) in a block's share; none behind the last.
 struct Unit {
   int row, mt, ta, tb;  // key tiles ta .. tb - 1
   Row is;
+  __device__ __forceinline__ bool none() const { return ta == tb; }
   __device__ __forceinline__ bool whole() const { return ta == 0 && tb == is.tiles(); }
 };
 
-// Walks through the units of a share, every warp for itself: the lanes hold 32 rows.
+// Walks through the units of a share: the lanes of one warp hold 32 rows.
 struct Walk {
-  const AttnTreeArgs& a;
-  int rows, g, lane, base, left;
+  int base, left;
   Row mine;
   Unit u;
 
-  __device__ __forceinline__ void fetch() {
-    mine = {0, 0, 0, 0};
-    if (base + lane < rows) mine = row_of(a, base + lane);
-  }
-  __device__ __forceinline__ void enter(int r) {
-    u.row = r;
-    u.is.paged = __shfl_sync(0xffffffffu, mine.paged, r - base);
-    u.is.all = __shfl_sync(0xffffffffu, mine.all, r - base);
-    u.is.t0 = __shfl_sync(0xffffffffu, mine.t0, r - base);
-    u.is.m = __shfl_sync(0xffffffffu, mine.m, r - base);
-  }
   __device__ __forceinline__ void cut() {
     u.tb = min(u.is.tiles(), u.ta + left);
     left -= u.tb - u.ta;
   }
-  __device__ __forceinline__ Walk(const AttnTreeArgs& args, int rows_, int g_, int row, int mt,
-                                  int ta, int tiles)
-      : a(args), rows(rows_), g(g_), lane(threadIdx.x & 31), base(row & ~31), left(tiles) {
-    fetch();
-    enter(row);
-    u.mt = mt;
-    u.ta = ta;
-    cut();
-  }
-  __device__ __forceinline__ bool next() {
+  // the next unit; from a row that is not there (base = row | 31) the first one behind it
+  __device__ __forceinline__ bool next(const AttnTreeArgs& a, int rows, int g, int lane) {
     if (left <= 0) return false;
-    u.ta = 0;
     if (u.mt + 1 < query_tiles(u.is.m, g)) {
       ++u.mt;
-      cut();
-      return true;
-    }
-    u.mt = 0;
-    int from = u.row - base + 1;
-    for (;;) {
-      const uint32_t some = __ballot_sync(0xffffffffu, mine.all > 0 && mine.m > 0) &
-                            (from < 32 ? 0xffffffffu << from : 0u);
-      if (some) {
-        enter(base + __ffs(some) - 1);
-        cut();
-        return true;
+    } else {
+      u.mt = 0;
+      int from = u.row - base + 1;
+      for (;;) {
+        if (from >= 32) {
+          base += from;
+          from = 0;
+          if (base >= rows) return false;  // only if lengths change under the call
+          mine = {0, 0, 0, 0};
+          if (base + lane < rows) mine = row_of(a, base + lane);
+        }
+        const uint32_t some = __ballot_sync(0xffffffffu, mine.all > 0 && mine.m > 0) & 0xffffffffu << from;
+        if (some) {
+          const int r = __ffs(some) - 1;
+          u.row = base + r;
+          u.is.paged = __shfl_sync(0xffffffffu, mine.paged, r);
+          u.is.all = __shfl_sync(0xffffffffu, mine.all, r);
+          u.is.t0 = __shfl_sync(0xffffffffu, mine.t0, r);
+          u.is.m = __shfl_sync(0xffffffffu, mine.m, r);
+          break;
+        }
+        from = 32;
       }
-      base += 32;
-      from = 0;
-      if (base >= rows) return false;  // only if lengths change under the call
-      fetch();
     }
+    u.ta = 0;
+    cut();
+    return true;
   }
 };
 
-// Equal contiguous shares of `blocks` blocks of a stream of tiles; the first `more` have one more
-// than `each`.
+// Equal contiguous shares of `blocks` blocks of a stream of fewer than 2^31 tiles; the first
+// `more` have one more than `each`.
 struct Shares {
-  long long each = 1, more = 0;
-  __device__ __forceinline__ Shares(long long total, int blocks) {
+  int each = 1, more = 0;
+  __device__ __forceinline__ Shares(int total, int blocks) {
     if (total > blocks) {
       each = total / blocks;
       more = total - each * blocks;
     }
   }
-  __device__ __forceinline__ long long first(int block) const {
-    return block * each + min((long long)block, more);
-  }
-  __device__ __forceinline__ int of(long long tile) const {  // block of a tile
-    const long long wide = more * (each + 1);
-    return (int)(tile < wide ? tile / (each + 1) : more + (tile - wide) / each);
+  __device__ __forceinline__ int first(int block) const { return block * each + min(block, more); }
+  __device__ __forceinline__ int of(int tile) const {  // block of a tile
+    const int wide = more * (each + 1);
+    return tile < wide ? tile / (each + 1) : more + (tile - wide) / each;
   }
 };
 
@@ -219,28 +211,45 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
 
 __device__ __forceinline__ void named_sync(int id, int nthreads) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
-// Registers a thread from here on; all warps of four call it.
+// Registers a thread from here on; all warps of four call it.  (As the other .aligned instructions
+// here it wants its warp together, which a branch before it does not promise.)
 template <int N>
 __device__ __forceinline__ void give_registers() {
+  __syncwarp();
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 template <int N>
 __device__ __forceinline__ void take_registers() {
+  __syncwarp();
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// 16-byte async copy global -> shared; keys and values that the call reads once are the first to
+// leave L2, so that what is read again stays.
 __device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-__device__ __forceinline__ void cp_async16_once(uint32_t dst, const void* src, int src_bytes,
-                                                uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n" ::"r"(dst),
-               "l"(src), "r"(src_bytes), "l"(policy));
+template <bool kOnce>
+__device__ __forceinline__ void cp_async16_whole(uint32_t dst, const void* src, uint64_t policy) {
+  if constexpr (kOnce)
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n" ::"r"(dst),
+                 "l"(src), "l"(policy));
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src));
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src));
+}
+
+// An arrival on `bar` when all copies that this thread has started have landed.
+__device__ __forceinline__ void arrive_when_landed(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.f : m; }
@@ -249,65 +258,86 @@ __device__ __forceinline__ float lse_of(float ref, float sum) {
   return sum == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
 }
 
-// A warp's copies of its 32 keys of a tile.  Lane i finds where key i lies.
-template <int D>
+// What the copies of a tile need to know of it.
+struct TileAt {
+  int row, key0, paged, all, first, m, unit, pad;
+};
+
+// A warp's copies of its 32 keys of a tile: D / 8 lanes a row, each group of lanes a run of rows,
+// so that a lane finds the places of its rows by itself.
+template <int D, bool kOnce>
 struct Copies {
+  static constexpr int kLanes = D / 8, kRows = kLanes;  // lanes of a row; rows of a group of lanes
   const AttnTreeArgs& a;
   const int warp, lane, ps_shift;
   const uint64_t policy;
-  int page = -1, inside = 0, key = 0;      // of the tile looked up
-  const bf16_t *k = nullptr, *v = nullptr; // of the tile being copied; null: zeros
 
-  __device__ __forceinline__ void look_up(const Unit& u, int t) {
-    key = t * BN + warp * 32 + lane;
-    page = -1;
-    if (key < u.is.paged) {
-      const int idx = ps_shift >= 0 ? key >> ps_shift : key / a.page_size;
-      inside = key - idx * a.page_size;
-      page = a.block_table[(size_t)u.row * a.max_pages + idx];
-    }
+  __device__ __forceinline__ int page_index(int key) const {
+    return ps_shift >= 0 ? key >> ps_shift : key / a.page_size;
   }
-  __device__ __forceinline__ void resolve(const Unit& u) {
-    k = v = nullptr;
-    if (key < u.is.paged) {
-      if ((uint32_t)page < (uint32_t)a.capacity) {
-        const size_t at = ((size_t)page * a.page_size + inside) * D;
-        k = a.k_pages + at;
-        v = a.v_pages + at;
-      } else {
-        fault();
-      }
-    } else if (key < u.is.all) {
-      const size_t at = ((size_t)u.row * a.w + (key - u.is.paged)) * D;
-      k = a.ring_k + at;
-      v = a.ring_v + at;
-    }
+  // whether key `lane` of the warp's is there
+  __device__ __forceinline__ bool there(const TileAt& at, const int* ids) const {
+    const int key = at.key0 + warp * 32 + lane;
+    if (key >= at.paged) return key < at.all;
+    const bool good = (uint32_t)ids[warp * 32 + lane] < (uint32_t)a.capacity;
+    if (!good) fault();
+    return good;
   }
-  static constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a step
-  // where this lane's chunk of a step goes in a tile
-  __device__ __forceinline__ uint32_t place(int step) const {
-    const int c = lane % kLanes, row = warp * 32 + step * kRows + lane / kLanes;
-    return (uint32_t)(c >> 3) * kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-  }
-  __device__ __forceinline__ void copy(const bf16_t* from, uint32_t tile) const {
+  // row of the tile of this lane's i-th copy, and where the copy goes
+  __device__ __forceinline__ int row(int i) const { return warp * 32 + lane / kLanes * kRows + i; }
+  __device__ __forceinline__ uint32_t place(int i) const {
     const int c = lane % kLanes;
+    return (uint32_t)(c >> 3) * kBox + row(i) * 128 + (((c & 7) ^ (row(i) & 7)) << 4);
+  }
+  // All 32 keys are in pages that are there.  A lone warp issues an instruction every few cycles, so
+  // the copies have to be most of them: where a lane's rows lie in one page there is one address.
+  __device__ __forceinline__ void copy_paged(const TileAt& at, const int* ids, const bf16_t* pages,
+                                             uint32_t tile) const {
+    const int key0 = at.key0 + row(0);
+    const int idx = page_index(key0);
+    int inside = key0 - idx * a.page_size;
+    const bf16_t* from = pages + lane % kLanes * 8;
+    if (a.page_size % kRows == 0) {
+      from += ((size_t)ids[row(0)] * a.page_size + inside) * D;
 #pragma unroll
-    for (int i = 0; i < 32 / kRows; ++i) {
-      const bf16_t* src = reinterpret_cast<const bf16_t*>(__shfl_sync(
-          0xffffffffu, reinterpret_cast<unsigned long long>(from), i * kRows + lane / kLanes));
-      const int bytes = src ? 16 : 0;
-      src = src ? src + c * 8 : a.q;
-      if (a.read_once) cp_async16_once(tile + place(i), src, bytes, policy);
-      else cp_async16(tile + place(i), src, bytes);
+      for (int i = 0; i < kRows; ++i) cp_async16_whole<kOnce>(tile + place(i), from + i * D, policy);
+      return;
     }
+#pragma unroll 4
+    for (int i = 0; i < kRows; ++i) {
+      const bf16_t* src = from + ((size_t)ids[row(i)] * a.page_size + inside) * D;
+      cp_async16_whole<kOnce>(tile + place(i), src, policy);
+      if (++inside == a.page_size) inside = 0;
+    }
+  }
+  // Any keys: in pages, in the ring, or not there.
+  __device__ __forceinline__ void copy_any(const TileAt& at, const int* ids, const bf16_t* pages,
+                                           const bf16_t* ring, uint32_t tile) const {
+    const int c = lane % kLanes;
+#pragma unroll 1
+    for (int i = 0; i < kRows; ++i) {
+      const int key = at.key0 + row(i), page = ids[row(i)];
+      const bool paged = key < at.paged;
+      const bool ok = paged ? (uint32_t)page < (uint32_t)a.capacity : key < at.all;
+      const long long r = paged ? (long long)page * a.page_size + (key - page_index(key) * a.page_size)
+                                : (long long)at.row * a.w + (key - at.paged);
+      const bf16_t* src = ok ? (paged ? pages : ring) + (r * D + c * 8) : a.q;
+      cp_async16(tile + place(i), src, ok ? 16 : 0);
+    }
+  }
+  __device__ __forceinline__ void copy(bool whole, const TileAt& at, const int* ids,
+                                       const bf16_t* pages, const bf16_t* ring, uint32_t tile) const {
+    if (whole) copy_paged(at, ids, pages, tile);
+    else copy_any(at, ids, pages, ring, tile);
+    __syncwarp();
   }
   // Drafted rows lo .. hi - 1 of this warp's 32 of a V tile that has landed: what is not finite
   // becomes 0; true if there was any.  A lane looks at the chunks that it copied.
   __device__ __forceinline__ bool clean(uint8_t* tile, int lo, int hi) const {
     bool any = false;
-    for (int i = 0; i < 32 / kRows; ++i) {
-      const int row = i * kRows + lane / kLanes;
-      if (row < lo || row >= hi) continue;
+    for (int i = 0; i < kRows; ++i) {
+      const int r = row(i) - warp * 32;
+      if (r < lo || r >= hi) continue;
       uint32_t* x = reinterpret_cast<uint32_t*>(tile + place(i));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -324,15 +354,33 @@ struct Copies {
   }
 };
 
-template <int D>
+// The rest of a wait that does not end at once; false if it runs out, or another's in the block.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  const uint64_t t0 = tc::globaltimer();
+  for (;;) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (tc::globaltimer() - t0 > tc::kWaitLimitNs) {
+      *abort_flag = 1u;
+      atomicCAS(&g_attn_tree_error, 0, kErrWaitTimeout);
+      return false;
+    }
+  }
+}
+
+// The code is kept small: at 120 KB (a walk through the rows in every warp, a copy loop per case)
+// the warps waited for instructions a third of the time, 1.4 us a tile.
+template <int D, bool kOnce>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
     const __grid_constant__ AttnTreeArgs a, int rows, int ps_shift) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long warp_tiles[kWarps];
-  __shared__ int start_s[3];                 // row, query tile and key tile of the share's first
+  __shared__ int warp_tiles[kWarps];
+  __shared__ int start_s[1];                 // tiles of all rows
   __shared__ uint32_t misc[2];               // TMEM address, abort flag
-  __shared__ int clean_s[kCopyWarps][kStages][2];  // rows of a stage's V that are drafted
+  __shared__ __align__(16) TileAt at_s[kAhead];
+  __shared__ __align__(16) Unit unit_s[kUnits];
+  __shared__ __align__(16) int ids_s[kAhead][BN];          // page ids of a tile's keys
   __shared__ volatile uint32_t live_s[kLive][kCopyWarps];  // keys of a tile that are there
   __shared__ volatile int dirty_s[kDirty];   // n + 1: unit n has drafted values that are not finite
   const uint32_t raw = smem_u32(smem_raw);
@@ -357,6 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
   auto bar_p = [&](int i) { return bar0 + 8u * (17 + (i & 1)); };
   auto bar_o = [&](int i) { return bar0 + 8u * (19 + (i & 1)); };
   const uint32_t bar_done = bar0 + 8u * 21;
+  auto bar_ids = [&](int s) { return bar0 + 8u * (22 + s); };
+  auto bar_idsfree = [&](int s) { return bar0 + 8u * (22 + kAhead + s); };
+  auto bar_unit = [&](int n) { return bar0 + 8u * (22 + 2 * kAhead + n % kUnits); };
+  auto bar_unitfree = [&](int n) { return bar0 + 8u * (22 + 2 * kAhead + kUnits + n % kUnits); };
   volatile uint32_t* abort_flag = misc + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.Hq / a.Hkv;
@@ -364,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
   if (tid == 0) {
     tc::mbar_init(bar_q, kSoftThreads);
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(bar_kfull(s), kCopyWarps);
+      tc::mbar_init(bar_kfull(s), kCopyWarps * 33);  // every thread's copies, and each warp's word
       tc::mbar_init(bar_kempty(s), 1);
-      tc::mbar_init(bar_vfull(s), kCopyWarps);
+      tc::mbar_init(bar_vfull(s), kCopyWarps * 32);
       tc::mbar_init(bar_vempty(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -375,65 +427,77 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       tc::mbar_init(bar_p(s), kSoftThreads);
       tc::mbar_init(bar_o(s), 1);
     }
-    tc::mbar_init(bar_done, 1);
+    tc::mbar_init(bar_done, 2);
+    for (int s = 0; s < kAhead; ++s) {
+      tc::mbar_init(bar_ids(s), 1);
+      tc::mbar_init(bar_idsfree(s), kCopyWarps);
+    }
+    for (int s = 0; s < kUnits; ++s) {
+      tc::mbar_init(bar_unit(s), 1);
+      tc::mbar_init(bar_unitfree(s), kSoftThreads / 32 + 2);
+    }
     misc[1] = 0u;
     tc::fence_mbar_init();
   }
   if (tid < kDirty) dirty_s[tid] = 0;
-  if (tid < 3) start_s[tid] = 0;  // stays only if lengths change under the call
   // started beside the end of the kernel before; the join must not start beside that one too
   wait_for_previous();
   let_next_start();
 
-  // --- tiles of all rows: every thread a contiguous range of them
+  // --- tiles of all rows, every thread a contiguous range of them; in a second pass the row, query
+  // tile and key tile where the share begins
   const int per = (rows + kThreads - 1) / kThreads;
   const int r0 = min(tid * per, rows), r1 = min(r0 + per, rows);
-  long long mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    const Row x = row_of(a, r);
-    mine += x.m > 0 ? (long long)x.tiles() * query_tiles(x.m, g) : 0;
-    if (blockIdx.x == 0) {
-      const int b = r % a.B, m = a.tok_start[b + 1] - a.tok_start[b];
-      if (a.seq_lens[r] != x.paged || m != x.m || x.paged < x.m) fault();
-    }
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_tiles[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += warp_tiles[w];
-    total += warp_tiles[w];
-  }
-  const Shares shares(total, gridDim.x);
   Ends* ends = static_cast<Ends*>(a.ws);
-  if (blockIdx.x >= total) {
-    if (tid == 0) ends[blockIdx.x] = {-1, 0, 0, 0};
-    return;
-  }
-  const long long s0 = shares.first(blockIdx.x);
-  const int tiles = (int)(min(shares.first(blockIdx.x + 1), total) - s0);
-  if (before <= s0 && s0 < before + mine) {
-    long long at = s0 - before;
-    for (int r = r0; r < r1; ++r) {
-      const Row x = row_of(a, r);
-      const long long n = x.m > 0 ? (long long)x.tiles() * query_tiles(x.m, g) : 0;
-      if (at < n) {
-        start_s[0] = r;
-        start_s[1] = (int)(at / x.tiles());
-        start_s[2] = (int)(at - (long long)start_s[1] * x.tiles());
-        break;
+  int mine = 0, before = 0, s0 = -1, tiles = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 0 || (before <= s0 && s0 < before + mine)) {
+      int at = s0 - before;
+#pragma unroll 1
+      for (int r = r0; r < r1; ++r) {
+        const Row x = row_of(a, r);
+        const int nt = x.tiles(), n = nt * query_tiles(x.m, g);  // 0 without drafted tokens
+        if (pass == 0) {
+          mine += n;
+          if (blockIdx.x == 0 && (a.seq_lens[r] != x.paged || x.paged < x.m || x.m < 0)) fault();
+        } else if (at < n) {
+          const int mt = at / nt, ta = at - mt * nt;
+          Unit u = {r, mt, ta, min(nt, ta + tiles), x};
+          unit_s[0] = u;
+          Ends e = {-1, 0, 0, 0};
+          if (ta > 0 && u.tb == nt) e = {r, mt, Shares(start_s[0], gridDim.x).of(s0 - ta), 0};
+          ends[blockIdx.x] = e;
+          break;
+        } else {
+          at -= n;
+        }
       }
-      at -= n;
     }
+    if (pass) break;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_tiles[warp] = incl;
+    if (tid == 0) unit_s[0] = {0, 0, 0, 0, {0, 0, 0, 0}};  // stays only if lengths change under the call
+    __syncthreads();
+    const int theirs = lane < kWarps ? warp_tiles[lane] : 0;  // every warp for itself
+    const int total = __reduce_add_sync(0xffffffffu, theirs);
+    before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0);
+    if ((int)blockIdx.x >= total) {
+      if (tid == 0) ends[blockIdx.x] = {-1, 0, 0, 0};
+      return;
+    }
+    const Shares shares(total, gridDim.x);
+    s0 = shares.first(blockIdx.x);
+    tiles = min(shares.first(blockIdx.x + 1), total) - s0;
+    start_s[0] = total;  // the same by all
   }
-  if (warp == kMmaWarp) {
+  __syncwarp();
+  if (warp == kScoreWarp) {
     tc::tmem_alloc(smem_u32(misc), kTmemCols);
     tc::tmem_relinquish();
   }
@@ -441,156 +505,186 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
   tc::fence_after_sync();
   const uint32_t tmem = misc[0];
   const uint32_t t_p = tmem + C::COL_P, t_q = tmem + C::COL_Q, t_o = tmem + C::COL_O;
-  if (tid == 0) {
-    Ends e = {-1, 0, 0, 0};
-    const int nt = row_of(a, start_s[0]).tiles();
-    if (start_s[2] > 0 && start_s[2] + tiles >= nt)
-      e = {start_s[0], start_s[1], shares.of(s0 - start_s[2]), 0};
-    ends[blockIdx.x] = e;
-  }
-  // A wait that has run out, here or elsewhere in the block: from then on a warp only goes
-  // through the motions (arrivals and named barriers, no waits, no TMEM), so that none is left
-  // waiting for it.  The same in all lanes.
+  // One thread's wait; false if it has run out, or another's in the block.
+  auto wait_alone = [&](uint32_t bar, uint32_t parity) -> bool {
+    return tc::mbar_try_wait(bar, parity) || wait_on(bar, parity, abort_flag);
+  };
+  // A warp's.  Once one has run out, a warp only goes through the motions (arrivals and named
+  // barriers, no waits, no TMEM), so that none is left waiting for it.  The same in all lanes.
   bool dead = false;
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (dead) return;
-    bool ok = tc::mbar_wait(bar, parity);
-    if (!ok) {
-      *abort_flag = 1u;
-      atomicCAS(&g_attn_tree_error, 0, kErrWaitTimeout);
-    }
-    ok = ok && !*abort_flag;
-    dead = !__all_sync(0xffffffffu, ok);
+    if (!dead) dead = !__all_sync(0xffffffffu, wait_alone(bar, parity));
   };
 
   if (warp < kCopyWarps) {
     // ============================================================ copies of K and V
     give_registers<kCopyRegs>();
-    Walk walk(a, rows, g, start_s[0], start_s[1], start_s[2], tiles);
-    Copies<D> copies{a, warp, lane, ps_shift, read_once_policy()};
-    int unit = 0, t = walk.u.ta;
-    // copy 2 i is K of tile i of the share, copy 2 i + 1 its V; one is announced when it has
-    // landed, kLag copies later
-    auto announce = [&](int c) {
-      const int i = c >> 1, s = i % kStages;
-      if (c & 1) {
-        const int lo = clean_s[warp][s][0], hi = clean_s[warp][s][1];
-        // the unit's number is kept beside the first row
-        if ((lo & 63) < hi && copies.clean(smem + C::OFF_V + s * C::TILE, lo & 63, hi))
-          dirty_s[(lo >> 6) % kDirty] = (lo >> 6) + 1;
-      }
+    Copies<D, kOnce> copies{a, warp, lane, ps_shift, read_once_policy()};
+    // A stage is announced by its copies as they land; the issuer of the products makes them visible
+    // to the tensor core.  V of a tile with drafted rows is searched first, when the next tile's
+    // copies are on their way.
+    int held = -1, held_unit = 0, held_lo = 0, held_hi = 0;  // such a tile
+    auto release = [&] {
+      const int s = held % kStages;
+      if (copies.clean(smem + C::OFF_V + s * C::TILE, held_lo, held_hi))
+        dirty_s[held_unit % kDirty] = held_unit + 1;
       tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive((c & 1) ? bar_vfull(s) : bar_kfull(s));
+      tc::mbar_arrive(bar_vfull(s));
+      held = -1;
     };
-    copies.look_up(walk.u, t);
-    int i = 0;
-    for (; i < tiles && !dead; ++i) {
-      copies.resolve(walk.u);
+    for (int i = 0; i < tiles && !dead; ++i) {
+      wait(bar_ids(i % kAhead), (uint32_t)(i / kAhead) & 1u);
+      if (dead) break;
+      const TileAt at = at_s[i % kAhead];
+      const int* ids = ids_s[i % kAhead];
+      const uint32_t there = __ballot_sync(0xffffffffu, copies.there(at, ids));
+      const bool whole = !~there && at.key0 + warp * 32 + 32 <= at.paged;
       const int s = i % kStages;
-      const uint32_t empty = (uint32_t)(i / kStages & 1) ^ 1u;
-      // the tile's drafted rows among this warp's
-      const int k0 = t * BN + warp * 32;
-      const int lo = max(0, min(32, walk.u.is.first() - k0)), hi = max(0, min(32, walk.u.is.paged - k0));
-      const int mark = unit << 6 | lo, end = walk.u.is.m > 1 && lo < hi ? hi : -1;
-      // where the next tile's keys lie, a tile early
-      if (i + 1 < tiles) {
-        if (++t == walk.u.tb) {
-          walk.next();
-          t = walk.u.ta;
-          ++unit;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        wait(kv ? bar_vempty(s) : bar_kempty(s), (uint32_t)(i / kStages & 1) ^ 1u);
+        if (dead) break;
+        copies.copy(whole, at, ids, kv ? a.v_pages : a.k_pages, kv ? a.ring_v : a.ring_k,
+                    (kv ? sV : sK) + s * C::TILE);
+        cp_async_commit();
+        if (kv == 0) {
+          if (lane == 0) {
+            live_s[i % kLive][warp] = there;
+            tc::mbar_arrive(bar_kfull(s));
+          }
+          arrive_when_landed(bar_kfull(s));
         }
-        copies.look_up(walk.u, t);
       }
-      const uint32_t there = __ballot_sync(0xffffffffu, copies.k != nullptr);
-      wait(bar_kempty(s), empty);
       if (dead) break;
-      if (lane == 0) live_s[i % kLive][warp] = there;
-      copies.copy(copies.k, sK + s * C::TILE);
-      cp_async_commit();
-      cp_async_wait<kLag>();
-      if (2 * i >= kLag) announce(2 * i - kLag);
-      wait(bar_vempty(s), empty);
-      if (dead) break;
-      if (lane == 0) {
-        clean_s[warp][s][0] = mark;
-        clean_s[warp][s][1] = end < 0 ? 0 : end;
+      if (lane == 0) tc::mbar_arrive(bar_idsfree(i % kAhead));
+      const int k0 = at.key0 + warp * 32;
+      const int lo = max(0, min(32, at.first - k0)), hi = at.m > 1 ? max(0, min(32, at.paged - k0)) : 0;
+      if (held >= 0) {
+        cp_async_wait<2>();
+        release();
       }
-      copies.copy(copies.v, sV + s * C::TILE);
-      cp_async_commit();
-      cp_async_wait<kLag>();
-      if (2 * i + 1 >= kLag) announce(2 * i + 1 - kLag);
+      if (lo < hi) {
+        held = i;
+        held_unit = at.unit;
+        held_lo = lo;
+        held_hi = hi;
+      } else {
+        arrive_when_landed(bar_vfull(s));
+      }
     }
     cp_async_wait<0>();
-    if (!dead)
-      for (int c = max(0, 2 * tiles - kLag); c < 2 * tiles; ++c) announce(c);
-  } else if (warp >= kMmaWarp) {
-    // ============================================================ MMA issuer
+    if (held >= 0 && !dead) release();
+  } else if (warp >= kScoreWarp) {
+    // ============================================================ products, page ids
     give_registers<kMmaRegs>();
-    if (warp == kMmaWarp) {
-      Walk walk(a, rows, g, start_s[0], start_s[1], start_s[2], tiles);
-      constexpr uint32_t idesc_s = tc::idesc_bf16(BM, BN);
-      constexpr uint32_t idesc_o = tc::idesc_bf16_bmn(BM, D);
-      int gs = 0, gp = 0;  // S and P V products issued (all units)
-      int n = 0;
-      do {
-        const int count = walk.u.tb - walk.u.ta;
-        // the unit's query rows are in TMEM, and the softmax threads have read the previous
-        // unit's O (they arrive after both), so P V(0) may overwrite it
-        wait(bar_q, (uint32_t)n & 1u);
-        ++n;
-        for (int j = 0; j <= count && !dead; ++j) {
-          if (j < count) {  // S = Q K^T into S buffer gs & 1
-            const int s = gs % kStages, sbuf = gs & 1;
-            wait(bar_kfull(s), (uint32_t)(gs / kStages) & 1u);
-            wait(bar_sempty(sbuf), ((uint32_t)(gs >> 1) & 1u) ^ 1u);
-            if (dead) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-              const uint32_t k_s = sK + s * C::TILE;
-  #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t o = (uint32_t)(k >> 2) * kBox + (uint32_t)(k & 3) * 32u;
-                tc::mma_bf16_ts(tmem + (uint32_t)(sbuf * BN), t_q + 8u * k, tc::sdesc_sw128(k_s + o),
-                                idesc_s, k > 0 ? 1u : 0u);
-              }
-              tc::commit(bar_sfull(sbuf));
-              tc::commit(bar_kempty(s));
-            }
-            __syncwarp();
-            ++gs;
-          }
-          if (j >= 1) {  // O += P V of the unit's tile j - 1
-            const int s = gp % kStages;
-            wait(bar_p(gp), (uint32_t)(gp >> 1) & 1u);
-            wait(bar_vfull(s), (uint32_t)(gp / kStages) & 1u);
-            if (dead) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-              const uint32_t v_s = sV + s * C::TILE;
-  #pragma unroll
-              for (int k = 0; k < BN / 16; ++k)
-                tc::mma_bf16_ts(t_o, t_p + 8u * k, tc::sdesc_sw128_mn(v_s + 2048u * k, kBox), idesc_o,
-                                (j > 1 || k > 0) ? 1u : 0u);
-              tc::commit(bar_vempty(s));
-              tc::commit(bar_o(gp));
-            }
-            __syncwarp();
-            ++gp;
-          }
+    if (warp == kScoreWarp) {
+      // S = Q K^T of a tile into S buffer tile & 1; one lane issues and waits
+      constexpr uint32_t idesc = tc::idesc_bf16(BM, BN);
+      int i = 0;
+      bool ok = lane == 0;
+      for (int n = 0; ok && (ok = wait_alone(bar_unit(n), (uint32_t)(n / kUnits) & 1u)); ++n) {
+        const int end = i + unit_s[n % kUnits].tb - unit_s[n % kUnits].ta;
+        tc::mbar_arrive(bar_unitfree(n));
+        if (end == i || !wait_alone(bar_q, (uint32_t)n & 1u)) break;  // the query rows are in TMEM
+        for (; i < end; ++i) {
+          const int s = i % kStages, buf = i & 1;
+          ok = wait_alone(bar_kfull(s), (uint32_t)(i / kStages) & 1u) &&
+               wait_alone(bar_sempty(buf), ((uint32_t)(i >> 1) & 1u) ^ 1u);
+          if (!ok) break;
+          tc::fence_after_sync();
+          tc::fence_proxy_async_smem();
+          const uint64_t k_s = tc::sdesc_sw128(sK + s * C::TILE);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc::mma_bf16_ts(tmem + (uint32_t)(buf * BN), t_q + 8u * k,
+                            k_s + (((uint32_t)(k >> 2) * kBox + (uint32_t)(k & 3) * 32u) >> 4),
+                            idesc, k > 0 ? 1u : 0u);
+          tc::commit(bar_sfull(buf));
+          tc::commit(bar_kempty(s));
         }
-      } while (!dead && walk.next());
-      // drain: every MMA issued so far has completed once this commit lands
-      if (lane == 0) {
-        tc::commit(bar_done);
-        tc::mbar_wait(bar_done, 0);
+      }
+      __syncwarp();
+    } else if (warp == kValueWarp) {
+      // O += P V of a tile
+      constexpr uint32_t idesc = tc::idesc_bf16_bmn(BM, D);
+      int i = 0;
+      bool ok = lane == 0;
+      for (int n = 0; ok && (ok = wait_alone(bar_unit(n), (uint32_t)(n / kUnits) & 1u)); ++n) {
+        const int first = i, end = i + unit_s[n % kUnits].tb - unit_s[n % kUnits].ta;
+        tc::mbar_arrive(bar_unitfree(n));
+        if (end == i) break;
+        for (; i < end; ++i) {
+          // the first P of a unit comes after the previous unit's O was read
+          const int s = i % kStages;
+          ok = wait_alone(bar_vfull(s), (uint32_t)(i / kStages) & 1u) &&
+               wait_alone(bar_p(i), (uint32_t)(i >> 1) & 1u);
+          if (!ok) break;
+          tc::fence_after_sync();
+          tc::fence_proxy_async_smem();
+          const uint64_t v_s = tc::sdesc_sw128_mn(sV + s * C::TILE, kBox);
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            tc::mma_bf16_ts(t_o, t_p + 8u * k, v_s + (uint32_t)(2048 * k >> 4), idesc,
+                            (i > first || k > 0) ? 1u : 0u);
+          tc::commit(bar_vempty(s));
+          tc::commit(bar_o(i));
+        }
+      }
+      __syncwarp();
+    } else if (warp == kFindWarp) {
+      // the units, and the page ids of their tiles' keys: these are asked for tile by tile and
+      // announced when they have come
+      Walk walk;
+      walk.u = unit_s[0];
+      walk.base = walk.u.row | 31;  // its row is not among the lanes'
+      walk.base -= 31;
+      walk.left = tiles - (walk.u.tb - walk.u.ta);
+      walk.mine = {0, 0, 0, 0};
+      if (walk.base + lane < rows) walk.mine = row_of(a, walk.base + lane);
+      __syncwarp();
+      auto announce = [&](int c) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar_ids(c % kAhead));
+      };
+      int i = 0, n = 0;
+      for (bool more = true; more && !dead; more = walk.next(a, rows, g, lane), ++n) {
+        wait(bar_unitfree(n), ((uint32_t)(n / kUnits) & 1u) ^ 1u);
+        if (dead) break;
+        if (lane == 0) {
+          unit_s[n % kUnits] = walk.u;
+          tc::mbar_arrive(bar_unit(n));
+        }
+        const Unit& u = walk.u;
+        const int* table = a.block_table + (size_t)u.row * a.max_pages;
+        for (int t = u.ta; t < u.tb; ++t, ++i) {
+          const int s = i % kAhead;
+          wait(bar_idsfree(s), ((uint32_t)(i / kAhead) & 1u) ^ 1u);
+          if (dead) break;
+#pragma unroll
+          for (int c = lane; c < BN; c += 32) {
+            const int key = t * BN + c;
+            if (key < u.is.paged)
+              cp_async4(smem_u32(&ids_s[s][c]), table + (ps_shift >= 0 ? key >> ps_shift : key / a.page_size));
+          }
+          cp_async_commit();
+          if (lane == 0) at_s[s] = {u.row, t * BN, u.is.paged, u.is.all, u.is.first(), u.is.m, n, 0};
+          cp_async_wait<kAhead - 2>();
+          if (i >= kAhead - 2) announce(i - (kAhead - 2));
+        }
+      }
+      cp_async_wait<0>();
+      if (!dead)
+        for (int c = max(0, i - (kAhead - 2)); c < i; ++c) announce(c);
+      wait(bar_unitfree(n), ((uint32_t)(n / kUnits) & 1u) ^ 1u);
+      if (lane == 0 && !dead) {
+        unit_s[n % kUnits].ta = unit_s[n % kUnits].tb = 0;
+        tc::mbar_arrive(bar_unit(n));
       }
       __syncwarp();
     }
   } else {
     // ============================================================ softmax + epilogue
     take_registers<kSoftRegs>();
-    Walk walk(a, rows, g, start_s[0], start_s[1], start_s[2], tiles);
     constexpr int OC = D / 2;   // O columns of this thread in the rescale / epilogue
     constexpr int QW = D / 4;   // 32-bit words (bf16 pairs) of the query row per thread
     const int st = tid - kSoftWarp * 32;     // softmax thread
@@ -623,22 +717,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       if (a.parent && st < u.is.m) my_up = a.parent[u.is.t0 + st];
     };
     auto store_q = [&] {
+      __syncwarp();
       if (dead) return;
       if constexpr (QW == 32) tc::tmem_st32(t_q + lane_off + (uint32_t)(h * QW), qv);
       else tc::tmem_st16(t_q + lane_off + (uint32_t)(h * QW), qv);
       tc::tmem_st_wait();
+      tc::fence_before_sync();
+      tc::mbar_arrive(bar_q);
     };
-    load_q(walk.u);
-    store_q();
+    // Unit n; where a wait has run out in any warp all of them stop here, none in the same way.
+    auto fetch = [&](int n) -> Unit {
+      wait(bar_unit(n), (uint32_t)(n / kUnits) & 1u);
+      Unit u = unit_s[n % kUnits];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar_unitfree(n));
+      __syncwarp();
+      if (tc::bar_or(2, kSoftThreads, dead)) u.ta = u.tb;
+      return u;
+    };
+    Unit u = fetch(0);
+    if (!u.none()) {
+      load_q(u);
+      store_q();
+    }
     int gs = 0;  // tiles processed (all units): S buffer, exchange buffer, P and O barriers
     int sees_of = -1;  // sequence whose tree is in `sees`
-    for (int n = 0;; ++n) {
-      const Unit u = walk.u;
+    for (int n = 0; !u.none(); ++n) {
       const int x = u.mt * BM + row, live = u.is.m * g - u.mt * BM;  // query rows of the unit
       const int i = x / g, hd = x - i * g, first = u.is.first();
       const bool mine_live = row < live, warp_live = eq * 32 < live;
-      tc::fence_before_sync();
-      tc::mbar_arrive(bar_q);  // the unit's query rows are in TMEM, the previous unit's O is read
       // --- which drafted tokens each one sees, if the segment has drafted keys
       const int b = u.row % a.B;
       if (a.parent && u.is.m > 1 && u.tb * BN > first && sees_of != b) {
@@ -664,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
             for (int w = 0; w < kWords; ++w) sees[st * kWords + w] = bits[w];
             up[st] = p;
           }
+          __syncwarp();
           more = tc::bar_or(2, kSoftThreads, p >= 0);
           if (p >= 0) {
 #pragma unroll
@@ -679,10 +787,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         tc::fence_after_sync();
         if (!warp_live) {
           tc::mbar_arrive(bar_sempty(s));
+          if (j > u.ta) wait(bar_o(gs - 1), (uint32_t)((gs - 1) >> 1) & 1u);
           tc::mbar_arrive(bar_p(gs));
           continue;
         }
         uint32_t v[KC];
+        __syncwarp();
         if (!dead) {
 #pragma unroll
           for (int c = 0; c < KC; c += 32)
@@ -753,9 +863,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         if (j > u.ta) {
           wait(bar_o(gs - 1), (uint32_t)((gs - 1) >> 1) & 1u);
           tc::fence_after_sync();
+          __syncwarp();
           if (!dead && any_need) {
             const uint32_t to = t_o + lane_off + (uint32_t)(h * OC);
-#pragma unroll
+#pragma unroll 1
             for (int cb = 0; cb < OC; cb += 32) {
               tc::tmem_ld32(to + cb, v);
               tc::tmem_ld_wait();
@@ -766,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
             tc::tmem_st_wait();
           }
         }
+        __syncwarp();
         if (!dead) {
           tc::tmem_st32(t_p + lane_off + (uint32_t)(h * (KC / 2)), pk);
           tc::tmem_st_wait();
@@ -773,15 +885,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         tc::fence_before_sync();
         tc::mbar_arrive(bar_p(gs));
       }
-      const bool go_on = walk.next();
-      // the next unit's query rows load while this unit's O is finished, and take the place of this
-      // unit's, whose S products are complete
-      if (go_on) load_q(walk.u);
+      // the next unit's query rows take the place of this unit's, whose S products are complete, so
+      // that its first ones run while this unit's O is finished and written
+      const Unit next = fetch(n + 1);
+      if (!next.none()) {
+        load_q(next);
+        store_q();
+      }
       // the last two P V products of the unit (on o[0] and o[1]) complete O
       if (u.tb - u.ta > 1) wait(bar_o(gs - 2), (uint32_t)((gs - 2) >> 1) & 1u);
       wait(bar_o(gs - 1), (uint32_t)((gs - 1) >> 1) & 1u);
       tc::fence_after_sync();
-      if (go_on) store_q();
       if (warp_live) {
         xl[h * BM + row] = lsum;
         named_sync(3 + eq, 64);
@@ -793,6 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
 #pragma unroll 1
         for (int cb = 0; cb < OC && !dead; cb += 32) {
           uint32_t v[32];
+          __syncwarp();
           tc::tmem_ld32(t_o + lane_off + (uint32_t)(h * OC + cb), v);
           tc::tmem_ld_wait();
           if (dirty && mine_live) {
@@ -846,12 +961,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
           }
         }
       }
-      if (!go_on) break;
+      u = next;
     }
   }
 
+  // every product issued so far has completed once these commits land
+  if ((warp == kScoreWarp || warp == kValueWarp) && lane == 0) {
+    tc::commit(bar_done);
+    tc::mbar_wait(bar_done, 0);
+  }
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
@@ -932,7 +1052,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(
 }
 
 template <int D>
-cudaError_t launch(AttnTreeArgs a, int rows, cudaStream_t s) {
+cudaError_t launch(const AttnTreeArgs& a, int rows, cudaStream_t s) {
   using C = Cfg<D>;
   static int nsm[64] = {};
   int dev = 0;
@@ -948,16 +1068,17 @@ cudaError_t launch(AttnTreeArgs a, int rows, cudaStream_t s) {
     for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
   const long long row_tiles = ((long long)a.max_pages * a.page_size + a.w + BN - 1) / BN;
   const long long query = ((long long)a.max_draft * (a.Hq / a.Hkv) + BM - 1) / BM;
-  a.read_once = query == 1 && (long long)rows * row_tiles * 2 * C::TILE > kL2Bytes / 2;
+  const bool read_once = query == 1 && (long long)rows * row_tiles * 2 * C::TILE > kL2Bytes / 2;
   const int sms = std::min(nsm[dev], kMaxBlocks);
   // no more blocks than tiles could need
   const int blocks = (int)std::min<long long>(sms, (long long)rows * query * row_tiles);
-  e = cudaFuncSetAttribute(attn_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const auto kernel = read_once ? attn_tree_kernel<D, true> : attn_tree_kernel<D, false>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   count_launches(2);
   Launch first(dim3(blocks), kThreads, s);
   first.cfg.dynamicSmemBytes = C::SMEM;
-  e = cudaLaunchKernelEx(&first.cfg, attn_tree_kernel<D>, a, rows, shift);
+  e = cudaLaunchKernelEx(&first.cfg, kernel, a, rows, shift);
   if (e != cudaSuccess) return e;
   Launch join(dim3(blocks, BM * (D / 8) / kJoinThreads), kJoinThreads, s);
   return cudaLaunchKernelEx(&join.cfg, attn_tree_join_kernel<D>, a, rows);
@@ -969,8 +1090,7 @@ size_t attn_tree_workspace_bytes(int d) {
   return ends_bytes() + (size_t)kMaxBlocks * 2 * part_floats(d) * sizeof(float);
 }
 
-cudaError_t launch_attn_tree(const AttnTreeArgs& args, cudaStream_t s) {
-  AttnTreeArgs a = args;
+cudaError_t launch_attn_tree(const AttnTreeArgs& a, cudaStream_t s) {
   const int rows = a.L * a.Hkv * a.B;
   if (rows == 0 || a.N == 0) return cudaSuccess;
   return a.d == 128 ? launch<128>(a, rows, s) : launch<64>(a, rows, s);

@@ -26,7 +26,6 @@ struct AttnTreeArgs {
   bf16_t* o = nullptr;              // [L][Hq][N][d]
   float* lse = nullptr;             // [L][Hq][N] or null
   void* ws = nullptr;
-  bool read_once = false;           // set at launch: keys and values leave L2 first
 };
 
 size_t attn_tree_workspace_bytes(int d);
