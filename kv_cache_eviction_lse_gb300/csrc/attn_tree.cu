@@ -117,7 +117,7 @@ struct Row {
 };
 
 __device__ __forceinline__ Row row_of(const AttnTreeArgs& a, int r) {
-  const int b = r % a.B, t0 = a.tok_start[b], t1 = a.tok_start[b + 1];
+  const int b = r - a.by_batch.of(r) * a.B, t0 = a.tok_start[b], t1 = a.tok_start[b + 1];
   const int paged = max(0, min(a.seq_lens[r], a.max_pages * a.page_size));
   const bool good = t0 >= 0 && t1 >= t0 && t1 <= a.N && t1 - t0 <= a.max_draft;
   return {paged, paged + (a.w > 0 ? max(0, min(a.pos[b], a.w)) : 0), t0, good ? t1 - t0 : -1};
@@ -151,6 +151,7 @@ struct Walk {
     } else {
       u.mt = 0;
       int from = u.row - base + 1;
+#pragma unroll 1
       for (;;) {
         if (from >= 32) {
           base += from;
@@ -209,6 +210,13 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
+
+// A value that the compiler does not see through: loops stay loops (it peels those whose first or
+// last turns differ, which made 20 KB of the search for page ids).
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
 
 __device__ __forceinline__ void named_sync(int id, int nthreads) {
   __syncwarp();
@@ -269,12 +277,9 @@ template <int D, bool kOnce>
 struct Copies {
   static constexpr int kLanes = D / 8, kRows = kLanes;  // lanes of a row; rows of a group of lanes
   const AttnTreeArgs& a;
-  const int warp, lane, ps_shift;
+  const int warp, lane;
   const uint64_t policy;
 
-  __device__ __forceinline__ int page_index(int key) const {
-    return ps_shift >= 0 ? key >> ps_shift : key / a.page_size;
-  }
   // whether key `lane` of the warp's is there
   __device__ __forceinline__ bool there(const TileAt& at, const int* ids) const {
     const int key = at.key0 + warp * 32 + lane;
@@ -294,7 +299,7 @@ struct Copies {
   __device__ __forceinline__ void copy_paged(const TileAt& at, const int* ids, const bf16_t* pages,
                                              uint32_t tile) const {
     const int key0 = at.key0 + row(0);
-    const int idx = page_index(key0);
+    const int idx = a.by_page.of(key0);
     int inside = key0 - idx * a.page_size;
     const bf16_t* from = pages + lane % kLanes * 8;
     if (a.page_size % kRows == 0) {
@@ -319,7 +324,7 @@ struct Copies {
       const int key = at.key0 + row(i), page = ids[row(i)];
       const bool paged = key < at.paged;
       const bool ok = paged ? (uint32_t)page < (uint32_t)a.capacity : key < at.all;
-      const long long r = paged ? (long long)page * a.page_size + (key - page_index(key) * a.page_size)
+      const long long r = paged ? (long long)page * a.page_size + (key - a.by_page.of(key) * a.page_size)
                                 : (long long)at.row * a.w + (key - at.paged);
       const bf16_t* src = ok ? (paged ? pages : ring) + (r * D + c * 8) : a.q;
       cp_async16(tile + place(i), src, ok ? 16 : 0);
@@ -335,6 +340,7 @@ struct Copies {
   // becomes 0; true if there was any.  A lane looks at the chunks that it copied.
   __device__ __forceinline__ bool clean(uint8_t* tile, int lo, int hi) const {
     bool any = false;
+#pragma unroll 1
     for (int i = 0; i < kRows; ++i) {
       const int r = row(i) - warp * 32;
       if (r < lo || r >= hi) continue;
@@ -354,15 +360,23 @@ struct Copies {
   }
 };
 
-// The rest of a wait that does not end at once; false if it runs out, or another's in the block.
+// The rest of a wait that does not end at once; false if it runs out, or another's in the block.  The
+// hardware holds the thread up to 20 us at a time, so that waiting warps leave the others their issue
+// slots.
 __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
   const uint64_t t0 = tc::globaltimer();
   for (;;) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
     if (*abort_flag) return false;
     if (tc::globaltimer() - t0 > tc::kWaitLimitNs) {
       *abort_flag = 1u;
-      atomicCAS(&g_attn_tree_error, 0, kErrWaitTimeout);
       return false;
     }
   }
@@ -372,7 +386,7 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
 // the warps waited for instructions a third of the time, 1.4 us a tile.
 template <int D, bool kOnce>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
-    const __grid_constant__ AttnTreeArgs a, int rows, int ps_shift) {
+    const __grid_constant__ AttnTreeArgs a, int rows) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int warp_tiles[kWarps];
@@ -451,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
   Ends* ends = static_cast<Ends*>(a.ws);
   int mine = 0, before = 0, s0 = -1, tiles = 0;
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
+  for (int pass = opaque(0); pass < 2; ++pass) {
     if (pass == 0 || (before <= s0 && s0 < before + mine)) {
       int at = s0 - before;
 #pragma unroll 1
@@ -519,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
   if (warp < kCopyWarps) {
     // ============================================================ copies of K and V
     give_registers<kCopyRegs>();
-    Copies<D, kOnce> copies{a, warp, lane, ps_shift, read_once_policy()};
+    Copies<D, kOnce> copies{a, warp, lane, read_once_policy()};
     // A stage is announced by its copies as they land; the issuer of the products makes them visible
     // to the tensor core.  V of a tile with drafted rows is searched first, when the next tile's
     // copies are on their way.
@@ -532,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       tc::mbar_arrive(bar_vfull(s));
       held = -1;
     };
+#pragma unroll 1
     for (int i = 0; i < tiles && !dead; ++i) {
       wait(bar_ids(i % kAhead), (uint32_t)(i / kAhead) & 1u);
       if (dead) break;
@@ -586,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         const int end = i + unit_s[n % kUnits].tb - unit_s[n % kUnits].ta;
         tc::mbar_arrive(bar_unitfree(n));
         if (end == i || !wait_alone(bar_q, (uint32_t)n & 1u)) break;  // the query rows are in TMEM
+#pragma unroll 1
         for (; i < end; ++i) {
           const int s = i % kStages, buf = i & 1;
           ok = wait_alone(bar_kfull(s), (uint32_t)(i / kStages) & 1u) &&
@@ -613,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         const int first = i, end = i + unit_s[n % kUnits].tb - unit_s[n % kUnits].ta;
         tc::mbar_arrive(bar_unitfree(n));
         if (end == i) break;
+#pragma unroll 1
         for (; i < end; ++i) {
           // the first P of a unit comes after the previous unit's O was read
           const int s = i % kStages;
@@ -647,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         if (lane == 0) tc::mbar_arrive(bar_ids(c % kAhead));
       };
       int i = 0, n = 0;
+#pragma unroll 1
       for (bool more = true; more && !dead; more = walk.next(a, rows, g, lane), ++n) {
         wait(bar_unitfree(n), ((uint32_t)(n / kUnits) & 1u) ^ 1u);
         if (dead) break;
@@ -656,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         }
         const Unit& u = walk.u;
         const int* table = a.block_table + (size_t)u.row * a.max_pages;
+#pragma unroll 1
         for (int t = u.ta; t < u.tb; ++t, ++i) {
           const int s = i % kAhead;
           wait(bar_idsfree(s), ((uint32_t)(i / kAhead) & 1u) ^ 1u);
@@ -664,12 +683,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
           for (int c = lane; c < BN; c += 32) {
             const int key = t * BN + c;
             if (key < u.is.paged)
-              cp_async4(smem_u32(&ids_s[s][c]), table + (ps_shift >= 0 ? key >> ps_shift : key / a.page_size));
+              cp_async4(smem_u32(&ids_s[s][c]), table + a.by_page.of(key));
           }
           cp_async_commit();
           if (lane == 0) at_s[s] = {u.row, t * BN, u.is.paged, u.is.all, u.is.first(), u.is.m, n, 0};
           cp_async_wait<kAhead - 2>();
-          if (i >= kAhead - 2) announce(i - (kAhead - 2));
+          if (opaque(i) >= kAhead - 2) announce(i - (kAhead - 2));
         }
       }
       cp_async_wait<0>();
@@ -699,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
     auto load_q = [&](const Unit& u) {
       const int x = u.mt * BM + row;
       if (x < u.is.m * g) {
-        const int i = x / g, hd = x - i * g, l_hk = u.row / a.B;
+        const int i = a.by_group.of(x), hd = x - i * g, l_hk = a.by_batch.of(u.row);
         const uint4* src = reinterpret_cast<const uint4*>(
             a.q + (((size_t)l_hk * g + hd) * a.N + u.is.t0 + i) * D + h * OC);
 #pragma unroll
@@ -744,10 +763,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
     int sees_of = -1;  // sequence whose tree is in `sees`
     for (int n = 0; !u.none(); ++n) {
       const int x = u.mt * BM + row, live = u.is.m * g - u.mt * BM;  // query rows of the unit
-      const int i = x / g, hd = x - i * g, first = u.is.first();
+      const int i = a.by_group.of(x), hd = x - i * g, first = u.is.first();
       const bool mine_live = row < live, warp_live = eq * 32 < live;
       // --- which drafted tokens each one sees, if the segment has drafted keys
-      const int b = u.row % a.B;
+      const int b = u.row - a.by_batch.of(u.row) * a.B;
       if (a.parent && u.is.m > 1 && u.tb * BN > first && sees_of != b) {
         sees_of = b;
         uint32_t bits[kWords];
@@ -781,8 +800,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         }
       }
       float m_used = -CUDART_INF_F, lsum = 0.f;
+      Unit next;
+#pragma unroll 1
       for (int j = u.ta; j < u.tb; ++j, ++gs) {
         const int s = gs & 1;  // max-exchange buffer and S buffer
+        // the next unit's query rows are asked for two tiles early: under a saturated HBM they take
+        // longer than one
+        if (j == max(u.ta, u.tb - 2)) {
+          next = fetch(n + 1);
+          if (!next.none()) load_q(next);
+        }
         wait(bar_sfull(s), (uint32_t)(gs >> 1) & 1u);
         tc::fence_after_sync();
         if (!warp_live) {
@@ -887,11 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       }
       // the next unit's query rows take the place of this unit's, whose S products are complete, so
       // that its first ones run while this unit's O is finished and written
-      const Unit next = fetch(n + 1);
-      if (!next.none()) {
-        load_q(next);
-        store_q();
-      }
+      if (!next.none()) store_q();
       // the last two P V products of the unit (on o[0] and o[1]) complete O
       if (u.tb - u.ta > 1) wait(bar_o(gs - 2), (uint32_t)((gs - 2) >> 1) & 1u);
       wait(bar_o(gs - 1), (uint32_t)((gs - 1) >> 1) & 1u);
@@ -902,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         lsum += xl[(h ^ 1) * BM + row];
         const bool dirty = dirty_s[n % kDirty] == n + 1;
         const float inv = inverse(lsum);
-        const size_t out = ((size_t)(u.row / a.B) * g + hd) * a.N + u.is.t0 + i;
+        const size_t out = ((size_t)a.by_batch.of(u.row) * g + hd) * a.N + u.is.t0 + i;
         float* part = block_part(a.ws, blockIdx.x, u.ta > 0 ? 0 : 1, part_floats(D));
 #pragma unroll 1
         for (int cb = 0; cb < OC && !dead; cb += 32) {
@@ -918,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
               const int slot = first + k;
               const bool seen = !a.parent ? k <= i : sees[i * kWords + (k >> 5)] >> (k & 31) & 1;
               if (!seen || slot < 0) continue;
-              const int idx = slot / a.page_size;
+              const int idx = a.by_page.of(slot);
               const int page = a.block_table[(size_t)u.row * a.max_pages + idx];
               if ((uint32_t)page >= (uint32_t)a.capacity) continue;
               const bf16_t* src =
@@ -971,6 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
     tc::mbar_wait(bar_done, 0);
   }
   __syncthreads();
+  if (tid == 0 && *abort_flag) atomicCAS(&g_attn_tree_error, 0, kErrWaitTimeout);
   if (warp == kScoreWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
@@ -990,7 +1014,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(
     const Row x = row_of(a, r);
     if (x.all > 0) continue;
     for (int i = lane; i < x.m * g; i += 32) {
-      const size_t out = ((size_t)(r / a.B) * g + i % g) * a.N + x.t0 + i / g;
+      const int tok = a.by_group.of(i);
+      const size_t out = ((size_t)a.by_batch.of(r) * g + i - tok * g) * a.N + x.t0 + tok;
       for (int e = 0; e < D / 8; ++e)
         reinterpret_cast<uint4*>(a.o + out * D)[e] = make_uint4(0, 0, 0, 0);
       if (a.lse) a.lse[out] = -INFINITY;
@@ -1042,8 +1067,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(
       acc[7] += y[i][1].w * v;
     }
   }
-  const int i = (int)x / g, hd = (int)x - i * g;
-  const size_t out = ((size_t)(end.row / a.B) * g + hd) * a.N + is.t0 + i;
+  const int i = a.by_group.of((int)x), hd = (int)x - i * g;
+  const size_t out = ((size_t)a.by_batch.of(end.row) * g + hd) * a.N + is.t0 + i;
   const float inv = inverse(sum);
   reinterpret_cast<uint4*>(a.o + out * D)[c8] =
       make_uint4(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv),
@@ -1052,7 +1077,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(
 }
 
 template <int D>
-cudaError_t launch(const AttnTreeArgs& a, int rows, cudaStream_t s) {
+cudaError_t launch(AttnTreeArgs a, int rows, cudaStream_t s) {
   using C = Cfg<D>;
   static int nsm[64] = {};
   int dev = 0;
@@ -1063,9 +1088,9 @@ cudaError_t launch(const AttnTreeArgs& a, int rows, cudaStream_t s) {
     e = cudaDeviceGetAttribute(&nsm[dev], cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
   }
-  int shift = -1;
-  if ((a.page_size & (a.page_size - 1)) == 0)
-    for (shift = 0; (1 << shift) < a.page_size; ++shift) {}
+  a.by_batch = Divisor(a.B);
+  a.by_page = Divisor(a.page_size);
+  a.by_group = Divisor(a.Hq / a.Hkv);
   const long long row_tiles = ((long long)a.max_pages * a.page_size + a.w + BN - 1) / BN;
   const long long query = ((long long)a.max_draft * (a.Hq / a.Hkv) + BM - 1) / BM;
   const bool read_once = query == 1 && (long long)rows * row_tiles * 2 * C::TILE > kL2Bytes / 2;
@@ -1078,7 +1103,7 @@ cudaError_t launch(const AttnTreeArgs& a, int rows, cudaStream_t s) {
   count_launches(2);
   Launch first(dim3(blocks), kThreads, s);
   first.cfg.dynamicSmemBytes = C::SMEM;
-  e = cudaLaunchKernelEx(&first.cfg, kernel, a, rows, shift);
+  e = cudaLaunchKernelEx(&first.cfg, kernel, a, rows);
   if (e != cudaSuccess) return e;
   Launch join(dim3(blocks, BM * (D / 8) / kJoinThreads), kJoinThreads, s);
   return cudaLaunchKernelEx(&join.cfg, attn_tree_join_kernel<D>, a, rows);
