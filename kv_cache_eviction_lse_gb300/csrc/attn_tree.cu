@@ -255,9 +255,21 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src));
 }
 
-// An arrival on `bar` when all copies that this thread has started have landed.
-__device__ __forceinline__ void arrive_when_landed(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+// The phase of `bar` that is going on also waits for all copies that this thread has started.
+__device__ __forceinline__ void wait_for_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+template <bool kOnce>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                         int c1, int c2, uint64_t policy) {
+  if constexpr (kOnce)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        : "memory");
+  else
+    tc::tma_load_3d(dst, map, bar, c0, c1, c2);
 }
 
 __device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.f : m; }
@@ -336,6 +348,19 @@ struct Copies {
     else copy_any(at, ids, pages, ring, tile);
     __syncwarp();
   }
+  // The same 32 keys by TMA, where pages divide them or they pages: a lane a box of up to 32 rows of
+  // 64 elements.
+  __device__ __forceinline__ void copy_boxes(const TileAt& at, const int* ids, const CUtensorMap* map,
+                                             uint32_t tile, uint32_t bar) const {
+    constexpr int KH = D / 64;
+    const int r = lane / KH * a.box_rows;
+    if (r < 32) {
+      const int key = at.key0 + warp * 32 + r, inside = key - a.by_page.of(key) * a.page_size;
+      tma_load<kOnce>(tile + lane % KH * kBox + (warp * 32 + r) * 128, map, bar, lane % KH * 64, inside,
+                      ids[warp * 32 + r], policy);
+    }
+    __syncwarp();
+  }
   // Drafted rows lo .. hi - 1 of this warp's 32 of a V tile that has landed: what is not finite
   // becomes 0; true if there was any.  A lane looks at the chunks that it copied.
   __device__ __forceinline__ bool clean(uint8_t* tile, int lo, int hi) const {
@@ -360,20 +385,18 @@ struct Copies {
   }
 };
 
-// The rest of a wait that does not end at once; false if it runs out, or another's in the block.  The
-// hardware holds the thread up to 20 us at a time, so that waiting warps leave the others their issue
-// slots.
+// The rest of a wait that does not end at once; false if it runs out, or another's in the block.
+// Threads that wait leave the others their issue slots: those that work ahead sleep, the others turn
+// in a loop of four instructions.
+template <int kSleepNs>
 __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
   const uint64_t t0 = tc::globaltimer();
   for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    if (ok) return true;
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+      if (tc::mbar_try_wait(bar, parity)) return true;
+      if constexpr (kSleepNs > 0) __nanosleep(kSleepNs);
+    }
     if (*abort_flag) return false;
     if (tc::globaltimer() - t0 > tc::kWaitLimitNs) {
       *abort_flag = 1u;
@@ -386,7 +409,8 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
 // the warps waited for instructions a third of the time, 1.4 us a tile.
 template <int D, bool kOnce>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
-    const __grid_constant__ AttnTreeArgs a, int rows) {
+    const __grid_constant__ AttnTreeArgs a, const __grid_constant__ CUtensorMap map_k,
+    const __grid_constant__ CUtensorMap map_v, int rows) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int warp_tiles[kWarps];
@@ -430,9 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
   if (tid == 0) {
     tc::mbar_init(bar_q, kSoftThreads);
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(bar_kfull(s), kCopyWarps * 33);  // every thread's copies, and each warp's word
+      tc::mbar_init(bar_kfull(s), kCopyWarps);
       tc::mbar_init(bar_kempty(s), 1);
-      tc::mbar_init(bar_vfull(s), kCopyWarps * 32);
+      tc::mbar_init(bar_vfull(s), kCopyWarps);
       tc::mbar_init(bar_vempty(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -521,13 +545,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
   const uint32_t t_p = tmem + C::COL_P, t_q = tmem + C::COL_Q, t_o = tmem + C::COL_O;
   // One thread's wait; false if it has run out, or another's in the block.
   auto wait_alone = [&](uint32_t bar, uint32_t parity) -> bool {
-    return tc::mbar_try_wait(bar, parity) || wait_on(bar, parity, abort_flag);
+    return tc::mbar_try_wait(bar, parity) || wait_on<0>(bar, parity, abort_flag);
   };
-  // A warp's.  Once one has run out, a warp only goes through the motions (arrivals and named
-  // barriers, no waits, no TMEM), so that none is left waiting for it.  The same in all lanes.
+  // A warp's.  Once one has run out, a warp only goes through the motions without waiting (tests of
+  // that around the work on TMEM cost 200 moves a tile), so that none is left waiting for it; what
+  // comes of it does not count.  The same in all lanes.
   bool dead = false;
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (!dead) dead = !__all_sync(0xffffffffu, wait_alone(bar, parity));
+  };
+  auto wait_ahead = [&](uint32_t bar, uint32_t parity) {
+    if (!dead)
+      dead = !__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity) || wait_on<100>(bar, parity, abort_flag));
   };
 
   if (warp < kCopyWarps) {
@@ -543,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       if (copies.clean(smem + C::OFF_V + s * C::TILE, held_lo, held_hi))
         dirty_s[held_unit % kDirty] = held_unit + 1;
       tc::fence_proxy_async_smem();
-      tc::mbar_arrive(bar_vfull(s));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar_vfull(s));
       held = -1;
     };
 #pragma unroll 1
@@ -553,42 +583,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       const TileAt at = at_s[i % kAhead];
       const int* ids = ids_s[i % kAhead];
       const uint32_t there = __ballot_sync(0xffffffffu, copies.there(at, ids));
-      const bool whole = !~there && at.key0 + warp * 32 + 32 <= at.paged;
+      const int k0 = at.key0 + warp * 32;
+      const int lo = max(0, min(32, at.first - k0)), hi = at.m > 1 ? max(0, min(32, at.paged - k0)) : 0;
+      const bool whole = !~there && k0 + 32 <= at.paged;
       const int s = i % kStages;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        wait(kv ? bar_vempty(s) : bar_kempty(s), (uint32_t)(i / kStages & 1) ^ 1u);
+        const uint32_t full = kv ? bar_vfull(s) : bar_kfull(s), to = (kv ? sV : sK) + s * C::TILE;
+        wait_ahead(kv ? bar_vempty(s) : bar_kempty(s), (uint32_t)(i / kStages & 1) ^ 1u);
         if (dead) break;
-        copies.copy(whole, at, ids, kv ? a.v_pages : a.k_pages, kv ? a.ring_v : a.ring_k,
-                    (kv ? sV : sK) + s * C::TILE);
-        cp_async_commit();
-        if (kv == 0) {
-          if (lane == 0) {
-            live_s[i % kLive][warp] = there;
-            tc::mbar_arrive(bar_kfull(s));
+        const bool search = kv && lo < hi;
+        if (!kv && lane == 0) live_s[i % kLive][warp] = there;
+        if (whole && a.box_rows && !search) {
+          if (lane == 0) tc::mbar_expect_tx(full, 32 * D * 2);
+          __syncwarp();
+          copies.copy_boxes(at, ids, kv ? &map_v : &map_k, to, full);
+        } else {
+          copies.copy(whole, at, ids, kv ? a.v_pages : a.k_pages, kv ? a.ring_v : a.ring_k, to);
+          if (!search) {
+            wait_for_copies(full);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(full);
           }
-          arrive_when_landed(bar_kfull(s));
+        }
+        cp_async_commit();
+        if (held >= 0) {  // the copies that came after it may still be on their way
+          cp_async_wait<1>();
+          release();
+        }
+        if (search) {
+          held = i;
+          held_unit = at.unit;
+          held_lo = lo;
+          held_hi = hi;
         }
       }
-      if (dead) break;
-      if (lane == 0) tc::mbar_arrive(bar_idsfree(i % kAhead));
-      const int k0 = at.key0 + warp * 32;
-      const int lo = max(0, min(32, at.first - k0)), hi = at.m > 1 ? max(0, min(32, at.paged - k0)) : 0;
-      if (held >= 0) {
-        cp_async_wait<2>();
-        release();
-      }
-      if (lo < hi) {
-        held = i;
-        held_unit = at.unit;
-        held_lo = lo;
-        held_hi = hi;
-      } else {
-        arrive_when_landed(bar_vfull(s));
-      }
+      if (lane == 0 && !dead) tc::mbar_arrive(bar_idsfree(i % kAhead));
     }
     cp_async_wait<0>();
     if (held >= 0 && !dead) release();
+    if (dead) {  // boxes on their way land within microseconds, before the block may leave
+      const uint64_t t0 = tc::globaltimer();
+      while (tc::globaltimer() - t0 < 1000000) {}
+    }
   } else if (warp >= kScoreWarp) {
     // ============================================================ products, page ids
     give_registers<kMmaRegs>();
@@ -663,27 +700,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar_ids(c % kAhead));
       };
-      int i = 0, n = 0;
-#pragma unroll 1
-      for (bool more = true; more && !dead; more = walk.next(a, rows, g, lane), ++n) {
-        wait(bar_unitfree(n), ((uint32_t)(n / kUnits) & 1u) ^ 1u);
-        if (dead) break;
-        if (lane == 0) {
+      // units are published one ahead of their tiles' page ids: the softmax asks for the next one when
+      // it begins one
+      auto publish = [&](int n, bool some) {
+        wait_ahead(bar_unitfree(n), ((uint32_t)(n / kUnits) & 1u) ^ 1u);
+        if (lane == 0 && !dead) {
           unit_s[n % kUnits] = walk.u;
+          if (!some) unit_s[n % kUnits].ta = unit_s[n % kUnits].tb;
           tc::mbar_arrive(bar_unit(n));
         }
-        const Unit& u = walk.u;
+        __syncwarp();
+      };
+      int i = 0, n = 0;
+      publish(0, true);
+#pragma unroll 1
+      for (bool more = true; more && !dead; ++n) {
+        const Unit u = walk.u;
+        more = walk.next(a, rows, g, lane);
+        publish(n + 1, more);
         const int* table = a.block_table + (size_t)u.row * a.max_pages;
 #pragma unroll 1
         for (int t = u.ta; t < u.tb; ++t, ++i) {
           const int s = i % kAhead;
-          wait(bar_idsfree(s), ((uint32_t)(i / kAhead) & 1u) ^ 1u);
+          wait_ahead(bar_idsfree(s), ((uint32_t)(i / kAhead) & 1u) ^ 1u);
           if (dead) break;
 #pragma unroll
           for (int c = lane; c < BN; c += 32) {
             const int key = t * BN + c;
-            if (key < u.is.paged)
-              cp_async4(smem_u32(&ids_s[s][c]), table + a.by_page.of(key));
+            if (key < u.is.paged) cp_async4(smem_u32(&ids_s[s][c]), table + a.by_page.of(key));
           }
           cp_async_commit();
           if (lane == 0) at_s[s] = {u.row, t * BN, u.is.paged, u.is.all, u.is.first(), u.is.m, n, 0};
@@ -694,11 +738,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       cp_async_wait<0>();
       if (!dead)
         for (int c = max(0, i - (kAhead - 2)); c < i; ++c) announce(c);
-      wait(bar_unitfree(n), ((uint32_t)(n / kUnits) & 1u) ^ 1u);
-      if (lane == 0 && !dead) {
-        unit_s[n % kUnits].ta = unit_s[n % kUnits].tb = 0;
-        tc::mbar_arrive(bar_unit(n));
-      }
       __syncwarp();
     }
   } else {
@@ -767,12 +806,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       const bool mine_live = row < live, warp_live = eq * 32 < live;
       // --- which drafted tokens each one sees, if the segment has drafted keys
       const int b = u.row - a.by_batch.of(u.row) * a.B;
+      // the next unit's query rows are asked for early: under a saturated HBM they take longer than a
+      // tile
+      const int up_now = my_up;
+      const Unit next = fetch(n + 1);
+      if (!next.none()) load_q(next);
       if (a.parent && u.is.m > 1 && u.tb * BN > first && sees_of != b) {
         sees_of = b;
         uint32_t bits[kWords];
         int p = -1;
         if (st < u.is.m) {
-          p = my_up;
+          p = up_now;
           if (p < -1 || p >= st) {
             fault();
             p = -1;
@@ -800,16 +844,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         }
       }
       float m_used = -CUDART_INF_F, lsum = 0.f;
-      Unit next;
 #pragma unroll 1
       for (int j = u.ta; j < u.tb; ++j, ++gs) {
         const int s = gs & 1;  // max-exchange buffer and S buffer
-        // the next unit's query rows are asked for two tiles early: under a saturated HBM they take
-        // longer than one
-        if (j == max(u.ta, u.tb - 2)) {
-          next = fetch(n + 1);
-          if (!next.none()) load_q(next);
-        }
         wait(bar_sfull(s), (uint32_t)(gs >> 1) & 1u);
         tc::fence_after_sync();
         if (!warp_live) {
@@ -820,12 +857,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         }
         uint32_t v[KC];
         __syncwarp();
-        if (!dead) {
 #pragma unroll
-          for (int c = 0; c < KC; c += 32)
-            tc::tmem_ld32(tmem + lane_off + (uint32_t)(s * BN + h * KC + c), v + c);
-          tc::tmem_ld_wait();
-        }
+        for (int c = 0; c < KC; c += 32)
+          tc::tmem_ld32(tmem + lane_off + (uint32_t)(s * BN + h * KC + c), v + c);
+        tc::tmem_ld_wait();
         // of the thread's 64 keys: those there are, without drafted ones that are not seen
         uint64_t vis = (uint64_t)live_s[gs % kLive][2 * h + 1] << 32 | live_s[gs % kLive][2 * h];
         tc::fence_before_sync();
@@ -837,7 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
                                 : mine_live ? bits_from(sees + i * kWords, kb - first) : 0ull;
           vis &= ~drafts | seen;
         }
-        if (~vis) {
+        if (__any_sync(0xffffffffu, ~vis != 0)) {
+          asm volatile("");  // a branch: most tiles have nothing to mask
           const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
 #pragma unroll
           for (int c = 0; c < KC; ++c)
@@ -891,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
           wait(bar_o(gs - 1), (uint32_t)((gs - 1) >> 1) & 1u);
           tc::fence_after_sync();
           __syncwarp();
-          if (!dead && any_need) {
+          if (any_need) {
             const uint32_t to = t_o + lane_off + (uint32_t)(h * OC);
 #pragma unroll 1
             for (int cb = 0; cb < OC; cb += 32) {
@@ -905,10 +941,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
           }
         }
         __syncwarp();
-        if (!dead) {
-          tc::tmem_st32(t_p + lane_off + (uint32_t)(h * (KC / 2)), pk);
-          tc::tmem_st_wait();
-        }
+        tc::tmem_st32(t_p + lane_off + (uint32_t)(h * (KC / 2)), pk);
+        tc::tmem_st_wait();
         tc::fence_before_sync();
         tc::mbar_arrive(bar_p(gs));
       }
@@ -928,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         const size_t out = ((size_t)a.by_batch.of(u.row) * g + hd) * a.N + u.is.t0 + i;
         float* part = block_part(a.ws, blockIdx.x, u.ta > 0 ? 0 : 1, part_floats(D));
 #pragma unroll 1
-        for (int cb = 0; cb < OC && !dead; cb += 32) {
+        for (int cb = 0; cb < OC; cb += 32) {
           uint32_t v[32];
           __syncwarp();
           tc::tmem_ld32(t_o + lane_off + (uint32_t)(h * OC + cb), v);
@@ -1091,6 +1125,9 @@ cudaError_t launch(AttnTreeArgs a, int rows, cudaStream_t s) {
   a.by_batch = Divisor(a.B);
   a.by_page = Divisor(a.page_size);
   a.by_group = Divisor(a.Hq / a.Hkv);
+  // pages of 8, 16 or 32 rows, or of several times 32, come by TMA
+  a.box_rows = a.page_size % 32 == 0 ? 32 : a.page_size == 8 || a.page_size == 16 ? a.page_size : 0;
+  if (a.capacity == 0) a.box_rows = 0;
   const long long row_tiles = ((long long)a.max_pages * a.page_size + a.w + BN - 1) / BN;
   const long long query = ((long long)a.max_draft * (a.Hq / a.Hkv) + BM - 1) / BM;
   const bool read_once = query == 1 && (long long)rows * row_tiles * 2 * C::TILE > kL2Bytes / 2;
@@ -1100,10 +1137,17 @@ cudaError_t launch(AttnTreeArgs a, int rows, cudaStream_t s) {
   const auto kernel = read_once ? attn_tree_kernel<D, true> : attn_tree_kernel<D, false>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
+  CUtensorMap map_k, map_v;
+  e = tma_map_bf16_3d(&map_k, a.box_rows ? a.k_pages : a.q, D, a.box_rows ? a.page_size : 1,
+                      a.box_rows ? a.capacity : 1, a.box_rows ? a.box_rows : 8);
+  if (e == cudaSuccess)
+    e = tma_map_bf16_3d(&map_v, a.box_rows ? a.v_pages : a.q, D, a.box_rows ? a.page_size : 1,
+                        a.box_rows ? a.capacity : 1, a.box_rows ? a.box_rows : 8);
+  if (e != cudaSuccess) return e;
   count_launches(2);
   Launch first(dim3(blocks), kThreads, s);
   first.cfg.dynamicSmemBytes = C::SMEM;
-  e = cudaLaunchKernelEx(&first.cfg, kernel, a, rows);
+  e = cudaLaunchKernelEx(&first.cfg, kernel, a, map_k, map_v, rows);
   if (e != cudaSuccess) return e;
   Launch join(dim3(blocks, BM * (D / 8) / kJoinThreads), kJoinThreads, s);
   return cudaLaunchKernelEx(&join.cfg, attn_tree_join_kernel<D>, a, rows);

@@ -40,6 +40,7 @@ struct AttnTreeArgs {
   bf16_t* o = nullptr;              // [L][Hq][N][d]
   float* lse = nullptr;             // [L][Hq][N] or null
   void* ws = nullptr;
+  int box_rows = 0;                 // set at launch: rows of a TMA box, or 0
   Divisor by_batch, by_page, by_group;  // set at launch: by B, page_size, Hq / Hkv
 };
 

@@ -393,15 +393,21 @@ def test_two_streams_and_two_threads(C):
     rs = [call(C, c, stream=s) for c, s in zip(cs, streams)]
     torch.cuda.synchronize()
 
+    raised = []
+
     def work(r):
-        for _ in range(20):
-            r["go"]()
+        try:
+            for _ in range(20):
+                r["go"]()
+        except Exception as e:  # an exception of a thread fails no test by itself
+            raised.append(e)
 
     threads = [threading.Thread(target=work, args=(r,)) for r in rs]
     for t in threads:
         t.start()
     for t in threads:
         t.join()
+    assert not raised
     torch.cuda.synchronize()
     assert C.kvs_device_error() == 0
     for c, r, x in zip(cs, rs, want):
