@@ -306,32 +306,42 @@ struct Copies {
     const int c = lane % kLanes;
     return (uint32_t)(c >> 3) * kBox + row(i) * 128 + (((c & 7) ^ (row(i) & 7)) << 4);
   }
-  // All 32 keys are in pages that are there.  A lone warp issues an instruction every few cycles, so
-  // the copies have to be most of them: where a lane's rows lie in one page there is one address.
-  __device__ __forceinline__ void copy_paged(const TileAt& at, const int* ids, const bf16_t* pages,
-                                             uint32_t tile) const {
+  // The first `count` of the 32 keys, in pages that are there.  A lone warp issues an instruction
+  // every few cycles, so the copies have to be most of them: where a lane's rows lie in one page
+  // there is one address.  Rows behind them become zeros if asked for (of V: a weight of 0 times
+  // what lies there must be 0; scores of keys that are not there are masked).
+  __device__ __forceinline__ void copy_paged(const TileAt& at, const int* ids, int count, bool zeros,
+                                             const bf16_t* pages, uint32_t tile) const {
+    const int r0 = row(0) - warp * 32, mine = count - r0;  // of the lane's rows
     const int key0 = at.key0 + row(0);
-    const int idx = a.by_page.of(key0);
-    int inside = key0 - idx * a.page_size;
+    int inside = key0 - a.by_page.of(key0) * a.page_size;
     const bf16_t* from = pages + lane % kLanes * 8;
     if (a.page_size % kRows == 0) {
-      from += ((size_t)ids[row(0)] * a.page_size + inside) * D;
+      if (mine > 0) from += ((size_t)ids[row(0)] * a.page_size + inside) * D;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) cp_async16_whole<kOnce>(tile + place(i), from + i * D, policy);
-      return;
-    }
+      for (int i = 0; i < kRows; ++i)
+        if (i < mine) cp_async16_whole<kOnce>(tile + place(i), from + i * D, policy);
+    } else {
 #pragma unroll 4
-    for (int i = 0; i < kRows; ++i) {
-      const bf16_t* src = from + ((size_t)ids[row(i)] * a.page_size + inside) * D;
-      cp_async16_whole<kOnce>(tile + place(i), src, policy);
-      if (++inside == a.page_size) inside = 0;
+      for (int i = 0; i < kRows; ++i) {
+        if (i < mine)
+          cp_async16_whole<kOnce>(tile + place(i),
+                                  from + ((size_t)ids[row(i)] * a.page_size + inside) * D, policy);
+        if (++inside == a.page_size) inside = 0;
+      }
+    }
+    if (zeros && count < 32) {
+#pragma unroll 4
+      for (int i = 0; i < kRows; ++i)
+        if (i >= mine)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + place(i)), "r"(0) : "memory");
     }
   }
   // Any keys: in pages, in the ring, or not there.
   __device__ __forceinline__ void copy_any(const TileAt& at, const int* ids, const bf16_t* pages,
                                            const bf16_t* ring, uint32_t tile) const {
     const int c = lane % kLanes;
-#pragma unroll 1
+#pragma unroll 2
     for (int i = 0; i < kRows; ++i) {
       const int key = at.key0 + row(i), page = ids[row(i)];
       const bool paged = key < at.paged;
@@ -341,12 +351,6 @@ struct Copies {
       const bf16_t* src = ok ? (paged ? pages : ring) + (r * D + c * 8) : a.q;
       cp_async16(tile + place(i), src, ok ? 16 : 0);
     }
-  }
-  __device__ __forceinline__ void copy(bool whole, const TileAt& at, const int* ids,
-                                       const bf16_t* pages, const bf16_t* ring, uint32_t tile) const {
-    if (whole) copy_paged(at, ids, pages, tile);
-    else copy_any(at, ids, pages, ring, tile);
-    __syncwarp();
   }
   // The same 32 keys by TMA, where pages divide them or they pages: a lane a box of up to 32 rows of
   // 64 elements.
@@ -585,7 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       const uint32_t there = __ballot_sync(0xffffffffu, copies.there(at, ids));
       const int k0 = at.key0 + warp * 32;
       const int lo = max(0, min(32, at.first - k0)), hi = at.m > 1 ? max(0, min(32, at.paged - k0)) : 0;
-      const bool whole = !~there && k0 + 32 <= at.paged;
+      // the keys there are the first ones, in pages (no ring, no bad page id); all 32
+      const int here = max(0, min(32, at.paged - k0));
+      const bool plain = there == (uint32_t)low_bits(here), whole = here == 32 && !~there;
       const int s = i % kStages;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
@@ -599,8 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
           __syncwarp();
           copies.copy_boxes(at, ids, kv ? &map_v : &map_k, to, full);
         } else {
-          copies.copy(whole, at, ids, kv ? a.v_pages : a.k_pages, kv ? a.ring_v : a.ring_k, to);
+          const bf16_t* pages = kv ? a.v_pages : a.k_pages;
+          if (plain) copies.copy_paged(at, ids, here, kv, pages, to);
+          else copies.copy_any(at, ids, pages, kv ? a.ring_v : a.ring_k, to);
+          __syncwarp();
           if (!search) {
+            if (kv) tc::fence_proxy_async_smem();  // of the zeros
             wait_for_copies(full);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full);
