@@ -204,12 +204,18 @@ __device__ __forceinline__ uint64_t bits_from(const uint32_t* row, int off) {
   for (int i = 0; i < 3; ++i) w[i] = (uint32_t)(w0 + i) < (uint32_t)kWords ? row[w0 + i] : 0u;
   return (uint64_t)__funnelshift_r(w[1], w[2], s) << 32 | __funnelshift_r(w[0], w[1], s);
 }
+// The same of a row of one word.
+__device__ __forceinline__ uint64_t bits_of(uint32_t row, int off) {
+  return off >= 32 || off <= -64 ? 0ull : off >= 0 ? (uint64_t)(row >> off) : (uint64_t)row << -off;
+}
 // The lowest n of 64 bits.
 __device__ __forceinline__ uint64_t low_bits(int n) {
   return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
+// Bits 15 and 31: whether either half is not finite (its exponent plus one carries).
+__device__ __forceinline__ uint32_t not_finite2(uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; }
 
 // A value that the compiler does not see through: loops stay loops (it peels those whose first or
 // last turns differ, which made 20 KB of the search for page ids).
@@ -292,13 +298,23 @@ struct Copies {
   const int warp, lane;
   const uint64_t policy;
 
-  // whether key `lane` of the warp's is there
-  __device__ __forceinline__ bool there(const TileAt& at, const int* ids) const {
+  // Of the tile: the lane's key's row in the pool or in the rings (rows of a pool that fits the GPU
+  // stay within 32 bits), and which of the 32 keys are there and which are in the ring.
+  uint32_t at_row = 0, there = 0, ringed = 0;
+  __device__ __forceinline__ void resolve(const TileAt& at, const int* ids) {
     const int key = at.key0 + warp * 32 + lane;
-    if (key >= at.paged) return key < at.all;
-    const bool good = (uint32_t)ids[warp * 32 + lane] < (uint32_t)a.capacity;
-    if (!good) fault();
-    return good;
+    const bool paged = key < at.paged;
+    bool ok = key < at.all;
+    if (paged) {
+      const int page = ids[warp * 32 + lane], idx = a.by_page.of(key);
+      ok = (uint32_t)page < (uint32_t)a.capacity;
+      at_row = (uint32_t)page * (uint32_t)a.page_size + (uint32_t)(key - idx * a.page_size);
+      if (!ok) fault();
+    } else {
+      at_row = (uint32_t)at.row * (uint32_t)a.w + (uint32_t)(key - at.paged);
+    }
+    there = __ballot_sync(0xffffffffu, ok);
+    ringed = __ballot_sync(0xffffffffu, !paged);
   }
   // row of the tile of this lane's i-th copy, and where the copy goes
   __device__ __forceinline__ int row(int i) const { return warp * 32 + lane / kLanes * kRows + i; }
@@ -306,50 +322,43 @@ struct Copies {
     const int c = lane % kLanes;
     return (uint32_t)(c >> 3) * kBox + row(i) * 128 + (((c & 7) ^ (row(i) & 7)) << 4);
   }
-  // The first `count` of the 32 keys, in pages that are there.  A lone warp issues an instruction
-  // every few cycles, so the copies have to be most of them: where a lane's rows lie in one page
-  // there is one address.  Rows behind them become zeros if asked for (of V: a weight of 0 times
-  // what lies there must be 0; scores of keys that are not there are masked).
-  __device__ __forceinline__ void copy_paged(const TileAt& at, const int* ids, int count, bool zeros,
-                                             const bf16_t* pages, uint32_t tile) const {
-    const int r0 = row(0) - warp * 32, mine = count - r0;  // of the lane's rows
-    const int key0 = at.key0 + row(0);
-    int inside = key0 - a.by_page.of(key0) * a.page_size;
-    const bf16_t* from = pages + lane % kLanes * 8;
-    if (a.page_size % kRows == 0) {
-      if (mine > 0) from += ((size_t)ids[row(0)] * a.page_size + inside) * D;
+  // The keys that are there; what is not becomes zeros if asked for (of V: a weight of 0 times what
+  // lies there must be 0; scores of keys that are not there are masked).  A lone warp issues an
+  // instruction every few cycles, so rows are few instructions each, four at a time.
+  __device__ __forceinline__ void copy_rows(bool zeros, const bf16_t* pages, const bf16_t* ring,
+                                            uint32_t tile) const {
+    const int c = lane % kLanes * 8;
+    const bool some = ringed & there;
+    if (!some && a.page_size % kRows == 0) {  // a lane's rows lie in one page
+      const int r0 = row(0) - warp * 32;
+      const bf16_t* from = pages + (size_t)__shfl_sync(0xffffffffu, at_row, r0) * D + c;
+      const int mine = __popc(there >> r0 & ((1u << kRows) - 1));  // the first ones
 #pragma unroll
       for (int i = 0; i < kRows; ++i)
         if (i < mine) cp_async16_whole<kOnce>(tile + place(i), from + i * D, policy);
-    } else {
-#pragma unroll 4
-      for (int i = 0; i < kRows; ++i) {
-        if (i < mine)
-          cp_async16_whole<kOnce>(tile + place(i),
-                                  from + ((size_t)ids[row(i)] * a.page_size + inside) * D, policy);
-        if (++inside == a.page_size) inside = 0;
+      if (zeros && ~there) {
+#pragma unroll 1
+        for (int i = 0; i < kRows; ++i)
+          if (i >= mine)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + place(i)), "r"(0) : "memory");
       }
+      return;
     }
-    if (zeros && count < 32) {
-#pragma unroll 4
-      for (int i = 0; i < kRows; ++i)
-        if (i >= mine)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + place(i)), "r"(0) : "memory");
-    }
-  }
-  // Any keys: in pages, in the ring, or not there.
-  __device__ __forceinline__ void copy_any(const TileAt& at, const int* ids, const bf16_t* pages,
-                                           const bf16_t* ring, uint32_t tile) const {
-    const int c = lane % kLanes;
-#pragma unroll 2
-    for (int i = 0; i < kRows; ++i) {
-      const int key = at.key0 + row(i), page = ids[row(i)];
-      const bool paged = key < at.paged;
-      const bool ok = paged ? (uint32_t)page < (uint32_t)a.capacity : key < at.all;
-      const long long r = paged ? (long long)page * a.page_size + (key - a.by_page.of(key) * a.page_size)
-                                : (long long)at.row * a.w + (key - at.paged);
-      const bf16_t* src = ok ? (paged ? pages : ring) + (r * D + c * 8) : a.q;
-      cp_async16(tile + place(i), src, ok ? 16 : 0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < kRows; i0 += 2) {
+      const int r0 = row(i0) - warp * 32;
+      uint32_t r[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) r[j] = __shfl_sync(0xffffffffu, at_row, r0 + j);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bf16_t* base = some && (ringed >> (r0 + j) & 1) ? ring : pages;
+        const uint32_t to = tile + place(i0 + j);
+        if (there >> (r0 + j) & 1)
+          cp_async16_whole<kOnce>(to, base + (size_t)r[j] * D + c, policy);
+        else if (zeros)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+      }
     }
   }
   // The same 32 keys by TMA, where pages divide them or they pages: a lane a box of up to 32 rows of
@@ -369,23 +378,25 @@ struct Copies {
   // becomes 0; true if there was any.  A lane looks at the chunks that it copied.
   __device__ __forceinline__ bool clean(uint8_t* tile, int lo, int hi) const {
     bool any = false;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < kRows; ++i) {
       const int r = row(i) - warp * 32;
       if (r < lo || r >= hi) continue;
-      uint32_t* x = reinterpret_cast<uint32_t*>(tile + place(i));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t y = x[e];
-        if (not_finite(y)) y &= 0xffff0000u;
-        if (not_finite(y >> 16)) y &= 0xffffu;
-        if (y != x[e]) {
-          x[e] = y;
-          any = true;
-        }
-      }
+      const uint4 x = *reinterpret_cast<const uint4*>(tile + place(i));
+      any |= ((not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) & 0x80008000u) != 0;
     }
-    return any;
+    if (!any) return false;
+#pragma unroll 1
+    for (int i = 0; i < 4 * kRows; ++i) {
+      const int r = row(i >> 2) - warp * 32;
+      if (r < lo || r >= hi) continue;
+      uint32_t* x = reinterpret_cast<uint32_t*>(tile + place(i >> 2)) + (i & 3);
+      uint32_t y = *x;
+      if (not_finite(y)) y &= 0xffff0000u;
+      if (not_finite(y >> 16)) y &= 0xffffu;
+      *x = y;
+    }
+    return true;
   }
 };
 
@@ -586,12 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       if (dead) break;
       const TileAt at = at_s[i % kAhead];
       const int* ids = ids_s[i % kAhead];
-      const uint32_t there = __ballot_sync(0xffffffffu, copies.there(at, ids));
+      copies.resolve(at, ids);
+      const uint32_t there = copies.there;
       const int k0 = at.key0 + warp * 32;
       const int lo = max(0, min(32, at.first - k0)), hi = at.m > 1 ? max(0, min(32, at.paged - k0)) : 0;
-      // the keys there are the first ones, in pages (no ring, no bad page id); all 32
-      const int here = max(0, min(32, at.paged - k0));
-      const bool plain = there == (uint32_t)low_bits(here), whole = here == 32 && !~there;
+      const bool boxes = a.box_rows && !~(there & ~copies.ringed);
       const int s = i % kStages;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
@@ -600,14 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         if (dead) break;
         const bool search = kv && lo < hi;
         if (!kv && lane == 0) live_s[i % kLive][warp] = there;
-        if (whole && a.box_rows && !search) {
+        if (boxes && !search) {
           if (lane == 0) tc::mbar_expect_tx(full, 32 * D * 2);
           __syncwarp();
           copies.copy_boxes(at, ids, kv ? &map_v : &map_k, to, full);
         } else {
-          const bf16_t* pages = kv ? a.v_pages : a.k_pages;
-          if (plain) copies.copy_paged(at, ids, here, kv, pages, to);
-          else copies.copy_any(at, ids, pages, kv ? a.ring_v : a.ring_k, to);
+          copies.copy_rows(kv, kv ? a.v_pages : a.k_pages, kv ? a.ring_v : a.ring_k, to);
           __syncwarp();
           if (!search) {
             if (kv) tc::fence_proxy_async_smem();  // of the zeros
@@ -762,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
     const uint32_t lane_off = (uint32_t)(eq * 32) << 16;
     const float sc2 = rsqrtf((float)D) * kLog2e;
     uint32_t qv[QW];
-    int my_up = -1;       // parent of drafted token st
+    int my_up = -1;       // parent of drafted token st (or lane)
     // this thread's part of a unit's query row (zeros past the last), and its token's parent
     auto load_q = [&](const Unit& u) {
       const int x = u.mt * BM + row;
@@ -782,7 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
 #pragma unroll
         for (int c = 0; c < QW; ++c) qv[c] = 0u;
       }
-      if (a.parent && st < u.is.m) my_up = a.parent[u.is.t0 + st];
+      // with up to 32 tokens every warp has them all
+      const int token = u.is.m <= 32 ? lane : st;
+      if (a.parent && token < u.is.m) my_up = a.parent[u.is.t0 + token];
     };
     auto store_q = [&] {
       __syncwarp();
@@ -821,35 +831,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
       const int up_now = my_up;
       const Unit next = fetch(n + 1);
       if (!next.none()) load_q(next);
-      if (a.parent && u.is.m > 1 && u.tb * BN > first && sees_of != b) {
-        sees_of = b;
-        uint32_t bits[kWords];
-        int p = -1;
-        if (st < u.is.m) {
-          p = up_now;
-          if (p < -1 || p >= st) {
+      uint32_t mine_sees = 0;  // of up to 32 tokens
+      if (a.parent && u.is.m > 1 && u.tb * BN > first) {
+        if (u.is.m <= 32) {  // every warp for itself, a lane a token
+          int p = lane < u.is.m ? up_now : -1;
+          if (p < -1 || p >= lane) {
             fault();
             p = -1;
           }
-#pragma unroll
-          for (int w = 0; w < kWords; ++w) bits[w] = w == st >> 5 ? 1u << (st & 31) : 0u;
-        }
-        // after `round` rounds a token has the 2^round next ones on its way up, and `up` the one
-        // above those
-        bool more = true;
-        for (int round = 0; more && round < 9; ++round) {
-          named_sync(1, kSoftThreads);  // all have read the row of the round (or unit) before
-          if (st < u.is.m) {
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) sees[st * kWords + w] = bits[w];
-            up[st] = p;
+          uint32_t bits = 1u << lane;
+          // each round doubles the way up that a token has; p is the token above that
+          while (__any_sync(0xffffffffu, p >= 0)) {
+            const uint32_t theirs = __shfl_sync(0xffffffffu, bits, p & 31);
+            const int above = __shfl_sync(0xffffffffu, p, p & 31);
+            if (p >= 0) {
+              bits |= theirs;
+              p = above;
+            }
           }
-          __syncwarp();
-          more = tc::bar_or(2, kSoftThreads, p >= 0);
-          if (p >= 0) {
+          mine_sees = __shfl_sync(0xffffffffu, bits, i & 31);
+        } else if (sees_of != b) {
+          sees_of = b;
+          uint32_t bits[kWords];
+          int p = -1;
+          if (st < u.is.m) {
+            p = up_now;
+            if (p < -1 || p >= st) {
+              fault();
+              p = -1;
+            }
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) bits[w] |= sees[p * kWords + w];
-            p = up[p];
+            for (int w = 0; w < kWords; ++w) bits[w] = w == st >> 5 ? 1u << (st & 31) : 0u;
+          }
+          bool more = true;
+#pragma unroll 1
+          for (int round = 0; more && round < 9; ++round) {
+            named_sync(1, kSoftThreads);  // all have read the row of the round (or unit) before
+            if (st < u.is.m) {
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) sees[st * kWords + w] = bits[w];
+              up[st] = p;
+            }
+            __syncwarp();
+            more = tc::bar_or(2, kSoftThreads, p >= 0);
+            if (p >= 0) {
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) bits[w] |= sees[p * kWords + w];
+              p = up[p];
+            }
           }
         }
       }
@@ -879,6 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
         if (kb + KC > first && kb < u.is.paged) {
           const uint64_t drafts = low_bits(u.is.paged - kb) & ~low_bits(first - kb);
           const uint64_t seen = !a.parent || u.is.m == 1 ? low_bits(first + i + 1 - kb)
+                                : u.is.m <= 32 ? bits_of(mine_sees, kb - first)
                                 : mine_live ? bits_from(sees + i * kWords, kb - first) : 0ull;
           vis &= ~drafts | seen;
         }
@@ -983,7 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
 #pragma unroll 1
             for (int k = k0; k < k1; ++k) {
               const int slot = first + k;
-              const bool seen = !a.parent ? k <= i : sees[i * kWords + (k >> 5)] >> (k & 31) & 1;
+              const bool seen = !a.parent ? k <= i : u.is.m <= 32 ? mine_sees >> k & 1
+                                                    : sees[i * kWords + (k >> 5)] >> (k & 31) & 1;
               if (!seen || slot < 0) continue;
               const int idx = a.by_page.of(slot);
               const int page = a.block_table[(size_t)u.row * a.max_pages + idx];
