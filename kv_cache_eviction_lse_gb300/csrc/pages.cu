@@ -59,42 +59,56 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(
   if (!real) bad = false;
   if (bad) count = 0;
   const int base = n - m;
+  // Tokens j0 .. j0 + G - 1 of the path, a lane a token: where one comes from and goes to (rows of a
+  // pool that fits the GPU stay within 32 bits), -1 where it is in its place already.
+  uint32_t from = 0, to = 0;
+  bool moves = false;
+  auto path = [&](int j0) {
+    const int j = j0 + lane;
+    moves = false;
+    if (j >= count) return;
+    const int at = a.accept[t0 + j], before = j ? a.accept[t0 + j - 1] : -1;
+    const bool good = at > before && at < m && before >= -1;
+    const long long r = good ? pool_row(p, row, base + at) : -1, q = pool_row(p, row, base + j);
+    if (r < 0 || q < 0) bad = true;
+    from = (uint32_t)r;
+    to = (uint32_t)q;
+    moves = at != j;
+  };
   // the whole path, before anything moves
   int most = count;
   if (G < 32) most = max(most, __shfl_xor_sync(0xffffffffu, most, G));
-  for (int j0 = 0; j0 < most; j0 += G) {
-    const int j = j0 + lane;
-    if (j >= count) continue;
-    const int at = a.accept[t0 + j], before = j ? a.accept[t0 + j - 1] : -1;
-    if (at <= before || at >= m || before < -1) bad = true;
-    else if (pool_row(p, row, base + at) < 0 || pool_row(p, row, base + j) < 0) bad = true;
-  }
+  for (int j0 = 0; j0 < most; j0 += G) path(j0);
   const uint32_t any = __ballot_sync(0xffffffffu, bad);
   const uint32_t mine = G == 32 ? any : any >> (threadIdx.x & 31 & ~(G - 1)) & ((1u << (G % 32)) - 1);
   if (real && lane == 0) {
     a.seq_lens_out[row] = mine ? n : base + count;
     if (mine) fault(kErrPages);
   }
-  if (!real || mine) return;
+  if (mine) count = 0;
   uint4* pool = reinterpret_cast<uint4*>(lane < G / 2 ? p.k_pages : p.v_pages) + lane % (G / 2);
-  for (int j0 = 0; j0 < count; j0 += kAcceptAhead) {
-    uint4 x[kAcceptAhead];
-    long long to[kAcceptAhead];
-#pragma unroll
-    for (int i = 0; i < kAcceptAhead; ++i) {
-      to[i] = -1;
-      if (j0 + i >= count) continue;
-      const int at = a.accept[t0 + j0 + i];
-      if (at == j0 + i) continue;  // in its place already
-      // checked above; this holds also if another stream changes tables meanwhile
-      const long long from = pool_row(p, row, min(base + max(at, 0), n - 1));
-      to[i] = pool_row(p, row, base + j0 + i);
-      if (from < 0) to[i] = -1;
-      if (to[i] >= 0) x[i] = pool[from * (D / 8)];
+  for (int j0 = 0; j0 < most; j0 += G) {
+    if (most > G) {  // again: a longer path does not stay in the lanes
+      bad = false;
+      path(j0);
+      moves &= !bad;  // checked above; this holds also if another stream changes tables meanwhile
     }
+    if (mine) moves = false;
+    for (int i0 = 0; i0 < G && j0 + i0 < most; i0 += kAcceptAhead) {
+      uint4 x[kAcceptAhead];
+      uint32_t at[kAcceptAhead];
+      bool go[kAcceptAhead];
 #pragma unroll
-    for (int i = 0; i < kAcceptAhead; ++i)
-      if (to[i] >= 0) pool[to[i] * (D / 8)] = x[i];
+      for (int i = 0; i < kAcceptAhead; ++i) {
+        const uint32_t r = __shfl_sync(0xffffffffu, from, i0 + i, G);
+        at[i] = __shfl_sync(0xffffffffu, to, i0 + i, G);
+        go[i] = __shfl_sync(0xffffffffu, (int)moves, i0 + i, G);
+        if (go[i]) x[i] = pool[(size_t)r * (D / 8)];
+      }
+#pragma unroll
+      for (int i = 0; i < kAcceptAhead; ++i)
+        if (go[i]) pool[(size_t)at[i] * (D / 8)] = x[i];
+    }
   }
 }
 
@@ -294,22 +308,20 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(
 // ----------------------------------------------------------------------------- reclaim
 
 constexpr int kReclaimThreads = 256;
-constexpr int kMaxChunks = 2048;  // of the bits of a pool, counted in every block
+constexpr int kMaxChunks = 8192;  // of the bits of a pool, counted in every block
 
 // A bit per page that some row names, in chunks of 2^bits pages (at most kMaxChunks of them),
 // behind the head.
-struct ReclaimHead { int code, pad[3]; };
+// The head has the pages handed out so far (those that can be in use): the counter may be written
+// in place while blocks still come up.
+struct ReclaimHead { int code, next, pages, pad; };
 __host__ __device__ inline int chunk_bits(int capacity) {
-  int b = 10;
+  int b = 5;
   while (((capacity - 1) >> b) >= kMaxChunks) ++b;
   return b;
 }
 __device__ __forceinline__ uint32_t* live_words(void* ws) {
   return reinterpret_cast<uint32_t*>(static_cast<ReclaimHead*>(ws) + 1);
-}
-// Pages handed out so far: those that can be in use.
-__device__ __forceinline__ int handed_out(const PagedArgs& p, const ReclaimArgs& a) {
-  return max(0, min(a.next_page[0], p.capacity));
 }
 __device__ __forceinline__ int chunks_of(int pages, int bits) {
   return (int)(((long long)pages + (1 << bits) - 1) >> bits);
@@ -319,13 +331,14 @@ __global__ void __launch_bounds__(kReclaimThreads) reclaim_clear_kernel(
     const __grid_constant__ PagedArgs p, const __grid_constant__ ReclaimArgs a, int bits) {
   wait_for_previous();
   let_next_start();
-  const long long words = (long long)chunks_of(handed_out(p, a), bits) << (bits - 5);
+  const int next = a.next_page[0], pages = max(0, min(next, p.capacity));
+  const long long words = (long long)chunks_of(pages, bits) << (bits - 5);
   uint4* w = reinterpret_cast<uint4*>(live_words(a.ws));
-  for (long long i = (long long)blockIdx.x * kReclaimThreads + threadIdx.x; i < words / 4;
+  for (long long i = (long long)blockIdx.x * kReclaimThreads + threadIdx.x; i < (words + 3) / 4;
        i += (long long)gridDim.x * kReclaimThreads)
     w[i] = make_uint4(0, 0, 0, 0);
   if (blockIdx.x == 0 && threadIdx.x == 0)
-    static_cast<ReclaimHead*>(a.ws)->code = (uint32_t)a.next_page[0] > (uint32_t)p.capacity ? kErrPages : 0;
+    *static_cast<ReclaimHead*>(a.ws) = {(uint32_t)next > (uint32_t)p.capacity ? kErrPages : 0, next, pages, 0};
 }
 
 __global__ void __launch_bounds__(kReclaimThreads) reclaim_mark_kernel(
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(kReclaimThreads) reclaim_mark_kernel(
   const int lane = threadIdx.x & 31, warps = gridDim.x * (kReclaimThreads / 32);
   wait_for_previous();
   let_next_start();
-  const int pages = handed_out(p, a);
+  const int pages = static_cast<const ReclaimHead*>(a.ws)->pages;
   uint32_t* live = live_words(a.ws);
   bool bad = false;
   for (int row = blockIdx.x * (kReclaimThreads / 32) + (threadIdx.x >> 5); row < rows; row += warps) {
@@ -349,7 +362,8 @@ __global__ void __launch_bounds__(kReclaimThreads) reclaim_mark_kernel(
   if (bad) atomicMax(&static_cast<ReclaimHead*>(a.ws)->code, kErrPages);
 }
 
-// The bits of the live pages with the live pages before every chunk.
+// The bits of the live pages with the live pages before every chunk.  A chunk is a word, kept in
+// shared memory, until there are more than 262144 pages.
 struct Live {
   const uint32_t* words;
   const int* before;  // [chunks + 1]
@@ -373,11 +387,14 @@ struct Live {
     int left = s - (kHoles ? (lo << bits) - before[lo] : before[lo]);
     const int w0 = lo << (bits - 5), w1 = (lo + 1) << (bits - 5);
     for (int w = w0; w < w1; ++w) {
-      uint32_t x = kHoles ? ~words[w] : words[w];
+      const uint32_t x = kHoles ? ~words[w] : words[w];
       const int n = __popc(x);
       if (left >= n) { left -= n; continue; }
-      for (; left > 0; --left) x &= x - 1;
-      return w * 32 + __ffs(x) - 1;
+      int at = 0;  // the last bit with at most `left` below it that is set
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+        if (__popc(x & ((1u << (at + o)) - 1)) <= left) at += o;
+      return w * 32 + at;
     }
     return -1;  // not reached while the bits hold still
   }
@@ -385,21 +402,22 @@ struct Live {
 
 // Live pages from n_live on go to the holes below it, in order of their ids: as few pages move
 // as can, sources and targets are apart, and a page's new id is a matter of two ranks.  Every
-// block counts the bits for itself (64 thousand pages: 8 KB).
+// block counts the bits for itself (64 thousand pages: 8 KB).  A warp takes up to 32 moves, whose
+// pages its lanes look up at once.
 __global__ void __launch_bounds__(kReclaimThreads) reclaim_kernel(
     const __grid_constant__ PagedArgs p, const __grid_constant__ ReclaimArgs a, int rows, int bits) {
-  __shared__ int before[kMaxChunks + 1];
+  extern __shared__ int before[];  // [chunks + 1], and the words of one-word chunks
   __shared__ int warp_sum[kReclaimThreads / 32];
   constexpr int kWarps = kReclaimThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gw = blockIdx.x * kWarps + warp, warps = gridDim.x * kWarps;
   wait_for_previous();
-  const int pages = handed_out(p, a), chunks = chunks_of(pages, bits);
+  const ReclaimHead head = *static_cast<const ReclaimHead*>(a.ws);
+  const int pages = head.pages, chunks = chunks_of(pages, bits), code = head.code;
   const uint32_t* words = live_words(a.ws);
-  const int code = static_cast<const ReclaimHead*>(a.ws)->code;
   if (code) {  // everything as it was
     if (blockIdx.x == 0 && tid == 0) {
-      a.next_page_out[0] = a.next_page[0];
+      a.next_page_out[0] = head.next;
       fault(code);
     }
     if (a.block_table_out != p.block_table) {
@@ -410,38 +428,50 @@ __global__ void __launch_bounds__(kReclaimThreads) reclaim_kernel(
     }
     return;
   }
-  // live pages of each chunk, then of those before it
-  for (int c = warp; c < chunks; c += kWarps) {
-    int n = 0;
-    for (int w = lane; w < 1 << (bits - 5); w += 32) n += __popc(words[(c << (bits - 5)) + w]);
-    n = warp_sum_int(n);
-    if (lane == 0) before[c + 1] = n;
+  // live pages of each chunk, then of those before it, for a run of chunks a thread
+  uint32_t* copy = reinterpret_cast<uint32_t*>(before) + chunks + 1;
+  if (bits == 5) {
+    for (int c = tid; c < chunks; c += kReclaimThreads) {
+      const uint32_t x = words[c];
+      copy[c] = x;
+      before[c] = __popc(x);
+    }
+    words = copy;
+  } else {
+    for (int c = warp; c < chunks; c += kWarps) {
+      int n = 0;
+      for (int w = lane; w < 1 << (bits - 5); w += 32) n += __popc(words[(c << (bits - 5)) + w]);
+      n = warp_sum_int(n);
+      if (lane == 0) before[c] = n;
+    }
   }
-  if (tid == 0) before[0] = 0;
   __syncthreads();
-  int carry = 0;
-  for (int c0 = 0; c0 < chunks; c0 += kReclaimThreads) {
-    const int c = c0 + tid;
-    int incl = c < chunks ? before[c + 1] : 0;
+  const int run = (chunks + kReclaimThreads - 1) / kReclaimThreads;
+  const int c0 = min(tid * run, chunks), c1 = min(c0 + run, chunks);
+  int mine = 0;
+  for (int c = c0; c < c1; ++c) mine += before[c];
+  int incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) incl += warp_sum[w];
-      all += warp_sum[w];
-    }
-    if (c < chunks) before[c + 1] = carry + incl;
-    carry += all;
-    __syncthreads();
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int n_live = 0, earlier = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) earlier += warp_sum[w];
+    n_live += warp_sum[w];
+  }
+  for (int c = c0; c < c1; ++c) {
+    const int n = before[c];
+    before[c] = earlier;
+    earlier += n;
+  }
+  if (tid == 0) before[chunks] = n_live;
+  __syncthreads();
   const Live live{words, before, bits, chunks};
-  const int n_live = carry;
   const int below = n_live < pages ? live.rank(n_live) : n_live;  // live pages that stay
   const int moving = n_live - below;
   if (blockIdx.x == 0 && tid == 0) a.next_page_out[0] = n_live;
@@ -450,26 +480,38 @@ __global__ void __launch_bounds__(kReclaimThreads) reclaim_kernel(
   const int pieces = (chunks16 + 255) / 256;
   uint4* k = reinterpret_cast<uint4*>(p.k_pages);
   uint4* v = reinterpret_cast<uint4*>(p.v_pages);
-  for (long long i = gw; i < (long long)moving * pieces; i += warps) {
-    const int s = (int)(i / pieces), c0 = (int)(i - (long long)s * pieces) * 256 + lane;
-    const int from = live.select<false>(below + s), to = live.select<true>(s);
-    if (from < n_live || from >= pages || (uint32_t)to >= (uint32_t)n_live) continue;
-    const size_t src_at = (size_t)from * chunks16, dst_at = (size_t)to * chunks16;
-    uint4 x[8], y[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int c = c0 + u * 32;
-      if (c < chunks16) {
-        x[u] = k[src_at + c];
-        y[u] = v[src_at + c];
-      }
+  const long long moves = (long long)moving * pieces;
+  const int per = (int)max(1ll, min(32ll, (moves + warps - 1) / warps));
+  for (long long i0 = (long long)gw * per; i0 < moves; i0 += (long long)warps * per) {
+    const int count = (int)min((long long)per, moves - i0);
+    int from_of = -1, to_of = -1, part_of = 0;
+    if (lane < count) {
+      const int s = (int)((i0 + lane) / pieces);
+      part_of = (int)(i0 + lane - (long long)s * pieces);
+      from_of = live.select<false>(below + s);
+      to_of = live.select<true>(s);
     }
+    for (int i = 0; i < count; ++i) {
+      const int from = __shfl_sync(0xffffffffu, from_of, i), to = __shfl_sync(0xffffffffu, to_of, i);
+      const int first = __shfl_sync(0xffffffffu, part_of, i) * 256 + lane;
+      if (from < n_live || from >= pages || (uint32_t)to >= (uint32_t)n_live) continue;
+      const size_t src_at = (size_t)from * chunks16, dst_at = (size_t)to * chunks16;
+      uint4 x[8], y[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int c = c0 + u * 32;
-      if (c < chunks16) {
-        k[dst_at + c] = x[u];
-        v[dst_at + c] = y[u];
+      for (int u = 0; u < 8; ++u) {
+        const int c = first + u * 32;
+        if (c < chunks16) {
+          x[u] = k[src_at + c];
+          y[u] = v[src_at + c];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int c = first + u * 32;
+        if (c < chunks16) {
+          k[dst_at + c] = x[u];
+          v[dst_at + c] = y[u];
+        }
       }
     }
   }
@@ -496,7 +538,7 @@ size_t fork_workspace_bytes(int rows) {
 size_t reclaim_workspace_bytes(int capacity) {
   const int b = chunk_bits(capacity > 0 ? capacity : 1);
   const size_t chunks = ((size_t)capacity + ((size_t)1 << b) - 1) >> b;
-  return sizeof(ReclaimHead) + (chunks << (b - 3));
+  return sizeof(ReclaimHead) + ((chunks << (b - 3)) + 15) / 16 * 16;
 }
 
 cudaError_t launch_accept(const PagedArgs& p, const AcceptArgs& a, cudaStream_t s) {
@@ -538,6 +580,13 @@ cudaError_t launch_reclaim(const PagedArgs& p, const ReclaimArgs& a, cudaStream_
   e = cudaLaunchKernelEx(&m.cfg, reclaim_mark_kernel, p, a, rows);
   if (e != cudaSuccess) return e;
   Launch r(dim3(152 * 3), kReclaimThreads, s);
+  const int chunks = ((p.capacity - 1) >> bits) + 1;
+  r.cfg.dynamicSmemBytes = (chunks + 1 + (bits == 5 ? chunks : 0)) * sizeof(int);
+  if (r.cfg.dynamicSmemBytes > 48 * 1024) {
+    e = cudaFuncSetAttribute(reclaim_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)r.cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
+  }
   return cudaLaunchKernelEx(&r.cfg, reclaim_kernel, p, a, rows, bits);
 }
 
