@@ -63,9 +63,22 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(
   // pool that fits the GPU stay within 32 bits), -1 where it is in its place already.
   uint32_t from = 0, to = 0;
   bool moves = false;
+  int longest = m;
+  if (G < 32) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, G));
+  const bool few = longest <= G;
   auto path = [&](int j0) {
     const int j = j0 + lane;
     moves = false;
+    if (few) {  // the rows of all drafted tokens are asked for beside the path
+      const int at = j < count ? a.accept[t0 + j] : -1, before = __shfl_up_sync(0xffffffffu, at, 1, G);
+      const long long mine = j < m && !bad ? pool_row(p, row, base + j) : -1;
+      to = (uint32_t)mine;
+      from = __shfl_sync(0xffffffffu, to, at & (G - 1), G);
+      const bool there = __shfl_sync(0xffffffffu, (int)(mine >= 0), at & (G - 1), G);
+      if (j < count && (at >= m || at <= (j ? before : -1) || !there || mine < 0)) bad = true;
+      moves = j < count && at != j;
+      return;
+    }
     if (j >= count) return;
     const int at = a.accept[t0 + j], before = j ? a.accept[t0 + j - 1] : -1;
     const bool good = at > before && at < m && before >= -1;
@@ -579,7 +592,7 @@ cudaError_t launch_reclaim(const PagedArgs& p, const ReclaimArgs& a, cudaStream_
   Launch m(dim3(mark < 152 * 8 ? mark : 152 * 8), kReclaimThreads, s);
   e = cudaLaunchKernelEx(&m.cfg, reclaim_mark_kernel, p, a, rows);
   if (e != cudaSuccess) return e;
-  Launch r(dim3(152 * 3), kReclaimThreads, s);
+  Launch r(dim3(152 * 2), kReclaimThreads, s);
   const int chunks = ((p.capacity - 1) >> bits) + 1;
   r.cfg.dynamicSmemBytes = (chunks + 1 + (bits == 5 ? chunks : 0)) * sizeof(int);
   if (r.cfg.dynamicSmemBytes > 48 * 1024) {
