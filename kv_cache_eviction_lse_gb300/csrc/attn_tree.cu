@@ -899,11 +899,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
 #pragma unroll
         for (int c = 0; c < KC; c += 32)
           tc::tmem_ld32(tmem + lane_off + (uint32_t)(s * BN + h * KC + c), v + c);
-        tc::tmem_ld_wait();
-        // of the thread's 64 keys: those there are, without drafted ones that are not seen
+        // while they come: of the thread's 64 keys those there are, without drafted ones not seen
         uint64_t vis = (uint64_t)live_s[gs % kLive][2 * h + 1] << 32 | live_s[gs % kLive][2 * h];
-        tc::fence_before_sync();
-        tc::mbar_arrive(bar_sempty(s));  // the next S into this buffer may start now
         const int kb = j * BN + h * KC;
         if (kb + KC > first && kb < u.is.paged) {
           const uint64_t drafts = low_bits(u.is.paged - kb) & ~low_bits(first - kb);
@@ -912,7 +909,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
                                 : mine_live ? bits_from(sees + i * kWords, kb - first) : 0ull;
           vis &= ~drafts | seen;
         }
-        if (__any_sync(0xffffffffu, ~vis != 0)) {
+        const bool masked = __any_sync(0xffffffffu, ~vis != 0);
+        tc::tmem_ld_wait();
+        tc::fence_before_sync();
+        tc::mbar_arrive(bar_sempty(s));  // the next S into this buffer may start now
+        if (masked) {
           asm volatile("");  // a branch: most tiles have nothing to mask
           const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
 #pragma unroll
