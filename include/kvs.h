@@ -572,6 +572,8 @@ kvs_status kvs_attn_decode(const kvs_dims* dims, int32_t B, const kvs_bf16* q, i
  * word (10).
  *
  *   max_draft 1 .. 256: no sequence has more drafted tokens
+ *   (tiles of 128 query rows, at most max_draft * H_q / H_kv of them a row) x (tiles of 128 keys, at
+ *   most max_pages * page_size + w of them a row), over all rows (l, hk, b), stay below 2^31
  *   tok_start [B + 1] int32;  parent [N] int32, or NULL: token i follows token i - 1
  *   q, o   [L][H_q][N][d] bf16;  lse [L][H_q][N] fp32 output, or NULL
  *   k_pages, v_pages [capacity_pages][page_size][d] bf16 (not used with no pages)

@@ -850,6 +850,12 @@ kvs_status kvs_attn_tree(const kvs_dims* dims, int32_t B, int32_t N, int32_t max
           "kvs_attn_tree: too many rows");
   REQUIRE((int64_t)max_pages * page_size + w < INT32_MAX - 65536, KVS_ERR_UNSUPPORTED,
           "kvs_attn_tree: max_pages * page_size + w of a row above 2^31");
+  {  // key tiles of all rows and query tiles: the kernel counts them in 32 bits
+    const int64_t g = dims->H_q / dims->H_kv, keys = ((int64_t)max_pages * page_size + w + 127) / 128;
+    const int64_t each = (max_draft * g + 127) / 128 * B, all = N * g / 128 + B;
+    REQUIRE((double)dims->L * dims->H_kv * (double)(each < all ? each : all) * (double)keys < INT32_MAX,
+            KVS_ERR_UNSUPPORTED, "kvs_attn_tree: 2^31 tiles of 128 keys x 128 query rows or more");
+  }
   if (B == 0 || N == 0) return ok();
   REQUIRE_PTR(tok_start);
   REQUIRE_OPT_PTR(parent);

@@ -70,6 +70,14 @@ def test_tree_refusals(C):
         assert tree(C, md=md) == C.KVS_ERR_UNSUPPORTED
     assert tree(C, up=FAKE + 4) == C.KVS_ERR_ALIGN and tree(C, lse=FAKE + 8) == C.KVS_ERR_ALIGN
     assert tree(C, mp=1 << 27) == C.KVS_ERR_UNSUPPORTED
+    # tiles of all rows: 64 x 8 x 128 KV heads' rows, 8 query tiles each, keys for 2^22 / 128 tiles
+    deep = C.dims(64, 64, 8, 128)
+    big = dict(B=128, N=128 * 128, md=128, mp=1 << 18)
+    assert tree(C, deep, **big) == C.KVS_ERR_UNSUPPORTED and b"tiles" in C._lib.kvs_last_error()
+    # few drafted tokens in all, so a query tile a row (no workspace either way): 2^31 tiles with
+    # ((2^18 - 8) * 16 + 3 + 127) / 128 = 2^15 of keys, 2^31 - 2^16 with one less
+    assert tree(C, deep, B=128, N=15, md=128, mp=(1 << 18) - 8, wsb=0) == C.KVS_ERR_UNSUPPORTED
+    assert tree(C, deep, B=128, N=15, md=128, mp=(1 << 18) - 16, wsb=0) == C.KVS_ERR_CAPACITY
     for d in (64, 128):
         need = C.kvs_attn_tree_workspace_size(C.dims(1, 4, 2, d), 2, 6)
         assert need > 0 and tree(C, C.dims(1, 4, 2, d), wsb=need - 1) == C.KVS_ERR_CAPACITY
