@@ -342,9 +342,10 @@ def test_reclaim_refused_on_the_device(C):
     check(lambda c: put(c, "nxt", 0, c["cap"] + 1))
 
 
-def test_reclaim_of_a_pool_of_millions_of_pages(C):
-    """More pages than 2048 chunks of 1024: rows name the last of them and move to the front."""
-    cap, B, ps, d = 2_200_000, 64, 1, 64
+@pytest.mark.parametrize("cap", [250_000, 2_200_000])  # a word a chunk, 60 KB of them; more words a chunk
+def test_reclaim_of_a_large_pool(C, cap):
+    """Rows name the last of the pages and move to the front."""
+    B, ps, d = 64, 1, 64
     dm = C.dims(1, 1, 1, d)
     kp = torch.zeros(cap, ps, d, dtype=torch.bfloat16, device="cuda")
     ids = torch.cat([torch.tensor([0, 5, 31, 32, 1024]), torch.arange(cap - 59, cap)]).int()
