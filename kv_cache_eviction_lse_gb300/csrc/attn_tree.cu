@@ -13,16 +13,26 @@
 // equal contiguous share, and a pair that crosses a share's border is joined from partial sums
 // (running maximum, sum and weighted values) by a second kernel.  Shares depend on the lengths
 // alone, so results do too.  In a block:
-//   warps 0-3   copy K and V tiles by 16-byte cp.async into two 3-stage rings, in the 128-byte
-//               swizzled layout that the tensor core reads; pages may be of any size and end
-//               anywhere in a tile, which a TMA box could not
+//   warps 0-3   copy 32 keys each of every K and V tile into two 3-stage rings, in the 128-byte
+//               swizzled layout that the tensor core reads: whole runs of keys in pages that 32 keys
+//               divide or are divided by come as TMA boxes, all others by 16-byte cp.async (pages may
+//               be of any size and end anywhere in a tile, and so may the ring begin)
 //   warps 4-11  softmax, two threads per query row: S from TMEM, p = 2^(x - m), P as bf16 to TMEM
 //   warps 12, 14  issue S = Q K^T (Q in TMEM) and O += P V (P in TMEM), M = 128 each; one warp for
 //               both spent its time issuing (1.2 us a tile)
-//   warp 13     brings the page ids of the tiles to come, six tiles ahead (under a saturated HBM a
-//               load takes longer than a tile)
-// The registers of a block go to the softmax (setmaxnreg: 192 a thread, 80 for the copies, 48 for the rest).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax of the
-// one before.  O is rescaled only when a row's maximum grows by more than 2^8.
+//   warp 13     finds the share's units and brings the page ids of the tiles to come, six tiles ahead
+//               (under a saturated HBM a load takes longer than a tile)
+// The registers of a block go to the softmax (setmaxnreg: 192 a thread, 80 for the copies, 48 for
+// the rest).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax
+// of the one before.  O is rescaled only when a row's maximum grows by more than 2^8.
+//
+// Measured, a call in a graph: 8 drafts of one short sequence 12.3 us, 64 sequences of up to 2048
+// tokens 52 (floor 30), a document of 131072 tokens with 64 drafts 59 (22), wide trees at d = 64
+// 246 (63), 96 sequences of 16384 tokens 372 (362: 6.6 TB/s).  A tile with all 128 rows takes 2100
+// cycles: the softmax of two warps an SM quarter 1400, a wait that is over 180, P to TMEM 220, on to
+// the next tile 330; the tensor pipe is 22 % and the issue slots are 53 % busy.  P in two buffers
+// (at d = 128 in the place of S) changed that little, 262 for 246 and 50 for 52; scores read a tile
+// ahead cost 275 for 249, K and V copied by two warps each 259 and 62 for 246 and 52.
 //
 // Which drafted tokens a token sees is a row of 256 bits, closed over the parents in log2(depth)
 // rounds at the start of a (row, query tile) whose share reaches the drafted keys.  A masked key
@@ -421,7 +431,8 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
 }
 
 // The code is kept small: at 120 KB (a walk through the rows in every warp, a copy loop per case)
-// the warps waited for instructions a third of the time, 1.4 us a tile.
+// the warps waited for instructions a third of the time, 1.4 us a tile; now, at 79 to 85 KB, a
+// sixteenth at d = 64 and a twelfth at 128.
 template <int D, bool kOnce>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
     const __grid_constant__ AttnTreeArgs a, const __grid_constant__ CUtensorMap map_k,
