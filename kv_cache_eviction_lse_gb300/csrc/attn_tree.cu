@@ -22,12 +22,12 @@
 //               both spent its time issuing (1.2 us a tile)
 //   warp 13     finds the share's units and brings the page ids of the tiles to come, six tiles ahead
 //               (under a saturated HBM a load takes longer than a tile)
-// The registers of a block go to the softmax (setmaxnreg: 192 a thread, 80 for the copies, 48 for
-// the rest).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax
+// The registers of a block go to the softmax (setmaxnreg: 184 a thread, 96 for the copies, 48 for
+// the rest: less spills in either).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax
 // of the one before.  O is rescaled only when a row's maximum grows by more than 2^8.
 //
-// Measured, a call in a graph: 8 drafts of one short sequence 12.3 us, 64 sequences of up to 2048
-// tokens 52 (floor 30), a document of 131072 tokens with 64 drafts 59 (22), wide trees at d = 64
+// Measured, a call in a graph: 8 drafts of one short sequence 12.2 us, 64 sequences of up to 2048
+// tokens 52 (floor 30), 33 with rings and pages of 13 20.7 (5), a document of 131072 tokens with 64 drafts 59 (22), wide trees at d = 64
 // 246 (63), 96 sequences of 16384 tokens 372 (362: 6.6 TB/s).  A tile with all 128 rows takes 2100
 // cycles: the softmax of two warps an SM quarter 1400, a wait that is over 180, P to TMEM 220, on to
 // the next tile 330; the tensor pipe is 22 % and the issue slots are 53 % busy.  P in two buffers
@@ -67,7 +67,7 @@ constexpr int KC = BN / 2;     // keys of a softmax thread and tile
 constexpr int kAhead = 8;      // tiles whose page ids are on their way or not yet used
 constexpr uint32_t kBox = 128 * 128;  // 128 rows x 64 bf16 (one 128-byte swizzle span)
 constexpr uint32_t kTmemCols = 512;
-constexpr int kCopyRegs = 80, kSoftRegs = 192, kMmaRegs = 48;
+constexpr int kCopyRegs = 96, kSoftRegs = 184, kMmaRegs = 48;
 static_assert(kCopyRegs + 2 * kSoftRegs + kMmaRegs <= 65536 / 128, "what the launch has");
 constexpr float kRescale = 8.f;  // log2 growth of the row max that forces a rescale of O
 constexpr int kMaxBlocks = 160;  // of the persistent grid; sizes the workspace
@@ -334,18 +334,22 @@ struct Copies {
   }
   // The keys that are there; what is not becomes zeros if asked for (of V: a weight of 0 times what
   // lies there must be 0; scores of keys that are not there are masked).  A lone warp issues an
-  // instruction every few cycles, so rows are few instructions each, four at a time.
+  // instruction every few cycles, so a row is few of them: in a loop that chooses between page and
+  // ring row by row, 32 keys took 2400 cycles (33 rings and pages of 13: 24.4 us for 20.7).
   __device__ __forceinline__ void copy_rows(bool zeros, const bf16_t* pages, const bf16_t* ring,
                                             uint32_t tile) const {
     const int c = lane % kLanes * 8;
-    const bool some = ringed & there;
-    if (!some && a.page_size % kRows == 0) {  // a lane's rows lie in one page
+    const uint32_t in_ring = there & ringed;
+    // the first keys, all in pages or all in the ring: nothing to choose in a row
+    if (!(there & (there + 1)) && (!in_ring || in_ring == there)) {
       const int r0 = row(0) - warp * 32;
-      const bf16_t* from = pages + (size_t)__shfl_sync(0xffffffffu, at_row, r0) * D + c;
-      const int mine = __popc(there >> r0 & ((1u << kRows) - 1));  // the first ones
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        if (i < mine) cp_async16_whole<kOnce>(tile + place(i), from + i * D, policy);
+      const bf16_t* from = (in_ring ? ring : pages) + c;
+      const int mine = __popc(there >> r0 & ((1u << kRows) - 1));
+#pragma unroll 
+      for (int i = 0; i < kRows; ++i) {
+        const uint32_t r = __shfl_sync(0xffffffffu, at_row, r0 + i);
+        if (i < mine) cp_async16_whole<kOnce>(tile + place(i), from + (size_t)r * D, policy);
+      }
       if (zeros && ~there) {
 #pragma unroll 1
         for (int i = 0; i < kRows; ++i)
@@ -362,7 +366,7 @@ struct Copies {
       for (int j = 0; j < 2; ++j) r[j] = __shfl_sync(0xffffffffu, at_row, r0 + j);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const bf16_t* base = some && (ringed >> (r0 + j) & 1) ? ring : pages;
+        const bf16_t* base = ringed >> (r0 + j) & 1 ? ring : pages;
         const uint32_t to = tile + place(i0 + j);
         if (there >> (r0 + j) & 1)
           cp_async16_whole<kOnce>(to, base + (size_t)r[j] * D + c, policy);
@@ -431,7 +435,7 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
 }
 
 // The code is kept small: at 120 KB (a walk through the rows in every warp, a copy loop per case)
-// the warps waited for instructions a third of the time, 1.4 us a tile; now, at 79 to 85 KB, a
+// the warps waited for instructions a third of the time, 1.4 us a tile; now, at 80 to 89 KB, a
 // sixteenth at d = 64 and a twelfth at 128.
 template <int D, bool kOnce>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(
