@@ -7,7 +7,7 @@ import torch
 
 from oracle.drafts_oracle import way_up
 from .gpu_util import need_gpu
-from .test_gpu_tree import check, tree
+from .test_gpu_tree import call, case, check, tree
 
 pytestmark = pytest.mark.gpu
 
@@ -225,3 +225,48 @@ def test_a_captured_step_is_the_eager_one(C):
         b.same()
         for x, y in ((a.o, b.o), (a.lse, b.lse), (a.bt, b.bt), (a.sl, b.sl), (a.nxt, b.nxt)):
             assert torch.equal(x.cpu(), y.cpu())
+
+
+@pytest.mark.parametrize("ps", [16, 13])
+def test_a_pool_of_more_than_32_bit_offsets(C, ps):
+    """The last pages of a pool of 2^32 elements and more hold what a small pool holds: the same results, and
+    pages given back move from there to the front."""
+    c = case(5, L=2, Hq=8, H=2, B=3, d=128, ps=ps, n=300, m=(8, 1, 20))
+    small = call(C, c)
+    cap = 2 ** 32 // (ps * 128) + c["cap"] + 7
+    far = cap - c["cap"]
+    dm, B, N = C.dims(2, 8, 2, 128), 3, c["N"]
+    kp, vp = (torch.empty(cap, ps, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kp[far:], vp[far:] = small["kp"], small["vp"]
+    bt = small["bt"] + far
+    o, lse = torch.full_like(small["o"], 7.0), torch.full_like(small["lse"], 7.0)
+    nb = max(C.kvs_attn_tree_workspace_size(dm, B, N), C.kvs_reclaim_paged_workspace_size(dm, B, cap))
+    ws = torch.full((nb,), 255, dtype=torch.uint8, device="cuda")
+    C.kvs_attn_tree(dm, B, N, c["md"], small["ts"], small["parent"], small["q"], ps, kp, vp, cap, bt, c["mp"],
+                    small["sl"], 0, None, None, None, o, lse, ws, nb)
+    torch.cuda.synchronize()
+    assert C.kvs_device_error() == 0
+    assert torch.equal(o, small["o"]) and torch.equal(lse, small["lse"])
+    ts, i32 = c["ts"], lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    path = np.zeros(N, dtype=np.int32)
+    for b, p in enumerate(([1, 4, 7], [0], [0, 3, 9, 19])):
+        path[ts[b]:ts[b] + len(p)] = p
+    count, path, sl = i32([3, 1, 4]), i32(path.tolist()), small["sl"].clone()
+    C.kvs_accept_paged(dm, B, N, small["ts"], count, path, ps, small["kp"], small["vp"], c["cap"], small["bt"],
+                       c["mp"], small["sl"], small["sl"])
+    C.kvs_accept_paged(dm, B, N, small["ts"], count, path, ps, kp, vp, cap, bt, c["mp"], sl, sl)
+    nxt = i32([cap])
+    C.kvs_reclaim_paged(dm, B, ps, kp, vp, cap, nxt, nxt, bt, bt, c["mp"], sl, ws, nb)
+    torch.cuda.synchronize()
+    assert C.kvs_device_error() == 0 and torch.equal(sl, small["sl"])
+    lens, near = sl.cpu().numpy(), small["bt"].cpu().numpy()
+    used = 0
+    for r in np.ndindex(*lens.shape):
+        n = -(-int(lens[r]) // ps)
+        ids, was = bt[r][:n].long(), torch.from_numpy(near[r][:n]).long().cuda()
+        assert int(ids.max()) < int(nxt)
+        for new, old in ((kp, small["kp"]), (vp, small["vp"])):
+            a, b = new[ids].reshape(-1, 128)[:lens[r]], old[was].reshape(-1, 128)[:lens[r]]
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+        used += n
+    assert int(nxt) == used
