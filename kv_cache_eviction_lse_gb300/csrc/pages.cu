@@ -5,7 +5,7 @@
 //
 // Bound by latency (a chain of dependent loads: lengths -> table -> rows) until thousands of
 // rows move at once, then by HBM.  Measured, a call in a graph (floor): paths of four users' drafts
-// over 36 layers 2.7 us (0.4), of 64 users 15.5 (6.9); 3 forks of one sequence 7.0 (0.2), 31 forks
+// over 36 layers 2.6 us (0.4), of 64 users 14.8 (6.9); 3 forks of one sequence 7.0 (0.2), 31 forks
 // with rings 42 (42); pages given back with few to move 9.7 (0.6), with a third gone 28.5 (15.8).
 #include "common.cuh"
 #include "launch.cuh"
@@ -37,8 +37,10 @@ __device__ __forceinline__ long long pool_row(const PagedArgs& p, int row, int s
 
 // ----------------------------------------------------------------------------- accept
 
-constexpr int kAcceptThreads = 128;
-constexpr int kAcceptAhead = 8;  // tokens whose chunks are loaded before the first is stored
+// Tokens whose chunks are loaded before the first is stored: 16 in blocks of two warps, 64 users'
+// drafts 14.8 us; 8 in blocks of four 15.5 (16 in blocks of four 15.6).
+constexpr int kAcceptThreads = 64;
+constexpr int kAcceptAhead = 16;
 
 // A group of D / 4 lanes takes a row; a lane owns one 16-byte column of K or V and walks
 // through the accepted tokens in order.  Token j moves from slot base + accept[j] to base + j,
@@ -48,6 +50,7 @@ template <int D>
 __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(
     const __grid_constant__ PagedArgs p, const __grid_constant__ AcceptArgs a, int rows) {
   constexpr int G = D / 4;  // lanes of a row: D / 8 columns each of K and V
+  static_assert(G % kAcceptAhead == 0, "lanes hold the tokens of a round");
   const int lane = threadIdx.x % G;
   const int row = blockIdx.x * (kAcceptThreads / G) + threadIdx.x / G;
   wait_for_previous();
