@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(
   const int t0 = a.tok_start[b], t1 = a.tok_start[b + 1];
   const int n = real ? p.seq_lens[row] : 0;
   int count = real ? a.n_accept[b] : 0;
-  const int m = t1 - t0;
+  const int m = real ? t1 - t0 : 0;  // a row that is not there has no slots to look up
   bool bad = t0 < 0 || t1 < t0 || t1 > a.N || count < 0 || count > m || n < m || n > room_of(p);
   if (!real) bad = false;
   if (bad) count = 0;
