@@ -23,7 +23,7 @@
 //   warp 13     finds the share's units and brings the page ids of the tiles to come, six tiles ahead
 //               (under a saturated HBM a load takes longer than a tile)
 // The registers of a block go to the softmax (setmaxnreg: 184 a thread, 96 for the copies, 48 for
-// the rest: less spills in either).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax
+// the rest: with fewer the copies or the rest spill, which costs up to 10 us in 52).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax
 // of the one before.  O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // Measured, a call in a graph: 8 drafts of one short sequence 12.2 us, 64 sequences of up to 2048
