@@ -23,16 +23,18 @@
 //   warp 13     finds the share's units and brings the page ids of the tiles to come, six tiles ahead
 //               (under a saturated HBM a load takes longer than a tile)
 // The registers of a block go to the softmax (setmaxnreg: 184 a thread, 96 for the copies, 48 for
-// the rest: with fewer the copies or the rest spill, which costs up to 10 us in 52).  S is double-buffered in TMEM, so that the products of one tile run beside the softmax
-// of the one before.  O is rescaled only when a row's maximum grows by more than 2^8.
+// the rest: with fewer the copies or the rest spill, which costs up to 10 us in 52).  S is
+// double-buffered in TMEM, so that the products of one tile run beside the softmax of the one
+// before.  O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // Measured, a call in a graph: 8 drafts of one short sequence 12.2 us, 64 sequences of up to 2048
-// tokens 52 (floor 30), 33 with rings and pages of 13 20.7 (5), a document of 131072 tokens with 64 drafts 59 (22), wide trees at d = 64
-// 246 (63), 96 sequences of 16384 tokens 372 (362: 6.6 TB/s).  A tile with all 128 rows takes 2100
-// cycles: the softmax of two warps an SM quarter 1400, a wait that is over 180, P to TMEM 220, on to
-// the next tile 330; the tensor pipe is 22 % and the issue slots are 53 % busy.  P in two buffers
-// (at d = 128 in the place of S) changed that little, 262 for 246 and 50 for 52; scores read a tile
-// ahead cost 275 for 249, K and V copied by two warps each 259 and 62 for 246 and 52.
+// tokens 52 (floor 30), 33 with rings and pages of 13 20.7 (5), a document of 131072 tokens with 64
+// drafts 59 (22), wide trees at d = 64 246 (63), 96 sequences of 16384 tokens 372 (362: 6.6 TB/s).
+// A tile with all 128 rows takes 2100 cycles: the softmax of two warps an SM quarter 1400, a wait
+// that is over 180, P to TMEM 220, on to the next tile 330; the tensor pipe is 22 % and the issue
+// slots are 53 % busy.  P in two buffers (at d = 128 in the place of S) changed that little, 262
+// for 246 and 50 for 52; scores read a tile ahead cost 275 for 249, K and V copied by two warps
+// each 259 and 62 for 246 and 52.
 //
 // Which drafted tokens a token sees is a row of 256 bits, closed over the parents in log2(depth)
 // rounds at the start of a (row, query tile) whose share reaches the drafted keys.  A masked key
