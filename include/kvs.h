@@ -367,7 +367,9 @@ kvs_status kvs_value_refit(const kvs_dims* dims, const kvs_bf16* q, int32_t n_q,
  * block_table[r][seq_lens[r] / page_size] and zero-fills it.  If the pool
  * (capacity_pages) or the row's block table (max_pages) is full the token is not
  * appended and the device error word is set (kvs_device_error: 4 = pool full,
- * 5 = block table full).  With advance_pos != 0, pos[b] += 1 after the step.
+ * 5 = block table full); a full pool leaves next_page at capacity_pages, whatever was asked
+ * for, so that kvs_reclaim_paged can give pages back.  With advance_pos != 0, pos[b] += 1
+ * after the step.
  *
  *   pos          [B]                     int32 (device; read, advanced if asked)
  *   new_score    [L][H_kv][B]            fp32  score of the arriving token

@@ -65,7 +65,12 @@ __global__ void __launch_bounds__(256) decode_step_kernel(const DecodeArgs a) {
         if (lane == 0) pg = atomicAdd(a.next_page, 1);
         pg = __shfl_sync(0xffffffffu, pg, 0);
         if (pg >= a.capacity) {
-          if (lane == 0) atomicCAS(&g_decode_error, 0, kErrPoolFull);
+          if (lane == 0) {
+            // back to the pool's end: whoever failed does so after its own add, so that the counter
+            // stands there once all have, and stays one that kvs_reclaim_paged takes
+            atomicMin(a.next_page, a.capacity);
+            atomicCAS(&g_decode_error, 0, kErrPoolFull);
+          }
           pg = -1;
         } else {
           if (lane == 0) a.block_table[(size_t)row * a.max_pages + pi] = pg;

@@ -1,0 +1,92 @@
+"""Edges of the calls that move pages: pools that a decode step has filled."""
+import numpy as np
+import pytest
+import torch
+
+from .gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def C():
+    need_gpu()
+    from kv_cache_eviction_lse_gb300 import build
+    build.build()
+    from kv_cache_eviction_lse_gb300 import capi
+    return capi
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def bytes_of(n):
+    return torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")
+
+
+# ----------------------------------------------------------------------------- full pools
+
+class Decode:
+    """A cache without a ring that kvs_decode_step fills: every token is kept, and its keys hold
+    the step that brought it."""
+
+    def __init__(self, C, L, H, B, ps, cap, mp=8, d=64):
+        self.C, self.dm, self.shape, self.ps, self.cap, self.mp, self.d = C, C.dims(L, H, H, d), (L, H, B), ps, cap, mp, d
+        self.kp = torch.zeros(cap, ps, d, dtype=torch.bfloat16, device="cuda")
+        self.vp = torch.zeros_like(self.kp)
+        self.nxt, self.pos = i32([0]), torch.zeros(B, dtype=torch.int32, device="cuda")
+        self.bt = torch.full((L, H, B, mp), -1, dtype=torch.int32, device="cuda")
+        self.sl = torch.zeros(L, H, B, dtype=torch.int32, device="cuda")
+        self.steps = 0
+
+    def step(self):
+        L, H, B = self.shape
+        self.steps += 1
+        x = torch.full((L, H, B, self.d), float(self.steps), device="cuda").to(torch.bfloat16)
+        self.C.kvs_decode_step(self.dm, B, 0, self.pos, torch.zeros(L, H, B, device="cuda"), x, x, None, None, None,
+                               -1.0, self.ps, self.kp, self.vp, self.cap, self.nxt, self.bt, self.mp, self.sl)
+        torch.cuda.synchronize()
+        return self.C.kvs_device_error()
+
+    def tokens(self, r):
+        n = int(self.sl[r])
+        return self.kp[self.bt[r][: -(-n // self.ps)].long()].reshape(-1, self.d)[:n, 0].int().tolist()
+
+    def reclaim(self, nxt_out=None, bt_out=None):
+        ws = bytes_of(self.C.kvs_reclaim_paged_workspace_size(self.dm, self.shape[2], self.cap))
+        self.C.kvs_reclaim_paged(self.dm, self.shape[2], self.ps, self.kp, self.vp, self.cap, self.nxt,
+                                 self.nxt if nxt_out is None else nxt_out, self.bt,
+                                 self.bt if bt_out is None else bt_out, self.mp, self.sl, ws, ws.numel())
+        torch.cuda.synchronize()
+        return self.C.kvs_device_error()
+
+
+def test_pages_come_back_after_a_decode_step_filled_the_pool(C):
+    """Four rows, five pages: a step that asks for more leaves the counter at the pool's end, and
+    with a sequence ended its pages serve the other."""
+    s = Decode(C, 1, 2, 2, ps=4, cap=5)
+    codes = [s.step() for _ in range(7)]
+    assert codes == [0] * 4 + [4] * 3  # step 5 asks for four pages and gets one
+    assert int(s.nxt) == 5
+    assert sorted(s.sl.flatten().tolist()) == [4, 4, 4, 7]
+    before = [s.tokens((0, h, 0)) for h in range(2)]
+    s.sl[:, :, 1] = 0
+    for _ in range(2):  # a second call finds nothing to do
+        assert s.reclaim() == 0
+        assert int(s.nxt) == sum(-(-len(x) // 4) for x in before)
+        assert [s.tokens((0, h, 0)) for h in range(2)] == before
+    assert s.step() in (0, 4)  # the ended sequence's rows ask for pages too
+    assert [s.tokens((0, h, 0))[:len(x)] for h, x in enumerate(before)] == before
+    assert int(s.nxt) <= 5
+
+
+@pytest.mark.parametrize("cap", [1, 700, 1023, 1024, 2500])
+def test_a_full_pool_keeps_its_counter(C, cap):
+    """1024 rows ask at once, and again."""
+    s = Decode(C, 4, 8, 32, ps=1, cap=cap)
+    for asked in (1024, 2048, 3072):
+        assert s.step() == (4 if asked > cap else 0)
+        assert int(s.nxt) == min(asked, cap)
+    pages = torch.cat([s.bt[r][: int(s.sl[r])] for r in np.ndindex(4, 8, 32)]).tolist()
+    assert sorted(pages) == list(range(cap))
