@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(
 
 constexpr int kReclaimThreads = 256;
 constexpr int kMaxChunks = 8192;  // of the bits of a pool, counted in every block
+constexpr int kReclaimSmem = (2 * kMaxChunks + 1) * sizeof(int);  // their counts and bits at most
 
 // A bit per page that some row names, in chunks of 2^bits pages (at most kMaxChunks of them),
 // behind the head.
@@ -589,9 +590,14 @@ cudaError_t launch_reclaim(const PagedArgs& p, const ReclaimArgs& a, cudaStream_
   const int rows = p.L * p.Hkv * p.B, bits = chunk_bits(p.capacity);
   const size_t quads = reclaim_workspace_bytes(p.capacity) / 16;
   const int clear = (int)((quads + kReclaimThreads - 1) / kReclaimThreads);
+  // the same limit whatever this call needs, since another thread may launch for another pool, and
+  // before anything is enqueued
+  cudaError_t e = cudaFuncSetAttribute(reclaim_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kReclaimSmem);
+  if (e != cudaSuccess) return e;
   count_launches(3);
   Launch c(dim3(clear < 152 ? clear : 152), kReclaimThreads, s);
-  cudaError_t e = cudaLaunchKernelEx(&c.cfg, reclaim_clear_kernel, p, a, bits);
+  e = cudaLaunchKernelEx(&c.cfg, reclaim_clear_kernel, p, a, bits);
   if (e != cudaSuccess) return e;
   const int mark = (rows + kReclaimThreads / 32 - 1) / (kReclaimThreads / 32);
   Launch m(dim3(mark < 152 * 8 ? mark : 152 * 8), kReclaimThreads, s);
@@ -600,11 +606,6 @@ cudaError_t launch_reclaim(const PagedArgs& p, const ReclaimArgs& a, cudaStream_
   Launch r(dim3(152 * 2), kReclaimThreads, s);
   const int chunks = ((p.capacity - 1) >> bits) + 1;
   r.cfg.dynamicSmemBytes = (chunks + 1 + (bits == 5 ? chunks : 0)) * sizeof(int);
-  if (r.cfg.dynamicSmemBytes > 48 * 1024) {
-    e = cudaFuncSetAttribute(reclaim_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)r.cfg.dynamicSmemBytes);
-    if (e != cudaSuccess) return e;
-  }
   return cudaLaunchKernelEx(&r.cfg, reclaim_kernel, p, a, rows, bits);
 }
 

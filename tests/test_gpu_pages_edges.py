@@ -1,4 +1,7 @@
-"""Edges of the calls that move pages: pools that a decode step has filled."""
+"""Edges of the calls that move pages: pools that a decode step has filled, and pools of different
+sizes from two host threads."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -90,3 +93,52 @@ def test_a_full_pool_keeps_its_counter(C, cap):
         assert int(s.nxt) == min(asked, cap)
     pages = torch.cat([s.bt[r][: int(s.sl[r])] for r in np.ndindex(4, 8, 32)]).tolist()
     assert sorted(pages) == list(range(cap))
+
+
+# ----------------------------------------------------------------------------- sizes
+
+def test_two_threads_reclaim_pools_of_different_sizes(C):
+    """Calls that need more than 48 KB of shared memory a block, 50 KB and 62, at once."""
+    dm = C.dims(1, 1, 1, 64)
+
+    class Pool:
+        def __init__(self, cap, seed):
+            self.cap, self.B = cap, 64
+            self.kp = torch.zeros(cap, 1, 64, dtype=torch.bfloat16, device="cuda")
+            self.vp = torch.zeros_like(self.kp)
+            gen = torch.Generator().manual_seed(seed)
+            self.bt0 = torch.randperm(cap, generator=gen)[: self.B].int().view(1, 1, self.B, 1).cuda()
+            self.bt = self.bt0.clone()
+            self.nxt, self.out, self.sl = i32([cap]), i32([-7]), torch.ones(1, 1, self.B, dtype=torch.int32, device="cuda")
+            self.ws = bytes_of(C.kvs_reclaim_paged_workspace_size(dm, self.B, cap))
+            self.stream = torch.cuda.Stream()
+            self.raised = []
+
+        def go(self):
+            C.kvs_reclaim_paged(dm, self.B, 1, self.kp, self.vp, self.cap, self.nxt, self.out, self.bt0, self.bt, 1,
+                                self.sl, self.ws, self.ws.numel(), stream=self.stream)
+
+        def work(self):
+            for i in range(3000):
+                try:
+                    self.go()
+                except Exception as e:  # an exception of a thread fails no test by itself
+                    self.raised.append((i, e))
+                if i % 500 == 499:
+                    self.stream.synchronize()
+
+    pools = [Pool(200_000, 1), Pool(250_000, 2)]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=p.work) for p in pools]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not pools[0].raised and not pools[1].raised, [p.raised[:3] for p in pools]
+    assert C.kvs_device_error() == 0
+    for p in pools:
+        ids = p.bt0.flatten().tolist()
+        high, holes = sorted(x for x in ids if x >= p.B), [i for i in range(p.B) if i not in ids]
+        new = dict(zip(high, holes))
+        assert int(p.out) == p.B and p.bt.flatten().tolist() == [new.get(x, x) for x in ids]
