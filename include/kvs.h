@@ -491,7 +491,8 @@ kvs_status kvs_rope(const kvs_dims* dims, int32_t N, const int32_t* pos, int32_t
  *   k, v      [L][H_kv][N][d] bf16
  *   k_pages, v_pages [capacity_pages][page_size][d] bf16 state
  *   next_page, next_page_out [1] int32; may be the same (kvs_compact_paged leaves the
- *             count of used pages in needed_pages)
+ *             count of used pages in needed_pages); without sequences (B == 0) nothing else
+ *             is read or written
  *   block_table [L][H_kv][B][max_pages] int32 state
  *   seq_lens, seq_lens_out [L][H_kv][B] int32; may be the same
  *   ws        scratch of kvs_append_paged_workspace_size() bytes; calls that may overlap
@@ -641,7 +642,8 @@ kvs_status kvs_accept_paged(const kvs_dims* dims, int32_t B, int32_t N, const in
  *
  *   src, dst  [n_forks] int32, n_forks <= B <= 131072
  *   k_pages, v_pages [capacity_pages][page_size][d] bf16 state
- *   next_page, next_page_out [1] int32; may be the same
+ *   next_page, next_page_out [1] int32; may be the same; without forks nothing else is read or
+ *             written
  *   block_table [L][H_kv][B][max_pages] int32 state;  seq_lens [L][H_kv][B] int32 state
  *   pos [B] int32 state;  ring_score [L][H_kv][B][w] fp32 state;  ring_k, ring_v
  *             [L][H_kv][B][w][d] bf16 state (not used with w == 0)
@@ -676,7 +678,8 @@ kvs_status kvs_fork_paged(const kvs_dims* dims, int32_t B, int32_t n_forks, cons
  * All rows that use the pool are in one call.
  *
  *   k_pages, v_pages [capacity_pages][page_size][d] bf16 state
- *   next_page, next_page_out [1] int32; may be the same
+ *   next_page, next_page_out [1] int32; may be the same; without sequences (B == 0) nothing is
+ *             counted: next_page_out equals next_page, and nothing else is read or written
  *   block_table, block_table_out [L][H_kv][B][max_pages] int32; may be the same
  *   seq_lens  [L][H_kv][B] int32
  *   ws        scratch of kvs_reclaim_paged_workspace_size() bytes; calls that may overlap on

@@ -87,6 +87,13 @@ kvs_status check_dims(const kvs_dims* dm, const char* fn, bool need_heads = true
 
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
+// A call that takes no pages: the counter goes on as it is, also to one apart from it.
+kvs_status hand_on(const int32_t* next_page, int32_t* next_page_out, void* stream, const char* fn) {
+  if (!next_page || !next_page_out || next_page == next_page_out) return ok();
+  return cuda_status(cudaMemcpyAsync(next_page_out, next_page, sizeof(int32_t),
+                                     cudaMemcpyDeviceToDevice, as_stream(stream)), fn);
+}
+
 }  // namespace
 
 extern "C" {
@@ -738,7 +745,7 @@ kvs_status kvs_append_paged(const kvs_dims* dims, int32_t B, int32_t N, const in
           "kvs_append_paged: too many rows");
   REQUIRE((int64_t)dims->L * ((int64_t)dims->H_q + 2 * dims->H_kv) < INT32_MAX,
           KVS_ERR_UNSUPPORTED, "kvs_append_paged: too many heads");
-  if (B == 0) return ok();
+  if (B == 0) return hand_on(next_page, next_page_out, stream, __func__);
   REQUIRE_OPT_PTR(tok_start);
   const size_t row = (size_t)dims->L * N * dims->d * sizeof(kvs_bf16);
   const size_t rows = (size_t)dims->L * dims->H_kv * B;
@@ -964,7 +971,7 @@ kvs_status kvs_fork_paged(const kvs_dims* dims, int32_t B, int32_t n_forks, cons
   REQUIRE(B <= kvs::kMaxForkBatch, KVS_ERR_UNSUPPORTED, "kvs_fork_paged: B = %d (at most %d)", B,
           kvs::kMaxForkBatch);
   REQUIRE(n_forks <= B, KVS_ERR_SHAPE, "kvs_fork_paged: n_forks = %d above B = %d", n_forks, B);
-  if (n_forks == 0) return ok();
+  if (n_forks == 0) return hand_on(next_page, next_page_out, stream, __func__);
   REQUIRE_PTR(src);
   REQUIRE_PTR(dst);
   REQUIRE_PTR(next_page);
@@ -1006,7 +1013,7 @@ kvs_status kvs_reclaim_paged(const kvs_dims* dims, int32_t B, int32_t page_size,
   st = check_paged(__func__, dims, B, page_size, k_pages, v_pages, capacity_pages, block_table,
                    max_pages, seq_lens, &p);
   if (st) return st;
-  if (B == 0) return ok();
+  if (B == 0) return hand_on(next_page, next_page_out, stream, __func__);
   REQUIRE_PTR(next_page);
   REQUIRE_PTR(next_page_out);
   REQUIRE_PTR(block_table_out);

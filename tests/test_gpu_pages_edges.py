@@ -1,5 +1,5 @@
-"""Edges of the calls that move pages: pools that a decode step has filled, and pools of different
-sizes from two host threads."""
+"""Edges of the calls that move pages: pools that a decode step has filled, counters apart from
+their inputs in calls that move nothing, and pools of different sizes from two host threads."""
 import threading
 
 import numpy as np
@@ -93,6 +93,55 @@ def test_a_full_pool_keeps_its_counter(C, cap):
         assert int(s.nxt) == min(asked, cap)
     pages = torch.cat([s.bt[r][: int(s.sl[r])] for r in np.ndindex(4, 8, 32)]).tolist()
     assert sorted(pages) == list(range(cap))
+
+
+# ----------------------------------------------------------------------------- counters
+
+def fork(C, forks, nxt, out, B=2, cap=6, sl=(8, 4), L=1):
+    """Forks of sequence 0 to sequence 1, pages of four tokens."""
+    dm = C.dims(L, 1, 1, 64)
+    kp = torch.zeros(cap, 4, 64, dtype=torch.bfloat16, device="cuda")
+    bt, lens = i32([0, 1, -1, 2, -1, -1]), i32(list(sl))
+    ws = bytes_of(C.kvs_fork_paged_workspace_size(dm, 2, max(forks, 1)))
+    C.kvs_fork_paged(dm, B, forks, i32([0]), i32([1]), 4, kp, kp.clone(), cap, nxt, out, bt, 3, lens, 0, None, None,
+                     None, None, ws, ws.numel())
+    torch.cuda.synchronize()
+    return C.kvs_device_error(), bt.tolist(), lens.tolist()
+
+
+def test_calls_that_move_nothing_hand_the_counter_on(C):
+    """Separate counters alternate from call to call: one that is skipped would hand out pages that
+    are in use."""
+    for B, forks in ((2, 0), (0, 0)):
+        nxt, out = i32([3]), i32([-7])
+        assert fork(C, forks, nxt, out, B=B) == (0, [0, 1, -1, 2, -1, -1], [8, 4])
+        assert int(out) == 3 and int(nxt) == 3
+        assert fork(C, forks, nxt, nxt, B=B)[0] == 0 and int(nxt) == 3  # in place
+    # a batch of no sequences: nothing is counted
+    dm = C.dims(1, 1, 1, 64)
+    nxt, out, ws, x = i32([3]), i32([-7]), bytes_of(1 << 16), torch.zeros(4096, dtype=torch.bfloat16, device="cuda")
+    C.kvs_reclaim_paged(dm, 0, 4, x, x, 6, nxt, out, i32([]), i32([]), 3, i32([]), ws, ws.numel())
+    assert int(out) == 3
+    nxt, out = i32([4]), i32([-7])
+    C.kvs_append_paged(dm, 0, 0, None, None, 0, None, False, None, None, x, x, 4, x, x, 6, nxt, out, i32([]), 3, i32([]),
+                       i32([]), ws, ws.numel())
+    assert int(out) == 4
+    torch.cuda.synchronize()
+    assert C.kvs_device_error() == 0
+
+
+def test_a_counter_handed_on_in_a_graph(C):
+    nxt, out = i32([3]), i32([-7])
+    graph = torch.cuda.CUDAGraph()
+    dm = C.dims(1, 1, 1, 64)
+    kp, bt, lens = torch.zeros(6, 4, 64, dtype=torch.bfloat16, device="cuda"), i32([0, 1, 2]), i32([4])
+    with torch.cuda.graph(graph):
+        C.kvs_fork_paged(dm, 1, 0, None, None, 4, kp, kp, 6, nxt, out, bt, 3, lens, 0, None, None, None, None, None, 0)
+    assert int(out) == -7
+    for v in (5, 0):
+        nxt.fill_(v)
+        graph.replay()
+        assert int(out) == v
 
 
 # ----------------------------------------------------------------------------- sizes
