@@ -635,10 +635,11 @@ kvs_status kvs_accept_paged(const kvs_dims* dims, int32_t B, int32_t N, const in
  * and pos are copied too.  What dst[i] held before is dropped; its pages come free with
  * kvs_reclaim_paged.  A source's rows may not be cut back (a draft taken back) below the length
  * at which they were forked, since what follows would be written into shared pages.
- * All or nothing: if the pool is too small (error word 4), or a sequence number, length or the
- * counter is out of range, a target is named twice or is a source (11), nothing is written but
- * next_page_out, which equals next_page.  A bad id of the page to be copied counts as a page of
- * zeros and sets the error word (11); other ids are copied as they are.
+ * All or nothing: if the pool is too small for the new pages (error word 4), or a sequence number
+ * or length is out of range, the counter is not in [0, capacity_pages], or a target is named twice
+ * or is a source (11), nothing is written but next_page_out, which equals next_page.  A bad id of
+ * the page to be copied counts as a page of zeros and sets the error word (11); other ids are
+ * copied as they are.
  *
  *   src, dst  [n_forks] int32, n_forks <= B <= 131072
  *   k_pages, v_pages [capacity_pages][page_size][d] bf16 state
@@ -672,9 +673,10 @@ kvs_status kvs_fork_paged(const kvs_dims* dims, int32_t B, int32_t n_forks, cons
  *
  * Pages that do not move and the old places of those that do keep what they hold, so with
  * block_table_out and next_page_out apart from their inputs the state before the call stays
- * good until pages are next taken.  All or nothing: if the counter, a length or the id of a page
- * in use is out of range (ids of pages in use lie below next_page), nothing moves,
- * block_table_out and next_page_out equal their inputs, and the device error word is set (11).
+ * good until pages are next taken.  All or nothing: if the counter is not in [0, capacity_pages],
+ * or a length or the id of a page in use is out of range (ids of pages in use lie below next_page),
+ * nothing moves, block_table_out and next_page_out equal their inputs, and the device error word is
+ * set (11).
  * All rows that use the pool are in one call.
  *
  *   k_pages, v_pages [capacity_pages][page_size][d] bf16 state

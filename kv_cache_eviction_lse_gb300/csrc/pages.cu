@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(
   }
   base[tid] = next + before + incl - mine.pages;
   __syncthreads();
-  if (!code && total > 0 && (long long)next + total > p.capacity) code = kErrPoolFull;
+  if (!code && (long long)next + total > p.capacity) code = total > 0 ? kErrPoolFull : kErrPages;
   if (blockIdx.x == 0 && tid == 0) {
     a.next_page_out[0] = next + (code ? 0 : total);
     if (code) fault(code);

@@ -1,5 +1,6 @@
 """Edges of the calls that move pages: pools that a decode step has filled, counters apart from
-their inputs in calls that move nothing, and pools of different sizes from two host threads."""
+their inputs in calls that move nothing, counters out of range, and pools of different sizes from
+two host threads."""
 import threading
 
 import numpy as np
@@ -141,6 +142,21 @@ def test_a_counter_handed_on_in_a_graph(C):
     for v in (5, 0):
         nxt.fill_(v)
         graph.replay()
+        assert int(out) == v
+
+
+def test_fork_refuses_a_counter_above_the_capacity(C):
+    """Also where no page is needed (the source's rows end with a page); at the capacity it goes on."""
+    for v in (7, 2 ** 31 - 1, -1):
+        nxt, out = i32([v]), i32([-7])
+        assert fork(C, 1, nxt, out) == (11, [0, 1, -1, 2, -1, -1], [8, 4])
+        assert int(out) == v
+    nxt, out = i32([6]), i32([-7])
+    assert fork(C, 1, nxt, out) == (0, [0, 1, -1, 0, 1, -1], [8, 8])
+    assert int(out) == 6
+    for v in (6, 7, 2 ** 31 - 1):  # too small a pool where one is
+        nxt, out = i32([v]), i32([-7])
+        assert fork(C, 1, nxt, out, sl=(7, 4)) == (4, [0, 1, -1, 2, -1, -1], [7, 4])
         assert int(out) == v
 
 
