@@ -1,6 +1,6 @@
 """Edges of the calls that move pages: pools that a decode step has filled, counters apart from
-their inputs in calls that move nothing, counters out of range, and pools of different sizes from
-two host threads."""
+their inputs in calls that move nothing, counters out of range, pools of different sizes from two
+host threads, and the pool of a whole model."""
 import threading
 
 import numpy as np
@@ -161,6 +161,64 @@ def test_fork_refuses_a_counter_above_the_capacity(C):
 
 
 # ----------------------------------------------------------------------------- sizes
+
+def model_case(L, H, B, most, ps, d, gone, seed, spare=1000):
+    """Rows of up to `most` tokens, scattered pages of which each holds its id; some sequences end."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    rows = L * H * B
+    n = torch.randint(0, most + 1, (rows,), generator=gen, device="cuda")
+    need = (n + ps - 1) // ps
+    total = int(need.sum()) + spare
+    mp = int(need.max())
+    ids = torch.randperm(total, generator=gen, device="cuda").int()
+    bt = torch.full((rows, mp), -1, dtype=torch.int32, device="cuda")
+    used = torch.arange(mp, device="cuda") < need[:, None]
+    bt[used] = ids[: int(need.sum())]
+    n = (n.view(L * H, B) * (torch.rand(B, generator=gen, device="cuda") >= gone)).view(-1)
+    bt.view(L * H, B, mp)[:, 0] = bt.view(L * H, B, mp)[:, 1]  # two sequences share their pages
+    n.view(L * H, B)[:, 0] = n.view(L * H, B)[:, 1]
+    kp = torch.zeros(total, ps, d, dtype=torch.int16, device="cuda")
+    kp[:, 0, :2] = torch.arange(total, dtype=torch.int32, device="cuda").view(torch.int16).view(-1, 2)
+    kp[:, -1, -2:] = kp[:, 0, :2]
+    return dict(L=L, H=H, B=B, ps=ps, d=d, mp=mp, cap=total, n=n.int(), bt=bt, kp=kp.view(torch.bfloat16))
+
+
+def expected_reclaim(c):
+    """The new table, where each page goes, and their number, from the definition."""
+    need = (c["n"].long() + c["ps"] - 1) // c["ps"]
+    used = torch.arange(c["mp"], device="cuda") < need[:, None]
+    live = torch.zeros(c["cap"], dtype=torch.bool, device="cuda")
+    live[c["bt"][used].long()] = True
+    count = int(live.sum())
+    at = torch.arange(c["cap"], device="cuda")
+    new = at.clone()
+    new[live & (at >= count)] = at[~live & (at < count)]
+    bt = torch.full_like(c["bt"], -1)
+    bt[used] = new[c["bt"][used].long()].int()
+    return bt, live, new, count
+
+
+@pytest.mark.parametrize("gone", [0.0, 0.3, 1.0])
+@pytest.mark.parametrize("L, H, B, most, ps, spare", [
+    (3, 8, 16, 1200, 1, 7),       # 230 thousand pages: a word a chunk, in shared memory
+    (4, 8, 64, 3000, 1, 1000),    # 3 million: several words a chunk
+    (36, 8, 24, 3000, 4, 50000),  # 2.6 million in rows of a whole model
+])
+def test_reclaim_of_a_models_pool(C, L, H, B, most, ps, spare, gone):
+    c = model_case(L, H, B, most, ps, 64, gone, seed=B, spare=spare)
+    bt, live, new, count = expected_reclaim(c)
+    dm = C.dims(L, H, H, 64)
+    ws = bytes_of(C.kvs_reclaim_paged_workspace_size(dm, B, c["cap"]))
+    kp, vp = c["kp"].clone(), c["kp"].clone()
+    nxt, out, bt_out = i32([c["cap"]]), i32([-7]), torch.full_like(c["bt"], -7)
+    C.kvs_reclaim_paged(dm, B, ps, kp, vp, c["cap"], nxt, out, c["bt"], bt_out, c["mp"], c["n"], ws, ws.numel())
+    torch.cuda.synchronize()
+    assert C.kvs_device_error() == 0
+    assert int(out) == count and torch.equal(bt_out, bt)
+    want = c["kp"].view(torch.int16).clone()  # what moves, and all else as it was
+    want[new[live]] = c["kp"].view(torch.int16)[live]
+    assert torch.equal(kp.view(torch.int16), want) and torch.equal(vp.view(torch.int16), want)
+
 
 def test_two_threads_reclaim_pools_of_different_sizes(C):
     """Calls that need more than 48 KB of shared memory a block, 50 KB and 62, at once."""
