@@ -319,8 +319,8 @@ kvs_status kvs_surrogate(const kvs_dims* dims, const kvs_bf16* h, int32_t T, con
           dims->H_kv);
   REQUIRE(dims->D_h > 0 && dims->D_h % 128 == 0, KVS_ERR_UNSUPPORTED,
           "kvs_surrogate: D_h = %d must be a positive multiple of 128", dims->D_h);
-  REQUIRE(kvs::surrogate_smem_bytes(dims->D_h, dims->H_kv) <= 200 * 1024, KVS_ERR_UNSUPPORTED,
-          "kvs_surrogate: D_h * ceil(H_kv/8) = %d above 12800",
+  REQUIRE(kvs::surrogate_smem_bytes(dims->D_h, dims->H_kv) <= kvs::kSurrogateMaxSmem,
+          KVS_ERR_UNSUPPORTED, "kvs_surrogate: D_h * ceil(H_kv/8) = %d above 12800",
           dims->D_h * ((dims->H_kv + 7) / 8));
   if (T == 0) return ok();
   REQUIRE_PTR(h);

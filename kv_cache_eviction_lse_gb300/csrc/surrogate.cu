@@ -328,13 +328,20 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kWarps * 32)
 }  // namespace
 
 size_t surrogate_smem_bytes(int Dh, int Hkv) { return (size_t)Dh * ((Hkv + 7) / 8) * 16; }
+static_assert(kSurrogateMaxSmem + kWarps * 2 * 4 * 32 * sizeof(float) <= 232448, "of a block");
 
 cudaError_t launch_surrogate(const bf16_t* h, int L, int T, int Dh, int Hkv, const bf16_t* W,
                              const float* b, float* z, float tau, int w, uint8_t* mask,
                              int* keep, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
+  // the same limit whatever this call needs: another thread may launch for another hidden size
+  const auto kernel = Hkv <= 8 ? surrogate_kernel<1> : surrogate_kernel<2>;
+  const int split_smem = kWarps * ((Hkv + 7) / 8) * 4 * 32 * (int)sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSurrogateMaxSmem + split_smem);
+  if (e != cudaSuccess) return e;
   if (mask) {
-    cudaError_t e = cudaMemsetAsync(keep, 0, sizeof(int) * (size_t)L * Hkv, s);
+    e = cudaMemsetAsync(keep, 0, sizeof(int) * (size_t)L * Hkv, s);
     if (e != cudaSuccess) return e;
   }
   SurArgs a{h, W, b, z, mask, keep, T, Dh, Hkv, w, 8, tau, 1};
@@ -357,15 +364,9 @@ cudaError_t launch_surrogate(const bf16_t* h, int L, int T, int Dh, int Hkv, con
   dim3 grid(a.ksplit > 1 ? ntile : (ntile + kWarps * a.tiles_per_warp - 1) /
                                         (kWarps * a.tiles_per_warp), L);
   size_t smem = surrogate_smem_bytes(Dh, Hkv);
-  if (a.ksplit > 1) smem += (size_t)kWarps * ((Hkv + 7) / 8) * 4 * 32 * sizeof(float);
+  if (a.ksplit > 1) smem += split_smem;
   count_launches(1);
-  if (Hkv <= 8) {
-    cudaFuncSetAttribute(surrogate_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    surrogate_kernel<1><<<grid, kWarps * 32, smem, s>>>(a);
-  } else {
-    cudaFuncSetAttribute(surrogate_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    surrogate_kernel<2><<<grid, kWarps * 32, smem, s>>>(a);
-  }
+  kernel<<<grid, kWarps * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -6,6 +6,7 @@
 
 namespace kvs {
 
+constexpr int kSurrogateMaxSmem = 200 * 1024;  // of a block's weights
 size_t surrogate_smem_bytes(int Dh, int Hkv);
 
 cudaError_t launch_surrogate(const bf16_t* h, int L, int T, int Dh, int Hkv, const bf16_t* W,
