@@ -342,6 +342,11 @@ __host__ __device__ inline int chunk_bits(int capacity) {
 __device__ __forceinline__ uint32_t* live_words(void* ws) {
   return reinterpret_cast<uint32_t*>(static_cast<ReclaimHead*>(ws) + 1);
 }
+// The pages that can be in use; the bound holds even if another stream writes the workspace
+// meanwhile.
+__device__ __forceinline__ int pages_of(const ReclaimHead& head, int capacity) {
+  return max(0, min(head.pages, capacity));
+}
 __device__ __forceinline__ int chunks_of(int pages, int bits) {
   return (int)(((long long)pages + (1 << bits) - 1) >> bits);
 }
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(kReclaimThreads) reclaim_mark_kernel(
   const int lane = threadIdx.x & 31, warps = gridDim.x * (kReclaimThreads / 32);
   wait_for_previous();
   let_next_start();
-  const int pages = static_cast<const ReclaimHead*>(a.ws)->pages;
+  const int pages = pages_of(*static_cast<const ReclaimHead*>(a.ws), p.capacity);
   uint32_t* live = live_words(a.ws);
   bool bad = false;
   for (int row = blockIdx.x * (kReclaimThreads / 32) + (threadIdx.x >> 5); row < rows; row += warps) {
@@ -432,7 +437,7 @@ __global__ void __launch_bounds__(kReclaimThreads) reclaim_kernel(
   const int gw = blockIdx.x * kWarps + warp, warps = gridDim.x * kWarps;
   wait_for_previous();
   const ReclaimHead head = *static_cast<const ReclaimHead*>(a.ws);
-  const int pages = head.pages, chunks = chunks_of(pages, bits), code = head.code;
+  const int pages = pages_of(head, p.capacity), chunks = chunks_of(pages, bits), code = head.code;
   const uint32_t* words = live_words(a.ws);
   if (code) {  // everything as it was
     if (blockIdx.x == 0 && tid == 0) {
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(kReclaimThreads) reclaim_kernel(
     for (int i = 0; i < count; ++i) {
       const int from = __shfl_sync(0xffffffffu, from_of, i), to = __shfl_sync(0xffffffffu, to_of, i);
       const int first = __shfl_sync(0xffffffffu, part_of, i) * 256 + lane;
-      if (from < n_live || from >= pages || (uint32_t)to >= (uint32_t)n_live) continue;
+      if (from < n_live || from >= pages || (uint32_t)to >= (uint32_t)min(n_live, pages)) continue;
       const size_t src_at = (size_t)from * chunks16, dst_at = (size_t)to * chunks16;
       uint4 x[8], y[8];
 #pragma unroll

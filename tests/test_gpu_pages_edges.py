@@ -265,3 +265,48 @@ def test_two_threads_reclaim_pools_of_different_sizes(C):
         high, holes = sorted(x for x in ids if x >= p.B), [i for i in range(p.B) if i not in ids]
         new = dict(zip(high, holes))
         assert int(p.out) == p.B and p.bt.flatten().tolist() == [new.get(x, x) for x in ids]
+
+
+def test_graphs_that_share_a_workspace(C):
+    """Forks and reclaims of two caches of different sizes in graphs with one workspace, replayed in
+    turn on one stream, give what calls with workspaces of their own give."""
+    dm = [C.dims(2, 3, 3, 64), C.dims(5, 2, 2, 64)]
+    cs = [model_case(2, 3, 9, 60, 4, 64, 0.3, seed=1), model_case(5, 2, 40, 90, 1, 64, 0.0, seed=2)]
+    room = 3000  # pages behind the counter, for the forks
+
+    def tensors(c):
+        pad = torch.zeros(room, c["ps"], c["d"], dtype=torch.bfloat16, device="cuda")
+        kp = torch.cat([c["kp"], pad])
+        return dict(kp=kp, vp=kp.clone(), bt=c["bt"].clone(), sl=c["n"].clone(), nxt=i32([c["cap"]]))
+
+    def step(i, t, ws):
+        c = cs[i]
+        C.kvs_fork_paged(dm[i], c["B"], 2, src, dst, c["ps"], t["kp"], t["vp"], c["cap"] + room, t["nxt"], t["nxt"],
+                         t["bt"], c["mp"], t["sl"], 0, None, None, None, None, ws, ws.numel())
+        C.kvs_reclaim_paged(dm[i], c["B"], c["ps"], t["kp"], t["vp"], c["cap"] + room, t["nxt"], t["nxt"], t["bt"],
+                            t["bt"], c["mp"], t["sl"], ws, ws.numel())
+
+    src, dst = i32([2, 3]), i32([5, 7])
+    need = [max(C.kvs_fork_paged_workspace_size(d, c["B"], 2),
+                C.kvs_reclaim_paged_workspace_size(d, c["B"], c["cap"] + room)) for d, c in zip(dm, cs)]
+    want = [tensors(c) for c in cs]
+    for i, t in enumerate(want):
+        step(i, t, bytes_of(need[i]))
+    ws, first, got, graphs = bytes_of(max(need)), [tensors(c) for c in cs], [tensors(c) for c in cs], []
+    for i, t in enumerate(got):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(i, t, ws)
+        graphs.append(g)
+    for _ in range(3):
+        for t, f in zip(got, first):
+            for k in t:
+                t[k].copy_(f[k])
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert C.kvs_device_error() == 0
+        for t, w in zip(got, want):
+            for k in t:
+                x, y = (v.view(torch.int16) if v.dtype == torch.bfloat16 else v for v in (t[k], w[k]))
+                assert torch.equal(x, y), k
