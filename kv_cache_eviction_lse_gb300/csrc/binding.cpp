@@ -1,11 +1,13 @@
 // The Python side of the calls that a decode loop makes for every token: kvs_rope,
 // kvs_append_paged and kvs_attn_decode, and around drafted tokens kvs_attn_tree,
-// kvs_accept_paged, kvs_fork_paged and kvs_reclaim_paged.  Their kernels take 2 to 10 us for a token of a batch,
-// and up to 25 arguments checked and converted in Python took longer: calls back to back are
-// one per 6.8 us (rotation of 64 tokens), 13.2 (their append) and 8.7 (attention of a short
-// sequence) that way, and 2.9, 5.0 and 5.9 through this file, launches included.  Arguments
-// are those of the C functions; a tensor is checked for its type, size, device and layout, an
-// int is taken as an address and None as NULL.
+// kvs_accept_paged, kvs_fork_paged and kvs_reclaim_paged.  The kernels of the first three take 2 to
+// 10 us for a token of a batch, and up to 25 arguments checked and converted in Python took longer:
+// calls back to back are one per 6.8 us (rotation of 64 tokens), 13.2 (their append) and 8.7
+// (attention of a short sequence) that way, and 2.9, 5.0 and 5.9 through this file, launches
+// included.  The drafting calls take 3 to 15 us on small batches (accepted paths 3, forks 7,
+// reclaimed pages 10, a short tree 12) and come the same way.  Arguments are those of the C
+// functions; a tensor is checked for its type, size, device and layout, an int is taken as an
+// address and None as NULL.
 #define PY_SSIZE_T_CLEAN
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>

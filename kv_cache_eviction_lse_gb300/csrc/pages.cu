@@ -5,8 +5,11 @@
 //
 // Bound by latency (a chain of dependent loads: lengths -> table -> rows) until thousands of
 // rows move at once, then by HBM.  Measured, a call in a graph (floor): paths of four users' drafts
-// over 36 layers 2.6 us (0.4), of 64 users 14.8 (6.9); 3 forks of one sequence 7.0 (0.2), 31 forks
-// with rings 42 (42); pages given back with few to move 9.7 (0.6), with a third gone 28.5 (15.8).
+// over 36 layers 2.6 to 2.9 us (0.4), of 64 users 15 (6.9); 3 forks of one sequence 7.1 (0.2), 31
+// forks with rings 42 (42); pages given back with few to move 10 (0.6), with a third gone 29 (15.8).
+// The pool of a whole model, 3.5 million pages of 16 tokens at d = 64, 36 layers x 8 heads x 24
+// sequences: 830 us with 160 thousand pages to move (200), 1740 with a third gone (1007); every
+// block counts all bits and a rank walks words one by one there.
 #include "common.cuh"
 #include "launch.cuh"
 #include "pages.cuh"
